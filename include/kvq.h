@@ -58,7 +58,8 @@ typedef enum kvq_status {
   KVQ_ERR_DEVICE_BOUNDS = 5,       /* device: slot / block-table entry outside [0, num_pages*16)       */
   KVQ_ERR_NONFINITE_INPUT = 6,     /* device: non-finite key/value, or a scale that overflows fp16     */
   KVQ_ERR_RANGE = 7,               /* device: a value scale above KVQ_MAX_VALUE_SCALE (see kvq_append) */
-  KVQ_ERR_TIMEOUT = 8              /* device: a bounded wait for an asynchronous copy gave up          */
+  KVQ_ERR_TIMEOUT = 8,             /* device: a bounded wait for an asynchronous copy gave up          */
+  KVQ_ERR_NO_PAGES = 9             /* device: fewer free pages than the step needs (kvq_map_runs)      */
 } kvq_status;
 
 /* Storage formats of one plane ([C] table "Keys carry the cartridge quantization loss"; [W] Sec. 4.2). */
@@ -67,10 +68,14 @@ typedef enum kvq_fmt {
   KVQ_FMT_E4M3 = 1,        /* FP8 E4M3 raw cast, round-to-nearest-even, saturating at +-448; no scale     */
   KVQ_FMT_E4M3_SCALED = 2, /* FP8 E4M3 of x / s, s = fp16(amax / 448) per (token, kv head)               */
   KVQ_FMT_INT8_DITHER = 3, /* subtractively dithered INT8: code = rint(x/s + xi), s = fp16(amax / 126.5) */
-  KVQ_FMT_INT8_DITHER_G32 = 4 /* the same with one scale per token per group of 32 channels: channels
+  KVQ_FMT_INT8_DITHER_G32 = 4, /* the same with one scale per token per group of 32 channels: channels
                                  32g..32g+31 use s_g = fp16(amax_g / 126.5) ([W] Sec. 6.2.3, Table 4,
                                  G_c = 32); keys and values of one cache both in this format, no prefix,
                                  no key outlier bypass */
+  /* Formats of the page-scaled family: kvq_append_runs and kvq_attn_runs only (no witness, no meter, no prefix;
+     kvq_append and kvq_decode_attn* refuse them).  Keys and values of one cache both in the same one. */
+  KVQ_FMT_E4M3_PAGE = 16,       /* FP8 E4M3 of x 2^-e, one power-of-two scale 2^e per (page, kv head)      */
+  KVQ_FMT_INT8_PAGE = 17        /* INT8 code = rint(x 2^-e) in -127..127, one scale 2^e per (page, kv head) */
 } kvq_fmt;
 
 /* Element type of the key / value / query inputs. */
@@ -114,7 +119,8 @@ typedef enum kvq_dtype { KVQ_DTYPE_F32 = 0, KVQ_DTYPE_BF16 = 1 } kvq_dtype;
  *     ([W] Sec. 6.2.5 fixed-channel outlier bypass: a fixed set of m RoPE pairs per
  *     (layer, kv head) is stored in fp16 (round to nearest even) and left out of the
  *     INT8 amax; the INT8 code of a bypassed channel is 0).  Head-major like the scales.
- * INT8 codes (both INT8 formats) are stored offset binary: the byte is code + 128
+ *   scale, page-scaled formats (2 B, fp16 bits): the page's scale (head-major like the others)
+ * INT8 codes (all INT8 formats) are stored offset binary: the byte is code + 128
  * (code 0 is 0x80), so that the decode turns a byte into an fp16 operand with one
  * byte permute.
  * Band b holds the RoPE frequency pairs 4b..4b+3 of the half-split pairing
@@ -417,6 +423,88 @@ kvq_status kvq_meter(const float* meter_state_dev, int32_t n_layers, int32_t bat
                      const kvq_meter_params* meter, float* meter_a_dev, float* raw_a_dev, float* cert_b_dev,
                      float* out_bound_dev, float* two_sided_dev, float* tanh_dev, int32_t* counts_dev,
                      int32_t* ranking_dev, kvq_stream_t stream);
+
+/*
+ * Runs.  The calls below work on one step of many requests at once: request s brings the *run* of rows
+ * run_starts[s] .. run_starts[s + 1] - 1 of the step's tensors (run_starts_dev: [batch + 1] int32, non-decreasing, in
+ * [0, num_rows]), which are the last tokens of its context of seq_lens[s] tokens: row i of the run is at position
+ * seq_lens[s] - n + i.  A run may be empty, one token (decode), a few (a draft) or many (a prompt or a chunk of it).
+ * run_starts_dev == NULL: every request brings one token (num_rows == batch, row s is request s).  Rows behind the
+ * last run are left as they are, so num_rows can be the fixed size of a captured step.  A run that cannot be (outside
+ * [0, num_rows], longer than max_run, a length outside [0, 16 max_pages_per_seq]) is reported as
+ * KVQ_ERR_DEVICE_BOUNDS and skipped.  batch <= KVQ_MAX_BATCH.  Two runs of one call must not overlap or share a page that
+ * either of them writes.
+ */
+
+/*
+ * kvq_map_runs -- a step's page bookkeeping on the device: finished requests hand their pages back, the others get the
+ * pages that their new tokens need, and every row its slot and position.
+ *
+ * new_lens_dev: [batch] int32, tokens that request s adds (0 allowed); negative: the request is finished, its pages go
+ *   back and its length becomes 0.  seq_lens_dev: [batch] lengths before the step.
+ * free_pages_dev: [free_capacity] int32 stack of free pages, entries 0 .. *free_count_dev - 1 in use.  Pages handed back
+ *   are pushed in order of request and page, then the pages needed are popped one by one in order of request and page.
+ * block_table_dev: [batch][max_pages_per_seq]; the entries of new pages are written, the others kept (those of a
+ *   finished request are stale from then on).
+ * run_starts_dev: [batch + 1] out, the exclusive sum of the new tokens.  seq_lens_out_dev [batch] and free_count_out_dev
+ *   [1]: the state after the step; they may be seq_lens_dev and free_count_dev themselves (in place, as a captured step
+ *   needs it) or other buffers.  No other two buffers may overlap.
+ * slot_mapping_dev, positions_dev (both nullable): [max_rows] int32; row r's slot (page 16 + offset, as kvq_append
+ *   takes it) and position; rows behind the last run get slot -1 (which kvq_append skips) and position 0.
+ * All or nothing: with too few pages (KVQ_ERR_NO_PAGES), more than max_rows tokens, a length outside
+ *   [0, 16 max_pages_per_seq] before or after, or a stack height outside [0, free_capacity] (KVQ_ERR_DEVICE_BOUNDS) nothing
+ *   is handed out or back: the state is copied, run_starts and positions are 0 and slots -1.
+ */
+kvq_status kvq_map_runs(const int32_t* new_lens_dev, const int32_t* seq_lens_dev, int32_t batch, int32_t* free_pages_dev,
+                        int32_t free_capacity, const int32_t* free_count_dev, int32_t* block_table_dev,
+                        int32_t max_pages_per_seq, int32_t* run_starts_dev, int32_t* seq_lens_out_dev,
+                        int32_t* free_count_out_dev, int32_t* slot_mapping_dev, int32_t* positions_dev, int32_t max_rows,
+                        int32_t* err_word_dev, kvq_stream_t stream);
+
+/*
+ * kvq_append_runs -- quantize the runs' keys and values into a page-scaled cache (KVQ_FMT_E4M3_PAGE, KVQ_FMT_INT8_PAGE).
+ *
+ * k_dev, v_dev: [num_rows] rows of [num_kv_heads][128] post-RoPE keys / values of type in_dtype, 16-byte aligned, rows
+ *   k_row_stride / v_row_stride elements apart (>= num_kv_heads * 128, a multiple of 16 bytes), so that slices of a fused
+ *   projection are taken as they are.
+ * seq_lens_dev: lengths that count the run's tokens already (as kvq_map_runs leaves them).
+ * Scale of a (page, kv head) and plane: 2^e, e the smallest exponent in [-24, 15] with amax <= qmax 2^e over the page's
+ *   tokens so far (qmax 448 for E4M3, 127 for INT8).  Codes: rne(x 2^-e), E4M3 or integer.  When a later token raises e
+ *   by d, the codes already in the page become rne(code 2^-d): exact for E4M3 down to its subnormals; for INT8 the errors
+ *   of all such steps sum to less than one step of the final scale.  The page's slots behind the run get code 0.
+ * A page that starts inside the run (or at its first token) is written whole, whatever it held before.
+ * Device errors: KVQ_ERR_DEVICE_BOUNDS (a page outside the cache, a run longer than its context: skipped),
+ *   KVQ_ERR_NONFINITE_INPUT (a NaN is stored as 0, an infinity as the largest code; neither counts in amax),
+ *   KVQ_ERR_RANGE (amax > qmax 2^15: the codes saturate).
+ */
+kvq_status kvq_append_runs(const kvq_cache* cache, const void* k_dev, int64_t k_row_stride, const void* v_dev,
+                           int64_t v_row_stride, int32_t in_dtype, const int32_t* run_starts_dev, int32_t batch,
+                           int32_t num_rows, const int32_t* block_table_dev, int32_t max_pages_per_seq,
+                           const int32_t* seq_lens_dev, int32_t* err_word_dev, kvq_stream_t stream);
+
+/* Workspace bytes kvq_attn_runs needs on the current device; max_run is the call's. */
+size_t kvq_attn_runs_workspace_size(int32_t batch, int32_t num_rows, int32_t max_run, int32_t num_kv_heads,
+                                    int32_t num_q_heads, int32_t q_dtype);
+
+/*
+ * kvq_attn_runs -- causal attention of the runs' queries over a page-scaled cache, one layer: the query at position p of
+ * its request attends to tokens 0 .. p (its own key and value are in the cache already).
+ *
+ * q_dev: [num_rows] rows of [num_q_heads][128] post-RoPE queries (q_dtype), 16-byte aligned, q_row_stride elements apart
+ *   (>= num_q_heads * 128, a multiple of 16 bytes); query head h reads kv head h / (num_q_heads / num_kv_heads).
+ * max_run: no run of the call is longer; it chooses the kernels and sizes the workspace.
+ * out_dev: [num_rows][num_q_heads][128] in the queries' type.  lse_dev (nullable): [num_rows][num_q_heads] fp32,
+ *   ln sum_t e^{x_t}.  A row that sees no token (an empty context) gives 0 and -inf.
+ * BF16 queries: the softmax weights are rounded to fp16 (11 bits) before the value product, everything else is exact or
+ *   binary32.  F32 queries: queries and weights are carried in two fp16 parts (22 bits).
+ * workspace_dev: at least kvq_attn_runs_workspace_size() bytes, 16-byte aligned; calls that can run at the same time
+ *   need one each.
+ */
+kvq_status kvq_attn_runs(const kvq_cache* cache, const void* q_dev, int64_t q_row_stride, int32_t q_dtype,
+                         int32_t num_q_heads, const int32_t* run_starts_dev, int32_t batch, int32_t num_rows,
+                         int32_t max_run, const int32_t* block_table_dev, int32_t max_pages_per_seq,
+                         const int32_t* seq_lens_dev, float sm_scale, void* out_dev, float* lse_dev, void* workspace_dev,
+                         size_t ws_bytes, int32_t* err_word_dev, kvq_stream_t stream);
 
 /* Test hook: the dither xi of (seed, layer, kv_head, slots[i], channel c) into xi_dev[i * 128 + c]. */
 kvq_status kvq_debug_dither(uint64_t seed, int32_t layer, int32_t kv_head, const int32_t* slots_dev, int32_t n,

@@ -28,6 +28,8 @@ meter      meter finalisation, coverage, per-request risk ranking, gate contribu
            greedy page-in plan (test_oracle_meter_bytes, test_oracle_gate)
 bytes      byte account per layout and per workload (test_oracle_meter_bytes, test_oracle_groups)
 rope       binary32 RoPE-on-append and its cos/sin table (test_oracle_rope)
+runs       page maps, quantized append and causal attention of runs over a page-scaled cache
+           (test_oracle_runs)
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test in
 ``tests/test_oracle_*.py``; the Philox generator is additionally pinned word for

@@ -37,12 +37,17 @@ __all__ = [
     "tile_bytes",
     "status_string",
     "read_err",
+    "map_runs",
+    "append_runs",
+    "attn_runs",
+    "attn_runs_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("KVQ_LIB") or os.path.join(_HERE, "libkvq.so")
 
-FMT = {"bf16": 0, "e4m3": 1, "e4m3s": 2, "int8": 3, "int8g32": 4}
+FMT = {"bf16": 0, "e4m3": 1, "e4m3s": 2, "int8": 3, "int8g32": 4, "e4m3p": 16, "int8p": 17}
+PAGE_SCALED = ("e4m3p", "int8p")  # 8-bit codes with one power-of-two scale per (page, kv head)
 SCALE_TILE_BYTES = {"e4m3s": 32, "int8": 32, "int8g32": 128}  # fp16 scales of a page's 16 tokens
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 TIER_A, TIER_B, TIER_V, TIER_S = 1, 2, 4, 8
@@ -59,6 +64,7 @@ STATUS = {
     6: "KVQ_ERR_NONFINITE_INPUT",
     7: "KVQ_ERR_RANGE",
     8: "KVQ_ERR_TIMEOUT",
+    9: "KVQ_ERR_NO_PAGES",
 }
 
 
@@ -156,6 +162,18 @@ def load(path: str = LIB_PATH):
     L.kvq_meter.restype = c_int32
     L.kvq_meter.argtypes = [c_void_p, c_int32, c_int32, c_int32, POINTER(MeterParams), c_void_p, c_void_p,
                             c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]
+    L.kvq_map_runs.restype = c_int32
+    L.kvq_map_runs.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
+                               c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p]
+    L.kvq_append_runs.restype = c_int32
+    L.kvq_append_runs.argtypes = [POINTER(_Cache), c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_int32,
+                                  c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_void_p]
+    L.kvq_attn_runs_workspace_size.restype = c_size_t
+    L.kvq_attn_runs_workspace_size.argtypes = [c_int32] * 6
+    L.kvq_attn_runs.restype = c_int32
+    L.kvq_attn_runs.argtypes = [POINTER(_Cache), c_void_p, c_int64, c_int32, c_int32, c_void_p, c_int32, c_int32, c_int32,
+                                c_void_p, c_int32, c_void_p, c_float, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
+                                c_void_p]
     L.kvq_sizeof.restype = c_size_t
     L.kvq_sizeof.argtypes = [c_int32]
     L.kvq_debug_dither.restype = c_int32
@@ -202,7 +220,9 @@ def status_string(status: int) -> str:
 
 
 class PagedCache:
-    """One layer's paged planes (device memory owned by torch tensors)."""
+    """One layer's paged planes (device memory owned by torch tensors).
+
+    The page-scaled formats ("e4m3p", "int8p") have fp16 scale planes [num_kv_heads, num_pages] and no witness."""
 
     def __init__(self, k_fmt: str, v_fmt: str, num_kv_heads: int, num_pages: int, layer: int = 0,
                  seed: int = 0, device="cuda", witness: bool = True, value_witness: bool = False,
@@ -213,6 +233,12 @@ class PagedCache:
         kb = 4096 if k_fmt == "bf16" else 2048
         vb = 4096 if v_fmt == "bf16" else 2048
         z = dict(dtype=torch.uint8, device=device)
+        if k_fmt in PAGE_SCALED or v_fmt in PAGE_SCALED:
+            assert k_fmt == v_fmt and not value_witness and outlier_pairs is None
+            sc = dict(dtype=torch.float16, device=device)
+            self._page_scaled(torch.zeros((n, kb), **z), torch.zeros((n, vb), **z),
+                              torch.zeros((num_kv_heads, num_pages), **sc), torch.zeros((num_kv_heads, num_pages), **sc))
+            return
         self.k = torch.zeros((n, kb), **z)
         self.v = torch.zeros((n, vb), **z)
         self.k_scale = torch.zeros((n, SCALE_TILE_BYTES[k_fmt]), **z) if k_fmt in SCALE_TILE_BYTES else None
@@ -227,6 +253,28 @@ class PagedCache:
             assert outlier_pairs.shape[0] == num_kv_heads and outlier_pairs.dtype == torch.int32
             self.outlier_pairs = outlier_pairs.to(device).contiguous()
             self.k_outlier = torch.zeros((n, 256 if self.n_out <= 4 else 512), **z)
+
+    def _page_scaled(self, k, v, k_scale, v_scale):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.witness = self.v_witness = self.outlier_pairs = self.k_outlier = None
+        self.n_out = 0
+
+    @classmethod
+    def over(cls, k_fmt: str, v_fmt: str, num_kv_heads: int, num_pages: int, *, k: torch.Tensor, v: torch.Tensor,
+             k_scale: torch.Tensor, v_scale: torch.Tensor, layer: int = 0) -> "PagedCache":
+        """A page-scaled cache over planes that the caller has: k, v uint8 [num_pages * num_kv_heads, 2048], k_scale,
+        v_scale fp16 [num_kv_heads, num_pages]."""
+        assert k_fmt in PAGE_SCALED and v_fmt == k_fmt
+        n = num_pages * num_kv_heads
+        for t in (k, v):
+            assert t.dtype == torch.uint8 and t.shape == (n, 2048) and t.is_contiguous()
+        for t in (k_scale, v_scale):
+            assert t.dtype == torch.float16 and t.shape == (num_kv_heads, num_pages) and t.is_contiguous()
+        c = cls.__new__(cls)
+        c.k_fmt, c.v_fmt = k_fmt, v_fmt
+        c.num_kv_heads, c.num_pages, c.layer, c.seed = num_kv_heads, num_pages, layer, 0
+        c._page_scaled(k, v, k_scale, v_scale)
+        return c
 
     def desc(self) -> _Cache:
         return _Cache(FMT[self.k_fmt], FMT[self.v_fmt], self.num_kv_heads, self.num_pages, self.layer, 0,
@@ -393,6 +441,82 @@ def meter(meter_state: torch.Tensor, n_layers: int, batch: int, num_q_heads: int
     _check(lib().kvq_meter(meter_state.data_ptr(), n_layers, batch, num_q_heads, ctypes.byref(params),
                            meter_a.data_ptr(), raw_a.data_ptr(), _ptr(cert_b), _ptr(out_bound), _ptr(two_sided),
                            _ptr(det_tanh), counts.data_ptr(), _ptr(ranking), _stream(stream)), "kvq_meter")
+
+
+def _rows(x: torch.Tensor):
+    """Row stride of a [rows, heads, 128] tensor whose rows are dense: a slice of a fused projection is taken as it is."""
+    assert x.dim() == 3 and x.shape[2] == HEAD_DIM and x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == HEAD_DIM)
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * HEAD_DIM
+
+
+def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+             block_table: torch.Tensor, run_starts: torch.Tensor, seq_lens_out: torch.Tensor, free_count_out: torch.Tensor,
+             *, slot_mapping: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+             err: torch.Tensor | None = None, stream=None):
+    """kvq_map_runs: pages, slots and positions of a step from new_lens [B] (negative: finished) and seq_lens [B].
+
+    free_pages [capacity] is the stack of free pages with free_count [1] in use, block_table [B, max_pages]; run_starts
+    [B + 1], seq_lens_out [B] and free_count_out [1] are written (the latter two may be the inputs), and slot_mapping and
+    positions [max_rows] where given.  All int32 and contiguous."""
+    for t in (new_lens, seq_lens, free_pages, free_count, block_table, run_starts, seq_lens_out, free_count_out,
+              slot_mapping, positions):
+        assert t is None or (t.dtype == torch.int32 and t.is_contiguous())
+    B = new_lens.shape[0]
+    assert seq_lens.shape[0] == B and seq_lens_out.shape[0] == B and run_starts.shape[0] == B + 1
+    assert block_table.dim() == 2 and block_table.shape[0] == B
+    rows = slot_mapping.shape[0] if slot_mapping is not None else positions.shape[0] if positions is not None else 0x7FFFFFFF
+    assert positions is None or positions.shape[0] == rows
+    _check(lib().kvq_map_runs(new_lens.data_ptr(), seq_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.shape[0],
+                              free_count.data_ptr(), block_table.data_ptr(), block_table.shape[1], run_starts.data_ptr(),
+                              seq_lens_out.data_ptr(), free_count_out.data_ptr(), _ptr(slot_mapping), _ptr(positions), rows,
+                              _ptr(err), _stream(stream)), "kvq_map_runs")
+
+
+def append_runs(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
+                *, run_starts: torch.Tensor | None = None, err: torch.Tensor | None = None, stream=None):
+    """kvq_append_runs: quantize the runs' keys and values k, v [rows, Hkv, 128] (fp32 or bf16; rows may be strided) into
+    a page-scaled cache.  run_starts [B + 1]; None: one new token for each request."""
+    assert k.dtype == v.dtype and k.shape == v.shape and k.shape[1] == cache.num_kv_heads
+    assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous()
+    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2
+    B = block_table.shape[0]
+    assert seq_lens.shape[0] == B
+    if run_starts is not None:
+        assert run_starts.dtype == torch.int32 and run_starts.is_contiguous() and run_starts.shape[0] == B + 1
+    d = cache.desc()
+    _check(lib().kvq_append_runs(ctypes.byref(d), k.data_ptr(), _rows(k), v.data_ptr(), _rows(v), DTYPE[k.dtype],
+                                 _ptr(run_starts), B, k.shape[0], block_table.data_ptr(), block_table.shape[1],
+                                 seq_lens.data_ptr(), _ptr(err), _stream(stream)), "kvq_append_runs")
+
+
+def attn_runs_workspace_size(batch: int, num_rows: int, max_run: int, num_kv_heads: int, num_q_heads: int,
+                             q_dtype: torch.dtype) -> int:
+    return int(lib().kvq_attn_runs_workspace_size(batch, num_rows, max_run, num_kv_heads, num_q_heads, DTYPE[q_dtype]))
+
+
+def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, out: torch.Tensor,
+              workspace: torch.Tensor, *, run_starts: torch.Tensor | None = None, max_run: int = 1,
+              lse: torch.Tensor | None = None, sm_scale: float | None = None, err: torch.Tensor | None = None, stream=None):
+    """kvq_attn_runs: causal attention of the runs' queries q [rows, Hq, 128] (fp32 or bf16; rows may be strided) over a
+    page-scaled cache -> out [rows, Hq, 128] in q's type (+ lse [rows, Hq] fp32).  No run is longer than max_run;
+    run_starts None: one query token for each request."""
+    rows, Hq, _ = q.shape
+    assert out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
+    assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous()
+    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2
+    B = block_table.shape[0]
+    assert seq_lens.shape[0] == B
+    if run_starts is not None:
+        assert run_starts.dtype == torch.int32 and run_starts.is_contiguous() and run_starts.shape[0] == B + 1
+    if lse is not None:
+        assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (rows, Hq)
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    d = cache.desc()
+    _check(lib().kvq_attn_runs(ctypes.byref(d), q.data_ptr(), _rows(q), DTYPE[q.dtype], Hq, _ptr(run_starts), B, rows,
+                               int(max_run), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
+                               float(sm_scale), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)), "kvq_attn_runs")
 
 
 def debug_dither(seed: int, layer: int, kv_head: int, slots: torch.Tensor, out: torch.Tensor, stream=None):

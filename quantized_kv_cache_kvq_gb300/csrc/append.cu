@@ -239,6 +239,7 @@ using namespace kvq;
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 extern "C" size_t kvq_tile_bytes(int32_t fmt, int32_t plane) {
+  if (fmt_page_scaled(fmt)) return plane == 0 || plane == 1 ? tile_bytes_k(fmt) : plane == 2 || plane == 3 ? kPageScaleBytes : 0;
   if (fmt < KVQ_FMT_BF16 || fmt > KVQ_FMT_INT8_DITHER_G32) return 0;
   switch (plane) {
     case 0: return static_cast<size_t>(tile_bytes_k(fmt));

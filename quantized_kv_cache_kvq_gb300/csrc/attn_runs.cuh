@@ -1,0 +1,53 @@
+// attn_runs.cuh -- arguments shared by the kernels of kvq_attn_runs.
+//
+// For row r of a run (query token i = r / G of query head kvh G + r % G, at position p = len - n + i):
+//     x_t = sm_scale 2^{ek} (q . kc_t)   for t <= p,       out = sum_t e^{x_t} 2^{ev} vc_t / sum_t e^{x_t}
+// with kc, vc the codes and ek, ev the exponents of the page that holds t.  The value scale goes into the exponent:
+// with y_t = x_t log2 e + ev and m = max_t y_t,  out = sum_t 2^{y_t - m} vc_t / sum_t 2^{y_t - m} 2^{-ev}.  So the
+// products take the codes as they are, the weights never exceed 1, and both scales are exact.
+#pragma once
+
+#include "decode_kernel.cuh"
+#include "runs.cuh"
+
+namespace kvq {
+namespace runs {
+
+// Weights are multiplied by 2^kWeightShift before they are rounded to fp16, whose normal range then reaches down to
+// 2^-26 of the largest weight; numerator and denominator carry the same factor.
+constexpr int kWeightShift = 12;
+
+struct AttnArgs {
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint16_t* ks;
+  const uint16_t* vs;
+  int num_pages;
+  int Hkv, G, Hq;
+  const void* q;
+  long long q_stride;  // elements between rows
+  const int32_t* run_starts;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  int max_pages, batch, num_rows, max_run;
+  float sm_scale;
+  void* out;   // [num_rows][Hq][128], the queries' type
+  float* lse;  // [num_rows][Hq] or nullptr
+  int few_rows;  // runs of at most this many (token, head) rows are the split kernel's, the others the tile kernel's
+  // split kernel
+  long long* ws_cum_pages;  // [batch + 1] pages of all tiles of the runs before
+  int* ws_cum_tiles;        // [batch + 1] row tiles of the runs before
+  float* ws_stats;          // [slots][rows][2]: m, l
+  float* ws_acc;            // [slots][rows][128]
+  int max_tiles;            // row tiles that the workspace has room for
+  int w_max, nwa, stages;
+  // tile kernel
+  float* tw_acc;    // [2 w][256][128]
+  float* tw_stats;  // [2 w][256][2]
+  int32_t* tw_rec;  // [w][4]
+  int tile_ctas;
+  int32_t* err;
+};
+
+}  // namespace runs
+}  // namespace kvq

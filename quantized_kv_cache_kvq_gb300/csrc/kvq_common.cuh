@@ -32,6 +32,9 @@ __host__ __device__ constexpr bool fmt_group_scales(int f) { return f == KVQ_FMT
 __host__ __device__ constexpr bool fmt_has_scale(int f) {
   return f == KVQ_FMT_E4M3_SCALED || fmt_is_int8(f);
 }
+// 8-bit codes with one power-of-two scale per (page, kv head): kvq_append_runs / kvq_attn_runs
+__host__ __device__ constexpr bool fmt_page_scaled(int f) { return f == KVQ_FMT_E4M3_PAGE || f == KVQ_FMT_INT8_PAGE; }
+constexpr int kPageScaleBytes = 2;                     // one fp16 scale per (page, kv head)
 __host__ __device__ constexpr int tile_bytes_k(int f) { return fmt_is_16bit(f) ? 4096 : 2048; }
 __host__ __device__ constexpr int tile_bytes_v(int f) { return fmt_is_16bit(f) ? 4096 : 2048; }
 constexpr int kTileBytesW = 512;

@@ -1,0 +1,188 @@
+// map_runs.cu -- kvq_map_runs: block tables, slot map, positions and the free-page stack from request lengths.
+//
+// The mathematics are three exclusive sums over the batch (tokens, pages wanted, pages handed back) and
+// index arithmetic.  With fc pages on the stack, R handed back and A wanted, the i-th page handed out is entry F - 1 - i
+// of the stack with the handed-back pages on top (F = fc + R).  Since pages are only ever pushed at fc and above, and
+// only ever taken from below fc once the handed-back ones are used up, no entry is both read and written: every
+// output follows from the inputs alone, and the blocks share nothing but the inputs.  The states that may be updated in
+// place (lengths, stack height) are written behind a cluster barrier that all blocks reach after their reads.
+// Bound by latency: one launch, two dependent rounds of loads.
+#include "runs.cuh"
+
+namespace kvq {
+namespace runs {
+namespace {
+
+constexpr int kThreads = 1024;
+
+struct MapArgs {
+  const int32_t* new_lens;
+  const int32_t* seq_lens;
+  int batch;
+  int32_t* free_pages;
+  int free_capacity;
+  const int32_t* free_count;
+  int32_t* block_table;
+  int max_pages;
+  int32_t* run_starts;
+  int32_t* seq_lens_out;
+  int32_t* free_count_out;
+  int32_t* slots;
+  int32_t* positions;
+  int max_rows;
+  int32_t* err;
+};
+
+// Last index i in [0, n) with a[i] <= x; a is non-decreasing with a[0] = 0 and x < a[n].
+__device__ __forceinline__ int find_segment(const int* a, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) map_runs_kernel(const MapArgs a) {
+  __shared__ int s_start[kMaxBatch + 1], s_want[kMaxBatch + 1], s_back[kMaxBatch + 1];
+  __shared__ int s_old[kMaxBatch];
+  __shared__ long long s_tot[3][kThreads / 32];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_bad = 0;
+  const int fc = *a.free_count;
+  int old = 0, add = 0;
+  bool gone = false, bad = false;
+  if (tid < a.batch) {
+    old = a.seq_lens[tid];
+    add = a.new_lens[tid];
+    gone = add < 0;
+    if (gone) add = 0;
+    const long long cap = static_cast<long long>(a.max_pages) * kPage;
+    bad = old < 0 || old > cap || static_cast<long long>(old) + add > cap;
+  }
+  const int held = bad ? 0 : (old + kPage - 1) / kPage;
+  // (tokens, pages wanted, pages handed back), summed in 64 bits: the totals are checked before anything is written
+  long long v[3] = {bad ? 0 : add, bad || gone ? 0 : (static_cast<long long>(old) + add + kPage - 1) / kPage - held,
+                    gone ? held : 0};
+  long long inc[3] = {v[0], v[1], v[2]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc[q], o);
+      if (lane >= o) inc[q] += t;
+    }
+  if (lane == 31)
+    for (int q = 0; q < 3; ++q) s_tot[q][warp] = inc[q];
+  __syncthreads();
+  if (bad) s_bad = 1;
+  long long total[3];
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    long long t = s_tot[q][lane], before = lane < warp ? t : 0;  // kThreads / 32 == 32 warps, one per lane
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      t += __shfl_xor_sync(0xffffffffu, t, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    total[q] = t;
+    inc[q] += before;
+  }
+  __syncthreads();
+  int status = KVQ_OK;
+  if (s_bad || total[0] > a.max_rows || fc < 0 || fc > a.free_capacity || fc + total[2] - total[1] > a.free_capacity)
+    status = KVQ_ERR_DEVICE_BOUNDS;
+  else if (total[1] > fc + total[2])
+    status = KVQ_ERR_NO_PAGES;
+  const bool ok = status == KVQ_OK;
+  if (tid < a.batch) {
+    s_start[tid] = static_cast<int>(inc[0] - v[0]);
+    s_want[tid] = static_cast<int>(inc[1] - v[1]);
+    s_back[tid] = static_cast<int>(inc[2] - v[2]);
+    s_old[tid] = old;
+  }
+  const int n_rows = ok ? static_cast<int>(total[0]) : 0, A = ok ? static_cast<int>(total[1]) : 0,
+            R = ok ? static_cast<int>(total[2]) : 0, F = fc + R;
+  if (tid == 0) {
+    s_start[a.batch] = n_rows;
+    s_want[a.batch] = A;
+    s_back[a.batch] = R;
+  }
+  __syncthreads();
+  // every block has read the lengths and the stack height: they may be overwritten after this barrier's second half
+  asm volatile("barrier.cluster.arrive;" ::: "memory");
+
+  const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
+  auto handed_back = [&](int i) {  // i-th page of the finished requests
+    const int s = find_segment(s_back, a.batch, i);
+    return a.block_table[static_cast<size_t>(s) * a.max_pages + (i - s_back[s])];
+  };
+  auto page_of = [&](int i) {  // i-th page handed out
+    const int e = F - 1 - i;
+    return e >= fc ? handed_back(e - fc) : a.free_pages[e];
+  };
+  for (int i = first; i < A; i += stride) {
+    const int s = find_segment(s_want, a.batch, i);
+    a.block_table[static_cast<size_t>(s) * a.max_pages + (s_old[s] + kPage - 1) / kPage + (i - s_want[s])] = page_of(i);
+  }
+  for (int i = first; i < R - A; i += stride) a.free_pages[fc + i] = handed_back(i);
+  if (a.slots || a.positions) {
+    for (int r = first; r < a.max_rows; r += stride) {
+      int slot = -1, pos = 0;
+      if (r < n_rows) {
+        const int s = find_segment(s_start, a.batch, r);
+        const int o = s_old[s], h = (o + kPage - 1) / kPage;
+        pos = o + (r - s_start[s]);
+        const int j = pos / kPage;
+        const int page = j < h ? a.block_table[static_cast<size_t>(s) * a.max_pages + j] : page_of(s_want[s] + j - h);
+        if (page < 0 || page > 0x7FFFFFF) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
+        else slot = page * kPage + pos % kPage;
+      }
+      if (a.slots) a.slots[r] = slot;
+      if (a.positions) a.positions[r] = pos;
+    }
+  }
+  asm volatile("barrier.cluster.wait;" ::: "memory");
+  if (blockIdx.x == 0) {
+    if (tid < a.batch) {
+      a.run_starts[tid] = ok ? s_start[tid] : 0;
+      a.seq_lens_out[tid] = !ok ? old : gone ? 0 : old + add;
+    }
+    if (tid == 0) {
+      a.run_starts[a.batch] = n_rows;
+      *a.free_count_out = F - A;
+      if (!ok) report(a.err, status);
+    }
+  }
+}
+
+}  // namespace
+}  // namespace runs
+}  // namespace kvq
+
+extern "C" kvq_status kvq_map_runs(const int32_t* new_lens, const int32_t* seq_lens, int32_t batch, int32_t* free_pages,
+                                   int32_t free_capacity, const int32_t* free_count, int32_t* block_table,
+                                   int32_t max_pages_per_seq, int32_t* run_starts, int32_t* seq_lens_out,
+                                   int32_t* free_count_out, int32_t* slot_mapping, int32_t* positions, int32_t max_rows,
+                                   int32_t* err_word, kvq_stream_t stream) {
+  using namespace kvq::runs;
+  if (batch < 0 || batch > kMaxBatch || free_capacity < 0 || max_pages_per_seq < 0 || max_rows < 0) return KVQ_ERR_INVALID_ARG;
+  if (!free_count || !run_starts || !free_count_out || (free_capacity > 0 && !free_pages)) return KVQ_ERR_INVALID_ARG;
+  if (batch > 0 && (!new_lens || !seq_lens || !seq_lens_out || (max_pages_per_seq > 0 && !block_table)))
+    return KVQ_ERR_INVALID_ARG;
+  MapArgs a{new_lens,   seq_lens,     batch,          free_pages,   free_capacity, free_count, block_table, max_pages_per_seq,
+            run_starts, seq_lens_out, free_count_out, slot_mapping, positions,     max_rows,   err_word};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(8);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 8;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, map_runs_kernel, a) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}

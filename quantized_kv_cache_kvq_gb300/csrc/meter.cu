@@ -332,6 +332,7 @@ extern "C" const char* kvq_status_string(int32_t status) {
     case KVQ_ERR_NONFINITE_INPUT: return "KVQ_ERR_NONFINITE_INPUT";
     case KVQ_ERR_RANGE: return "KVQ_ERR_RANGE";
     case KVQ_ERR_TIMEOUT: return "KVQ_ERR_TIMEOUT";
+    case KVQ_ERR_NO_PAGES: return "KVQ_ERR_NO_PAGES";
   }
   return "KVQ_ERR_UNKNOWN";
 }
