@@ -120,7 +120,7 @@ __device__ void load_q(const AttnArgs& a, const Unit& u, Query<NT>& f, uint32_t*
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
     // the row times 2^-er, largest element in [2^8, 2^9): bf16 elements are then exact in fp16 down to 2^-22 of it
     int er = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8;
-    er = min(max(er, -100), 100);
+    er = min(max(er, -100), 120);
     const float f0 = exp2_int(-er);
 #pragma unroll
     for (int kb = 0; kb < 8; ++kb)
@@ -576,18 +576,25 @@ constexpr int kSplitWarps = 16;  // the most that any variant uses (sizes the wo
 int row_blocks(long long max_rows) { return max_rows <= 8 ? 1 : 2; }
 
 struct Workspace {
-  size_t cum_pages, cum_tiles, stats, acc, total;
-  int few_rows;
+  size_t cum_pages, cum_tiles, stats, acc, tw_acc, tw_stats, tw_rec, total;
+  int nt;        // row tiles of 8 nt rows
+  int few_rows;  // runs with more rows go to the tile kernel
+  bool tile;     // there may be such runs
   long long tiles;
 };
 
+// BF16 runs of more than 16 (token, head) rows are the tile kernel's; fp32 queries have the split kernel for every length.
+constexpr int kFewRows = 16;
+
 Workspace workspace(int batch, int num_rows, int max_run, int hkv, int hq, int q_dtype, int sms) {
-  (void)q_dtype;
   const int G = hq / hkv;
-  const int nt = row_blocks(static_cast<long long>(max_run) * G);
+  const long long max_rows = static_cast<long long>(max_run) * G;
+  const int nt = row_blocks(max_rows);
   Workspace w{};
-  w.few_rows = 0x7FFFFFFF;
-  const size_t tiles = (static_cast<size_t>(num_rows) * G) / (8 * nt) + batch;
+  w.nt = nt;
+  w.tile = q_dtype == KVQ_DTYPE_BF16 && max_rows > kFewRows;
+  w.few_rows = w.tile ? kFewRows : 0x7FFFFFFF;
+  const size_t tiles = w.tile ? batch : (static_cast<size_t>(num_rows) * G) / (8 * nt) + batch;
   w.tiles = static_cast<long long>(tiles);
   const size_t slots = static_cast<size_t>(sms) * kSplitWarps + tiles * hkv;
   w.cum_pages = 0;
@@ -595,6 +602,13 @@ Workspace workspace(int batch, int num_rows, int max_run, int hkv, int hq, int q
   w.stats = w.cum_tiles + align256((batch + 1) * sizeof(int));
   w.acc = w.stats + align256(slots * 8 * nt * 2 * sizeof(float));
   w.total = w.acc + align256(slots * 8 * nt * kHeadDim * sizeof(float));
+  if (w.tile) {
+    const size_t base = w.total;
+    w.total += tile_workspace(sms, &w.tw_acc, &w.tw_stats, &w.tw_rec);
+    w.tw_acc += base;
+    w.tw_stats += base;
+    w.tw_rec += base;
+  }
   return w;
 }
 
@@ -711,8 +725,13 @@ extern "C" kvq_status kvq_attn_runs(const kvq_cache* cache, const void* q, int64
   a.err = err_word;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = q_dtype == KVQ_DTYPE_F32;
-  const int nt = row_blocks(static_cast<long long>(mr) * a.G);
-  const cudaError_t e = cache->k_fmt == KVQ_FMT_INT8_PAGE ? launch<true>(a, f32, nt, sms, smem_max, s)
-                                                          : launch<false>(a, f32, nt, sms, smem_max, s);
+  const bool int8 = cache->k_fmt == KVQ_FMT_INT8_PAGE;
+  cudaError_t e = int8 ? launch<true>(a, f32, w.nt, sms, smem_max, s) : launch<false>(a, f32, w.nt, sms, smem_max, s);
+  if (e == cudaSuccess && w.tile) {
+    a.tw_acc = reinterpret_cast<float*>(ws + w.tw_acc);
+    a.tw_stats = reinterpret_cast<float*>(ws + w.tw_stats);
+    a.tw_rec = reinterpret_cast<int32_t*>(ws + w.tw_rec);
+    e = launch_tile(a, int8, sms, s);
+  }
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

@@ -44,10 +44,14 @@ struct AttnArgs {
   // tile kernel
   float* tw_acc;    // [2 w][256][128]
   float* tw_stats;  // [2 w][256][2]
-  int32_t* tw_rec;  // [w][4]
-  int tile_ctas;
+  int32_t* tw_rec;  // [w][8]
+  int tile_ctas, tile_min;  // CTAs, and the fewest tiles that are worth one
   int32_t* err;
 };
+
+// Tile kernel and its merge (attn_runs_tile.cu); its part of the workspace, with the offsets of the three arrays.
+cudaError_t launch_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s);
+size_t tile_workspace(int sms, size_t* acc, size_t* stats, size_t* rec);
 
 }  // namespace runs
 }  // namespace kvq

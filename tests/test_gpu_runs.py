@@ -323,6 +323,11 @@ def test_sharp_flat_and_negative_scales(kvq, new):
     attention_case(kvq, "e4m3p", "bf16", lens, new, 2, 4, q_scale=1e30, sm_scale=1e-31)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_several_tiles_and_units_for_every_block(kvq, fmt):
+    attention_case(kvq, fmt, "bf16", [2100, 900, 40, 700], [700, 900, 1, 3], 4, 2, behind=5)
+
+
 def test_long_context_in_random_pages(kvq):
     attention_case(kvq, "int8p", "bf16", [20011, 31, 7000], [1, 1, 1], 2, 7)
     attention_case(kvq, "e4m3p", "bf16", [9001, 31], [40, 31], 1, 8)
