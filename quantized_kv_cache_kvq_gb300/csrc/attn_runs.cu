@@ -731,6 +731,7 @@ extern "C" kvq_status kvq_attn_runs(const kvq_cache* cache, const void* q, int64
     a.tw_acc = reinterpret_cast<float*>(ws + w.tw_acc);
     a.tw_stats = reinterpret_cast<float*>(ws + w.tw_stats);
     a.tw_rec = reinterpret_cast<int32_t*>(ws + w.tw_rec);
+    if (a.num_pages == 0) a.k = a.v = ws;  // absent pages are read as page 0 and thrown away
     e = launch_tile(a, int8, sms, s);
   }
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

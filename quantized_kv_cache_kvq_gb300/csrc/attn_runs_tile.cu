@@ -59,20 +59,25 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
   // K-major, 128-byte swizzle: 1024 bytes between groups of 8 rows
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+// Issued by the whole converged warp with the same operands, predicated on the one lane that elect.sync picked: the operands
+// then stay in uniform registers (issued from one lane's branch, every product cost ~97 clocks to set up, 64 to run).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(kIdesc), "r"(acc), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(kIdesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(kIdesc), "r"(acc), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(leader)
+      : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -148,36 +153,49 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, const RunInfo& r, int
   return max(1, (limit + kKeys - 1) / kKeys);
 }
 
+// The roles' loops are kept small: what happens once a unit is a call, since code that does not fit the instruction
+// caches cost more than the work itself (131 KB of code in all, 2.20 ms on a prompt of 11996 tokens).
+struct UnitInfo {
+  int s, kvh, u, tiles;
+  RunInfo run;
+};
+__device__ __noinline__ UnitInfo unit_info(const AttnArgs& a, int s, int kvh, int u) {
+  UnitInfo i{s, kvh, u, 0, run_info(a, s)};
+  i.tiles = tiles_of(a, i.run, u);
+  return i;
+}
+__device__ __noinline__ UnitInfo next_unit(const AttnArgs& a, int s, int kvh, int u, int units) {
+  if (++u == units) {
+    u = 0;
+    if (++kvh == a.Hkv) {
+      kvh = 0;
+      do ++s; while (run_info(a, s).units == 0);  // called only where a later unit exists
+    }
+  }
+  return unit_info(a, s, kvh, u);
+}
+
 // Where a role is in its CTA's range of tiles.
 struct Cursor {
-  RunInfo run;
-  int s, kvh, u, j, tiles, left;
+  UnitInfo at;
+  int j, left;
   bool first;  // the tile is the first of its piece
   __device__ __forceinline__ void begin(const AttnArgs& a, const Tail* t) {
-    s = t->start[0]; kvh = t->start[1]; u = t->start[2]; j = t->start[3];
+    at = unit_info(a, t->start[0], t->start[1], t->start[2]);
+    j = t->start[3];
     left = t->n;
-    run = run_info(a, s);
-    tiles = tiles_of(a, run, u);
     first = true;
   }
-  __device__ __forceinline__ bool last() const { return left == 1 || j + 1 == tiles; }
-  __device__ __forceinline__ int halves(const AttnArgs& a) const { return run.n * a.G - u * kRows > 128 ? 2 : 1; }
+  __device__ __forceinline__ bool last() const { return left == 1 || j + 1 == at.tiles; }
   __device__ __forceinline__ void advance(const AttnArgs& a) {
     first = false;
-    if (--left == 0) return;
-    if (++j < tiles) return;
+    if (--left == 0 || ++j < at.tiles) return;
     j = 0;
     first = true;
-    if (++u == run.units) {
-      u = 0;
-      if (++kvh == a.Hkv) {
-        kvh = 0;
-        do run = run_info(a, ++s); while (run.units == 0);  // left > 0: a later run has units
-      }
-    }
-    tiles = tiles_of(a, run, u);
+    at = next_unit(a, at.s, at.kvh, at.u, at.run.units);
   }
 };
+__device__ __forceinline__ int halves_of(const AttnArgs& a, const UnitInfo& i) { return i.run.n * a.G - i.u * kRows > 128 ? 2 : 1; }
 
 // The CTA's range: the sums over the batch in `cum` (shared memory that the ring takes over later).
 __device__ void plan(const AttnArgs& a, Tail* t, long long* cum) {
@@ -274,112 +292,119 @@ template <bool INT8>
 __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
   const int cw = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   constexpr uint32_t kZero = INT8 ? 0x80808080u : 0u;
-  Cursor c, ahead;  // ahead: one tile further, for the block table
+  // Everything is loaded one step before its use and left untouched until then, so that no load is waited for where it is
+  // issued: block-table entries a tile ahead, scales and codes half a tile.  An absent page (behind the context, or an
+  // entry outside the cache) is read as page 0 and cleared when it is converted.
+  Cursor c;
   c.begin(a, t);
-  ahead = c;
-  // physical page of page (lane & 7) of the cursor's tile; -1: behind the context or outside the cache
-  auto load_phys = [&](const Cursor& k) {
-    const int page = k.j * kPagesPerTile + (lane & 7);
-    if (page * kPage >= k.run.len) return -1;
-    const int p = a.block_table[static_cast<size_t>(k.s) * a.max_pages + page];
-    if (p < 0 || p >= a.num_pages) {
-      if (cw == 0 && lane < 8) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
-      return -1;
-    }
-    return p;
+  const int total = c.left;
+  // Entry of page (lane & 7) of a tile; 0 behind the context.
+  auto load_entry = [&](int s, int j, int len) {
+    const int page = j * kPagesPerTile + (lane & 7);
+    return page * kPage < len ? a.block_table[static_cast<size_t>(s) * a.max_pages + page] : 0;
   };
+  auto absent = [&](int entry) { return entry < 0 || entry >= a.num_pages; };
   uint4 kr[8], vr[8];
-  float4 sc;
-  auto load_k = [&](const Cursor& k, int phys) {  // this warp's pages 2 cw, 2 cw + 1
+  uint16_t ks = 0, vs = 0;  // lanes 0, 1: scales of the warp's key pages
+  // pages 2 cw, 2 cw + 1 of the key tile, words of 512 bytes
+  auto load_k = [&](int kvh, int phys) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int p = __shfl_sync(dec::kFull, phys, 2 * cw + i);
-      const uint8_t* src = a.k + (static_cast<size_t>(max(p, 0)) * a.Hkv + k.kvh) * 2048 + lane * 16;
+      const uint8_t* src = a.k + ((static_cast<size_t>(p) * a.Hkv + kvh) * 2048 + lane * 16);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) kr[4 * i + w] = p >= 0 ? ldg_codes(src + w * 512) : make_uint4(kZero, kZero, kZero, kZero);
+      for (int w = 0; w < 4; ++w) kr[4 * i + w] = ldg_codes(src + w * 512);
     }
     const int p = __shfl_sync(dec::kFull, phys, 2 * cw + (lane & 1));
-    sc = make_float4(0.f, -INFINITY, 0.f, 0.f);
-    if (p >= 0 && lane < 2) {
-      const size_t si = static_cast<size_t>(k.kvh) * a.num_pages + p;
-      const int ek = f16_to_exp(a.ks[si]), ev = f16_to_exp(a.vs[si]);
-      sc = make_float4(fabsf(a.sm_scale) * dec::kLog2e * exp2_int(ek), static_cast<float>(ev), exp2_int(-ev), 0.f);
+    const size_t si = static_cast<size_t>(kvh) * a.num_pages + p;
+    if (a.num_pages > 0) {
+      ks = a.ks[si];
+      vs = a.vs[si];
     }
   };
-  auto load_v = [&](const Cursor& k, int phys) {  // channels 32 cw .. of all pages; odd rows take the pairs of pages crosswise
+  // channels 32 cw .. of all pages of the value tile; odd rows take the pairs of pages crosswise
+  auto load_v = [&](int kvh, int phys) {
 #pragma unroll
-    for (int pp = 0; pp < 4; ++pp)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int page = 2 * (pp ^ (g & 1)) + i;
-        const int p = __shfl_sync(dec::kFull, phys, page);
-        const int nvalid = k.run.len - (k.j * kPagesPerTile + page) * kPage;  // tokens of the page inside the context
-        const uint8_t* src = a.v + (static_cast<size_t>(max(p, 0)) * a.Hkv + k.kvh) * 2048 + (cw * 32 + lane) * 16;
-        uint4 w = p >= 0 ? ldg_codes(src) : make_uint4(kZero, kZero, kZero, kZero);
-        if (nvalid < kPage) {  // what lies behind the context may be anything, a NaN too
-          auto mask = [&](int tok) { return (tok < nvalid ? 0x00FF00FFu : 0u) | (tok + 1 < nvalid ? 0xFF00FF00u : 0u); };
-          const uint32_t m0 = mask(2 * q), m1 = mask(2 * q + 8);
-          w.x = (w.x & m0) | (kZero & ~m0);
-          w.z = (w.z & m0) | (kZero & ~m0);
-          w.y = (w.y & m1) | (kZero & ~m1);
-          w.w = (w.w & m1) | (kZero & ~m1);
-        }
-        vr[2 * pp + i] = w;
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int p = __shfl_sync(dec::kFull, phys, i ^ (2 * (g & 1)));
+      vr[i] = ldg_codes(a.v + ((static_cast<size_t>(p) * a.Hkv + kvh) * 2048 + (cw * 32 + lane) * 16));
+    }
   };
-  int slot = 0, idx = 0;
+  int slot = 0;
   uint32_t phase = 0;
-  auto next_slot = [&]() {
-    ++idx;
-    if (++slot == kSlots) { slot = 0; phase ^= 1u; }
-  };
   auto publish = [&]() {
     dec::fence_proxy_async();
     __syncwarp();
     if (lane == 0) arrive(&t->full[slot]);
-    next_slot();
+    if (++slot == kSlots) { slot = 0; phase ^= 1u; }
   };
-  const int total = c.left;
-  int phys = load_phys(c);
-  ahead.advance(a);
-  int phys_next = total > 1 ? load_phys(ahead) : -1;
-  load_k(c, phys);
+  // this lane's rows and chunks: token 8 h + g of page p goes to row 32 (p >> 1) + 8 (g >> 1) + 4 (p & 1) + 2 h + (g & 1)
+  const int k_row = 32 * cw + 8 * (g >> 1) + (g & 1);
+  const int v_row = 32 * cw + g;
+  int entry = load_entry(c.at.s, c.j, c.at.run.len), entry_next = 0;
+  int phys = absent(entry) ? 0 : entry;
+  load_k(c.at.kvh, phys);
   for (int jj = 0; jj < total; ++jj) {
-    load_v(c, phys);
-    if (!wait_warp(&t->empty[slot], phase ^ 1u, &t->abort)) return;
-    if (lane < 2) t->scale[jj % kScaleSlots][2 * cw + lane] = sc;
-    uint8_t* dst = ring + slot * kOperand;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {  // word (t >> 3, channel half): token 8 (w >> 1) + g, channels 64 (w & 1) + 16 q ..
-        const uint4 x = kr[4 * i + w];
-        const int p = 2 * cw + i;
-        // token 8 h + g -> row 32 (p >> 1) + 8 (g >> 1) + 4 (p & 1) + 2 h + (g & 1)
-        const int row = 32 * (p >> 1) + 8 * (g >> 1) + 4 * (p & 1) + 2 * (w >> 1) + (g & 1);
-        uint8_t* base = dst + (w & 1) * 16384 + row * 128;
-        *reinterpret_cast<uint4*>(base + (((2 * q) ^ (row & 7)) << 4)) =
-            make_uint4(cvt_lo<INT8>(x.x), cvt_hi<INT8>(x.x), cvt_lo<INT8>(x.y), cvt_hi<INT8>(x.y));
-        *reinterpret_cast<uint4*>(base + (((2 * q + 1) ^ (row & 7)) << 4)) =
-            make_uint4(cvt_lo<INT8>(x.z), cvt_hi<INT8>(x.z), cvt_lo<INT8>(x.w), cvt_hi<INT8>(x.w));
-      }
-    publish();
+    const int in_context = c.at.run.len - c.j * kKeys;  // tokens of the tile that the context has
+    const bool here = (lane & 7) * kPage < in_context;
+    const unsigned lost = __ballot_sync(dec::kFull, !here || absent(entry));  // bits 0..7: absent pages
+    if (here && absent(entry) && cw == 0 && lane < 8) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
+    load_v(c.at.kvh, phys);
+    // the next tile's table entries
+    const bool more = jj + 1 < total;
     c.advance(a);
-    if (jj + 1 < total) {
-      phys = phys_next;
-      load_k(c, phys);
-      ahead.advance(a);
-      phys_next = jj + 2 < total ? load_phys(ahead) : -1;
+    if (more) entry_next = load_entry(c.at.s, c.j, c.at.run.len);
+    if (!wait_warp(&t->empty[slot], phase ^ 1u, &t->abort)) return;
+    if (lane < 2) {
+      const int ek = f16_to_exp(ks), ev = f16_to_exp(vs);
+      t->scale[jj % kScaleSlots][2 * cw + lane] =
+          (lost >> (2 * cw + lane)) & 1u ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                                         : make_float4(fabsf(a.sm_scale) * dec::kLog2e * exp2_int(ek), static_cast<float>(ev), exp2_int(-ev), 0.f);
+    }
+    uint8_t* dst = ring + slot * kOperand + k_row * 128;
+    if (lost & 0xFFu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((lost >> (2 * cw + (i >> 2))) & 1u) kr[i] = make_uint4(kZero, kZero, kZero, kZero);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // page 2 cw + (i >> 2), word i & 3 = (token half, channel half)
+      const uint4 x = kr[i];
+      const int dr = 4 * (i >> 2) + 2 * ((i >> 1) & 1);  // (k_row + dr) & 7 = dr | (g & 1)
+      uint8_t* base = dst + (i & 1) * 16384 + dr * 128;
+      *reinterpret_cast<uint4*>(base + (((2 * q) ^ (dr | (g & 1))) << 4)) =
+          make_uint4(cvt_lo<INT8>(x.x), cvt_hi<INT8>(x.x), cvt_lo<INT8>(x.y), cvt_hi<INT8>(x.y));
+      *reinterpret_cast<uint4*>(base + (((2 * q + 1) ^ (dr | (g & 1))) << 4)) =
+          make_uint4(cvt_lo<INT8>(x.z), cvt_hi<INT8>(x.z), cvt_lo<INT8>(x.w), cvt_hi<INT8>(x.w));
+    }
+    publish();
+    if (more) {
+      entry = entry_next;
+      phys = absent(entry) ? 0 : entry;
+      load_k(c.at.kvh, phys);
     }
     if (!wait_warp(&t->empty[slot], phase ^ 1u, &t->abort)) return;
-    dst = ring + slot * kOperand;
+    if (in_context < kKeys || (lost & 0xFFu)) {  // what lies behind the context may be anything, a NaN too
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int page = i ^ (2 * (g & 1));
+        const int nvalid = (lost >> page) & 1u ? 0 : in_context - page * kPage;
+        auto mask = [&](int tok) { return (tok < nvalid ? 0x00FF00FFu : 0u) | (tok + 1 < nvalid ? 0xFF00FF00u : 0u); };
+        const uint32_t m0 = mask(2 * q), m1 = mask(2 * q + 8);
+        uint4& w = vr[i];
+        w.x = (w.x & m0) | (kZero & ~m0);
+        w.z = (w.z & m0) | (kZero & ~m0);
+        w.y = (w.y & m1) | (kZero & ~m1);
+        w.w = (w.w & m1) | (kZero & ~m1);
+      }
+    }
+    dst = ring + slot * kOperand + v_row * 128;
 #pragma unroll
     for (int pp = 0; pp < 4; ++pp) {
-      const int pair = pp ^ (g & 1);
       const uint4 x = vr[2 * pp], y = vr[2 * pp + 1];
-      // column 32 pair + 8 q + {page 2 pair: 0..3, page 2 pair + 1: 4..7}
-      const int chunk = (4 * (pair & 1) + q) ^ g;
-      uint8_t* base = dst + (pair >> 1) * 16384 + (32 * cw + g) * 128 + (chunk << 4);
+      // pair of pages pp ^ (g & 1): column 32 pair + 8 q + {page 2 pair: 0..3, page 2 pair + 1: 4..7}
+      const int chunk = (4 * ((pp ^ g) & 1) + q) ^ g;
+      uint8_t* base = dst + (pp >> 1) * 16384 + (chunk << 4);
       *reinterpret_cast<uint4*>(base) = make_uint4(cvt_lo<INT8>(x.x), cvt_lo<INT8>(x.y), cvt_lo<INT8>(y.x), cvt_lo<INT8>(y.y));
       *reinterpret_cast<uint4*>(base + 8 * 128) = make_uint4(cvt_hi<INT8>(x.x), cvt_hi<INT8>(x.y), cvt_hi<INT8>(y.x), cvt_hi<INT8>(y.y));
       *reinterpret_cast<uint4*>(base + 16 * 128) = make_uint4(cvt_lo<INT8>(x.z), cvt_lo<INT8>(x.w), cvt_lo<INT8>(y.z), cvt_lo<INT8>(y.w));
@@ -388,7 +413,7 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
     publish();
   }
   // the products' last arrivals on the ring land before the CTA may end
-  for (int i = 0; i < kSlots && i < idx; ++i) {
+  for (int i = 0; i < kSlots && i < 2 * total; ++i) {
     if (--slot < 0) { slot = kSlots - 1; phase ^= 1u; }
     if (!wait_warp(&t->empty[slot], phase, &t->abort)) return;
   }
@@ -398,6 +423,8 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
 __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_t tmem, int32_t* rec) {
   Cursor c;
   c.begin(a, t);
+  const uint32_t leader = dec::elect_one();
+  tmem = dec::uniform_u32(tmem);
   const uint64_t ring = smem_desc(smem_base + kOffRing);
   const uint64_t qd = smem_desc(smem_base + kOffQ);
   auto k_step = [](int ks) { return static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4); };
@@ -405,13 +432,13 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)
       mma_ss(tmem + kTmemS + 128 * i, qd + static_cast<uint64_t>(i * (kOperand >> 4)) + k_step(ks),
-             ring + static_cast<uint64_t>(slot * (kOperand >> 4)) + k_step(ks), ks > 0);
+             ring + static_cast<uint64_t>(slot * (kOperand >> 4)) + k_step(ks), ks > 0, leader);
   };
   auto pv = [&](int i, int slot, bool acc) {
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)
       mma_ts(tmem + kTmemO + 128 * i, tmem + kTmemS + 128 * i + 8 * ks,
-             ring + static_cast<uint64_t>(slot * (kOperand >> 4)) + k_step(ks), acc || ks > 0);
+             ring + static_cast<uint64_t>(slot * (kOperand >> 4)) + k_step(ks), acc || ks > 0, leader);
   };
   int slot = 0;  // of the operand tile taken next
   uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
@@ -422,24 +449,24 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
   bool have_s = false;  // the current tile's S products are issued
   int from = 0;         // first tile of the current piece
   for (int jj = 0; jj < total; ++jj) {
-    const int nh = c.halves(a);
+    const int nh = halves_of(a, c.at);
     if (c.first) from = c.j;
-    if (jj == total - 1 && from == 0 && c.j + 1 < c.tiles) {  // the unit began here and goes on in the next CTA
-      rec[1] = c.s;
-      rec[2] = c.kvh;
-      rec[3] = c.u;
+    if (leader && jj == total - 1 && from == 0 && c.j + 1 < c.at.tiles) {  // the unit began here and goes on in the next CTA
+      rec[1] = c.at.s;
+      rec[2] = c.at.kvh;
+      rec[3] = c.at.u;
       rec[0] = 1;
     }
     if (!have_s) {  // first tile of a piece
-      if (!wait(&t->full[slot], phase, &t->abort)) return;
+      if (!wait_warp(&t->full[slot], phase, &t->abort)) return;
       for (int i = 0; i < nh; ++i) {
-        if (!wait(&t->q_full[i], q_phase[i], &t->abort)) return;
+        if (!wait_warp(&t->q_full[i], q_phase[i], &t->abort)) return;
         q_phase[i] ^= 1u;
         fence_after();
         qk(i, slot);
-        commit(&t->s_full[i]);
+        commit(&t->s_full[i], leader);
       }
-      commit(&t->empty[slot]);
+      commit(&t->empty[slot], leader);
       next_slot();
     }
     const bool more = !c.last();
@@ -447,19 +474,19 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
     const uint32_t v_phase = phase;
     next_slot();
     for (int i = 0; i < nh; ++i) {
-      if (!wait(&t->p_full[i], p_phase[i], &t->abort)) return;
+      if (!wait_warp(&t->p_full[i], p_phase[i], &t->abort)) return;
       p_phase[i] ^= 1u;
-      if (i == 0 && !wait(&t->full[v_slot], v_phase, &t->abort)) return;
+      if (i == 0 && !wait_warp(&t->full[v_slot], v_phase, &t->abort)) return;
       fence_after();
       pv(i, v_slot, !c.first);
-      commit(&t->pv_done[i]);
-      if (i == nh - 1) commit(&t->empty[v_slot]);
+      commit(&t->pv_done[i], leader);
+      if (i == nh - 1) commit(&t->empty[v_slot], leader);
       if (more) {
-        if (i == 0 && !wait(&t->full[slot], phase, &t->abort)) return;
+        if (i == 0 && !wait_warp(&t->full[slot], phase, &t->abort)) return;
         fence_after();
         qk(i, slot);
-        commit(&t->s_full[i]);
-        if (i == nh - 1) commit(&t->empty[slot]);
+        commit(&t->s_full[i], leader);
+        if (i == nh - 1) commit(&t->empty[slot], leader);
       }
     }
     if (more) next_slot();
@@ -472,59 +499,214 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
 // Column k of a 32-column chunk: page parity (k >> 2) & 1, token of the page.
 __device__ __forceinline__ constexpr int col_token(int k) { return 2 * (k >> 3) + (k & 1) + 8 * ((k >> 1) & 1); }
 
+// The row's softmax goes over S in TMEM twice, 32 columns at a time with the next ones on their way: the maximum, then the
+// weights.  (All 128 values in registers instead: 184 registers do not hold them with the rest, and what spills costs far
+// more than reading S again: 3.00 -> 2.76 ms on a prompt of 11996 tokens.)  Pages 2 i and 2 i + 1 lie in chunk i, their
+// columns in groups of four.  y = x log2 e + ev = S k + ev; since k >= 0 a page's largest S gives its largest y.
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float row_max(uint32_t ts, const float4* scale, float rk) {
+  float tm = -INFINITY;
+  float sb[2][32];
+  tmem_ld32(ts, sb[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float* s = sb[i & 1];
+    wait_ld();
+    loaded<32>(s);
+    if (i < 3) tmem_ld32(ts + 32 * (i + 1), sb[(i + 1) & 1]);
+    float pm[2];
+#pragma unroll
+    for (int par = 0; par < 2; ++par) {
+      const float* x = s + 4 * par;  // columns 0..3, 8..11, 16..19, 24..27 from here
+      const float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[8], x[9]), m2 = max3(x[10], x[11], x[16]);
+      const float m3 = max3(x[17], x[18], x[19]), m4 = max3(x[24], x[25], x[26]);
+      pm[par] = fmaxf(max3(m0, m1, m2), max3(m3, m4, x[27]));
+    }
+    const float4 s0 = scale[2 * i], s1 = scale[2 * i + 1];
+    tm = max3(tm, fmaf(pm[0], s0.x * rk, s0.y), fmaf(pm[1], s1.x * rk, s1.y));
+  }
+  return tm;
+}
+// Weights 2^{y + base} as fp16 pairs over the columns that S leaves free, and their sum without the value scales.
+__device__ __forceinline__ float weights(uint32_t ts, const float4* scale, float rk, float base) {
+  float l = 0.f;
+  float sb[2][32];
+  tmem_ld32(ts, sb[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float* s = sb[i & 1];
+    wait_ld();
+    loaded<32>(s);
+    if (i < 3) tmem_ld32(ts + 32 * (i + 1), sb[(i + 1) & 1]);
+    const float4 s0 = scale[2 * i], s1 = scale[2 * i + 1];
+    const dec::f2x k2[2] = {dec::f2_splat(s0.x * rk), dec::f2_splat(s1.x * rk)};
+    const dec::f2x b2[2] = {dec::f2_splat(s0.y + base), dec::f2_splat(s1.y + base)};
+    dec::f2x sum[2];
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const int par = (e >> 2) & 1;
+      float y0, y1;
+      dec::f2_unpack(dec::f2_fma(dec::f2_pack(s[e], s[e + 1]), k2[par], b2[par]), y0, y1);
+      const float p0 = ex2(y0), p1 = ex2(y1);
+      const dec::f2x p2 = dec::f2_pack(p0, p1);
+      sum[par] = (e & ~4) == 0 ? p2 : dec::f2_add(sum[par], p2);
+      pk[e >> 1] = dec::pack_f16(p0, p1);
+    }
+    tmem_st16(ts + 16 * i, pk);
+    float l0, l1, l2, l3;
+    dec::f2_unpack(sum[0], l0, l1);
+    dec::f2_unpack(sum[1], l2, l3);
+    l = fmaf(l0 + l1, s0.z, fmaf(l2 + l3, s1.z, l));
+  }
+  return l;
+}
+// The same where a row does not see all 128 keys (token < seen of the tile): the tiles on the diagonal.  Hidden logits are
+// -inf whatever the scale, and whatever S holds there.
+__device__ __noinline__ float row_max_masked(uint32_t ts, const float4* scale, float rk, int seen) {
+  float tm = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    float s[32];
+    tmem_ld32(ts + 32 * i, s);
+    wait_ld();
+    loaded<32>(s);
+    const float4 s0 = scale[2 * i], s1 = scale[2 * i + 1];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float y = (e >> 2) & 1 ? fmaf(s[e], s1.x * rk, s1.y) : fmaf(s[e], s0.x * rk, s0.y);
+      tm = fmaxf(tm, kPage * (2 * i + ((e >> 2) & 1)) + col_token(e) < seen ? y : -INFINITY);
+    }
+  }
+  return tm;
+}
+__device__ __noinline__ float weights_masked(uint32_t ts, const float4* scale, float rk, float base, int seen) {
+  float l = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    float s[32];
+    tmem_ld32(ts + 32 * i, s);
+    wait_ld();
+    loaded<32>(s);
+    const float4 s0 = scale[2 * i], s1 = scale[2 * i + 1];
+    float sum[2] = {0.f, 0.f};
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const int par = (e >> 2) & 1;
+      float p[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float y = par ? fmaf(s[e + h], s1.x * rk, s1.y + base) : fmaf(s[e + h], s0.x * rk, s0.y + base);
+        p[h] = kPage * (2 * i + par) + col_token(e + h) < seen ? ex2(y) : 0.f;
+        sum[par] += p[h];
+      }
+      pk[e >> 1] = dec::pack_f16(p[0], p[1]);
+    }
+    l = fmaf(sum[0], s0.z, fmaf(sum[1], s1.z, l));
+    tmem_st16(ts + 16 * i, pk);
+  }
+  return l;
+}
+// O times alpha, row by row.
+__device__ __noinline__ void rescale_o(uint32_t to, float alpha) {
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    float o[32];
+    tmem_ld32(to + 32 * i, o);
+    wait_ld();
+    loaded<32>(o);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] *= alpha;
+    tmem_st16(to + 32 * i, reinterpret_cast<const uint32_t*>(o));
+    tmem_st16(to + 32 * i + 16, reinterpret_cast<const uint32_t*>(o) + 16);
+  }
+}
+// This thread's row of the unit: its query times a power of two in shared memory, the factor returned.
+__device__ __noinline__ float stage_query(const uint16_t* src_row, bool valid, float sm_scale, uint8_t* qs, int row) {
+  const uint4* src = reinterpret_cast<const uint4*>(src_row);
+  uint4 w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max((u[e] >> 7) & 0xFFu, (u[e] >> 23) & 0xFFu));  // largest exponent field
+  }
+  // largest element in [2^8, 2^9): bf16 elements are then exact in fp16 down to 2^-22 of it
+  const int er = min(max(static_cast<int>(top) - 127 - 8, -100), 120);
+  const float f = copysignf(exp2_int(-er), sm_scale);  // a negative scale goes into the query
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      h[e] = dec::pack_f16(__uint_as_float(u[e] << 16) * f, __uint_as_float(u[e] & 0xFFFF0000u) * f);
+    *reinterpret_cast<uint4*>(qs + (i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  dec::fence_proxy_async();
+  return exp2_int(er);
+}
+// The row's O, divided and rounded, to the output.
+__device__ __noinline__ void store_out(uint32_t to, float inv, uint16_t* dst_row, bool valid) {
+  uint4* dst = reinterpret_cast<uint4*>(dst_row);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    float o[32];
+    tmem_ld32(to + 32 * i, o);
+    wait_ld();
+    loaded<32>(o);
+    if (valid) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        dst[4 * i + e] = make_uint4(dec::pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), dec::pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                    dec::pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), dec::pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+    }
+  }
+}
+// The row's O as it is, for the merge.
+__device__ __noinline__ void store_piece(uint32_t to, float* dst_row) {
+  float4* dst = reinterpret_cast<float4*>(dst_row);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    float o[32];
+    tmem_ld32(to + 32 * i, o);
+    wait_ld();
+    loaded<32>(o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dst[8 * i + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+  }
+}
+
 __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = warp >> 2;
   const int row = (warp & 3) * 32 + lane;  // of the half
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp & 3)
   const uint32_t ts = tmem + kTmemS + 128 * half + lanes, to = tmem + kTmemO + 128 * half + lanes;
-  uint8_t* qs = smem + kOffQ + half * kOperand + row * 128;
   Cursor c;
   c.begin(a, t);
   uint32_t s_phase = 0, pv_phase = 0;  // pv_phase: parity of the next PV to complete
   float m = -INFINITY, l = 0.f, rk = 1.f;
-  int limit = 0;
+  int limit = 0;         // tokens that the row sees; 0 for a row past the run's last
+  long long out_at = 0;  // row and head of the output
+  bool valid = false, begins = false;
   const int total = c.left;
-  int head = 0;
-  long long out_row = 0;
-  bool valid = false;
-  int piece_j0 = 0;
   for (int jj = 0; jj < total; ++jj, c.advance(a)) {
-    if (half >= c.halves(a)) continue;
+    if (half >= halves_of(a, c.at)) continue;
     if (c.first) {
-      // ---- the unit's query row, times a power of two, to shared memory
-      const int r = c.u * kRows + half * 128 + row;
-      valid = r < c.run.n * a.G;
-      const int tok = valid ? r / a.G : 0;
-      head = c.kvh * a.G + (valid ? r % a.G : 0);
-      out_row = c.run.row0 + tok;
-      limit = valid ? min(max(c.run.len - c.run.n + tok + 1, 0), c.run.len) : 0;
-      piece_j0 = c.j;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + out_row * a.q_stride + head * kHeadDim);
-      uint4 w[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, max((u[e] >> 7) & 0xFFu, (u[e] >> 23) & 0xFFu));  // largest exponent field
-      }
-      // largest element in [2^8, 2^9): bf16 elements are then exact in fp16 down to 2^-22 of it
-      const int er = min(max(static_cast<int>(top) - 127 - 8, -100), 120);
-      const float f = copysignf(exp2_int(-er), a.sm_scale);  // a negative scale goes into the query
-      rk = exp2_int(er);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          h[e] = dec::pack_f16(__uint_as_float(u[e] << 16) * f, __uint_as_float(u[e] & 0xFFFF0000u) * f);
-        *reinterpret_cast<uint4*>(qs + (i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-      }
-      dec::fence_proxy_async();
+      const int r = c.at.u * kRows + half * 128 + row;
+      valid = r < c.at.run.n * a.G;
+      const int tok = valid ? r / a.G : 0, head = c.at.kvh * a.G + (valid ? r - tok * a.G : 0);
+      const long long out_row = c.at.run.row0 + tok;
+      out_at = out_row * a.Hq + head;
+      limit = valid ? max(c.at.run.len - c.at.run.n + tok + 1, 0) : 0;
+      begins = c.j == 0;
+      rk = stage_query(static_cast<const uint16_t*>(a.q) + out_row * a.q_stride + head * kHeadDim, valid, a.sm_scale,
+                       smem + kOffQ + half * kOperand + row * 128, row);
       __syncwarp();
       if (lane == 0) arrive(&t->q_full[half]);
       m = -INFINITY;
@@ -532,131 +714,40 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     }
     if (!wait_warp(&t->s_full[half], s_phase, &t->abort)) return;
     s_phase ^= 1u;
-    __syncwarp();
     fence_after();
-    float s[128];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
-    wait_ld();
-    loaded<128>(s);
     const float4* scale = t->scale[jj % kScaleSlots];
-    const int t0 = c.j * kKeys;
-    const bool masked = __any_sync(dec::kFull, limit < t0 + kKeys);
-    float tm = -INFINITY;
-    if (masked) {  // the logits themselves, so that hidden ones are -inf whatever the scale
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const float4 sp = scale[p];
-        const float k = sp.x * rk;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int col = 32 * (p >> 1) + 8 * (e >> 2) + 4 * (p & 1) + (e & 3);
-          const int pos = t0 + p * kPage + col_token(col & 31);
-          const float y = fmaf(s[col], k, sp.y);
-          s[col] = pos < limit ? y : -INFINITY;
-          tm = fmaxf(tm, s[col]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        float pm = s[32 * (p >> 1) + 4 * (p & 1)];
-#pragma unroll
-        for (int e = 1; e < 16; ++e) pm = fmaxf(pm, s[32 * (p >> 1) + 8 * (e >> 2) + 4 * (p & 1) + (e & 3)]);
-        tm = fmaxf(tm, fmaf(pm, scale[p].x * rk, scale[p].y));
-      }
-    }
+    const int seen = limit - c.j * kKeys;
+    const bool masked = __any_sync(dec::kFull, seen < kKeys);
+    const float tm = masked ? row_max_masked(ts, scale, rk, seen) : row_max(ts, scale, rk);
     if (c.first) {
       m = tm;
     } else {
       const bool move = tm > m + kSlack || (m == -INFINITY && tm > m);
       if (__any_sync(dec::kFull, move)) {
         if (!wait_warp(&t->pv_done[half], pv_phase ^ 1u, &t->abort)) return;  // O is the previous tiles' sum
-        __syncwarp();
         fence_after();
-        const float mn = move ? tm : m;
-        const float alpha = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - mn);
-        m = mn;
+        const float alpha = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - tm);
+        m = move ? tm : m;
         l *= alpha;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float o[16];
-          uint32_t* ou = reinterpret_cast<uint32_t*>(o);
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-              "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-              : "=r"(ou[0]), "=r"(ou[1]), "=r"(ou[2]), "=r"(ou[3]), "=r"(ou[4]), "=r"(ou[5]), "=r"(ou[6]), "=r"(ou[7]),
-                "=r"(ou[8]), "=r"(ou[9]), "=r"(ou[10]), "=r"(ou[11]), "=r"(ou[12]), "=r"(ou[13]), "=r"(ou[14]), "=r"(ou[15])
-              : "r"(to + 16 * i));
-          wait_ld();
-          loaded<16>(o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= alpha;
-          tmem_st16(to + 16 * i, ou);
-        }
+        rescale_o(to, alpha);
       }
     }
     const float base = kTileShift - (m == -INFINITY ? 0.f : m);
-#pragma unroll
-    for (int cidx = 0; cidx < 4; ++cidx) {
-      uint32_t pk[16];
-      float sum[2] = {0.f, 0.f};
-      const float4 s0 = scale[2 * cidx], s1 = scale[2 * cidx + 1];
-      const float k0 = masked ? 1.f : s0.x * rk, k1 = masked ? 1.f : s1.x * rk;
-      const float b0 = masked ? base : s0.y + base, b1 = masked ? base : s1.y + base;
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const int par = (e >> 2) & 1;
-        const float p0 = ex2(fmaf(s[32 * cidx + e], par ? k1 : k0, par ? b1 : b0));
-        const float p1 = ex2(fmaf(s[32 * cidx + e + 1], par ? k1 : k0, par ? b1 : b0));
-        sum[par] += p0 + p1;
-        pk[e >> 1] = dec::pack_f16(p0, p1);
-      }
-      l = fmaf(sum[0], s0.z, fmaf(sum[1], s1.z, l));
-      tmem_st16(ts + 16 * cidx, pk);
-    }
+    l += masked ? weights_masked(ts, scale, rk, base, seen) : weights(ts, scale, rk, base);
     wait_st();
     fence_before();
     __syncwarp();
     if (lane == 0) arrive(&t->p_full[half]);
     pv_phase ^= 1u;  // this tile's PV is the next to complete
     if (c.last()) {
-      // ---- O of the piece
       if (!wait_warp(&t->pv_done[half], pv_phase ^ 1u, &t->abort)) return;
-      __syncwarp();
       fence_after();
-      const bool whole = piece_j0 == 0 && c.j + 1 == c.tiles;
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (out_row * a.Hq + head) * kHeadDim);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float o[32];
-          tmem_ld32(to + 32 * i, o);
-          wait_ld();
-          loaded<32>(o);
-          if (valid) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[4 * i + e] = make_uint4(dec::pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), dec::pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                          dec::pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), dec::pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-          }
-        }
-        if (a.lse && valid)
-          a.lse[out_row * a.Hq + head] = l == 0.f ? -INFINITY : (m + (log2f(l) - kTileShift)) * dec::kLn2;
+      if (begins && c.j + 1 == c.at.tiles) {
+        store_out(to, l == 0.f ? 0.f : 1.f / l, static_cast<uint16_t*>(a.out) + out_at * kHeadDim, valid);
+        if (a.lse && valid) a.lse[out_at] = l == 0.f ? -INFINITY : (m + (log2f(l) - kTileShift)) * dec::kLn2;
       } else {
-        const size_t slot = 2 * blockIdx.x + (piece_j0 == 0 ? 1 : 0);
-        const size_t at = slot * kRows + half * 128 + row;
-        float4* dst = reinterpret_cast<float4*>(a.tw_acc + at * kHeadDim);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float o[32];
-          tmem_ld32(to + 32 * i, o);
-          wait_ld();
-          loaded<32>(o);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dst[8 * i + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        }
+        const size_t at = static_cast<size_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kRows + half * 128 + row;
+        store_piece(to, a.tw_acc + at * kHeadDim);
         *reinterpret_cast<float2*>(a.tw_stats + at * 2) = make_float2(m, l);
       }
       fence_before();
@@ -667,7 +758,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
 // tw_rec of a CTA: [0] a unit begins here and goes on in the next CTA, [1..3] that unit, [4] the unit that began in an
 // earlier CTA ends here.
 template <bool INT8>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -695,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs a) {
     // which pieces of this CTA the merge has to look at
     Cursor c;
     c.begin(a, t);
-    rec[4] = c.j > 0 && c.j + c.left >= c.tiles;
+    rec[4] = c.j > 0 && c.j + c.left >= c.at.tiles;
     rec[0] = 0;
   }
   if (warp == 12) {
@@ -710,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const AttnArgs a) {
     softmax_role(a, t, smem, tmem);
   } else if (warp < 12) {
     convert_role<INT8>(a, t, smem + kOffRing);
-  } else if ((threadIdx.x & 31) == 0) {
+  } else {
     mma_role(a, t, smem_u32(smem), tmem, rec);
   }
   __syncwarp();
