@@ -13,6 +13,8 @@
 // converting warps), eight warps do the softmax of one half while the tensor core works on the other.
 //
 // Warps: 0-3 softmax of rows 0..127, 4-7 of rows 128..255, 8-11 convert, 12 issues the products.
+// The loops are kept rolled and what happens once a unit is called: all roles' code is live at once, and unrolled
+// (100 KB) it spent most of the time on instruction fetches (2.9 ms on a prompt of 11996 tokens).
 // Shared memory: Q 2 x 32 KB, then a ring of 32 KB slots taking K and V tiles in turn, every operand as 64-element
 // columns of 128-byte rows, 128-byte swizzle (16-byte chunk index ^ row & 7).
 // Key order inside a tile.  The value tiles hold tokens 2q, 2q+1, 2q+8, 2q+9 of a channel in one lane's word.  Two pages'
@@ -37,10 +39,18 @@ constexpr int kScaleSlots = 4;  // a tile's scales are read until its weights ar
 constexpr float kTileShift = 7.f;  // weights are held times 2^7 ..
 constexpr float kSlack = 8.f;      // .. and may grow to 2^15 before the running maximum (and O) is moved
 constexpr int kOffQ = 0, kOffRing = 2 * kOperand, kOffTail = kOffRing + kSlots * kOperand;
-constexpr int kTailBytes = 1024;
+constexpr int kTailBytes = 1536;
 constexpr int kSmemBytes = kOffTail + kTailBytes + 1024;  // + alignment of the base to 1024
 constexpr uint32_t kIdesc = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);  // fp16 x fp16 -> fp32, M = N = 128
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // columns: S (and P) of the two halves, then O
+
+struct RunInfo {
+  int len, n, row0, units;
+};
+struct UnitInfo {
+  int s, kvh, u, tiles;
+  RunInfo run;
+};
 
 struct Tail {  // shared memory behind the operands
   float4 scale[kScaleSlots][kPagesPerTile];  // 2^ek sm_scale log2 e, ev, 2^-ev, 0 (0, -inf, 0 for an absent page)
@@ -48,6 +58,7 @@ struct Tail {  // shared memory behind the operands
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
   uint32_t tmem;
   int abort;
+  UnitInfo unit[kThreads / 32];  // where each warp is
   int start[4];  // request, kv head, unit, first tile of the CTA's range
   long long T;
   int n;
@@ -113,22 +124,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* u) {
       : "memory");
 }
 
-// Bounded wait: false when the phase did not complete within the limit or another role has given up.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort) {
-  const unsigned long long t0 = dec::global_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (dec::mbar_try_wait(bar, parity)) return true;
+// Bounded wait (some seconds of clocks): false when the phase did not complete or another role has given up.
+constexpr long long kWaitClocks = 4000000000ll;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
+  if (dec::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!dec::mbar_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(abort)) return false;
-    if (dec::global_ns() - t0 > dec::kWaitNs) {
+    if (clock64() - t0 > kWaitClocks) {
       *reinterpret_cast<volatile int*>(abort) = 1;
       return false;
     }
   }
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
-  if (dec::mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, abort);
+  return true;
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {  // one verdict for the whole warp
   return __all_sync(dec::kFull, wait(bar, parity, abort));
@@ -138,9 +146,6 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 }
 
 // ------------------------------------------------------------------------------------------------ work
-struct RunInfo {
-  int len, n, row0, units;
-};
 __device__ __forceinline__ RunInfo run_info(const AttnArgs& a, int s) {
   const Run r = load_run(a.run_starts, a.seq_lens, s, a.num_rows, a.max_run, a.max_pages);
   const int rows = r.n * a.G;
@@ -153,49 +158,56 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, const RunInfo& r, int
   return max(1, (limit + kKeys - 1) / kKeys);
 }
 
-// The roles' loops are kept small: what happens once a unit is a call, since code that does not fit the instruction
-// caches cost more than the work itself (131 KB of code in all, 2.20 ms on a prompt of 11996 tokens).
-struct UnitInfo {
-  int s, kvh, u, tiles;
-  RunInfo run;
-};
-__device__ __noinline__ UnitInfo unit_info(const AttnArgs& a, int s, int kvh, int u) {
-  UnitInfo i{s, kvh, u, 0, run_info(a, s)};
-  i.tiles = tiles_of(a, i.run, u);
-  return i;
+__device__ __forceinline__ int halves_of(const AttnArgs& a, const RunInfo& r, int u) { return r.n * a.G - u * kRows > 128 ? 2 : 1; }
+
+// Where a warp is in its CTA's range of tiles.  The unit lives in shared memory: in registers it would be spilled, and
+// with 227 KB of shared memory the L1 that is left loses what is spilled to the L2 (~500 clocks a use).
+__device__ __noinline__ int set_unit(const AttnArgs& a, UnitInfo* at, int s, int kvh, int u) {
+  const RunInfo r = run_info(a, s);
+  const UnitInfo i{s, kvh, u, tiles_of(a, r, u), r};
+  __syncwarp();
+  *at = i;  // every lane the same
+  __syncwarp();
+  return i.tiles << 1 | (halves_of(a, r, u) - 1);
 }
-__device__ __noinline__ UnitInfo next_unit(const AttnArgs& a, int s, int kvh, int u, int units) {
-  if (++u == units) {
-    u = 0;
-    if (++kvh == a.Hkv) {
-      kvh = 0;
-      do ++s; while (run_info(a, s).units == 0);  // called only where a later unit exists
+__device__ __noinline__ int next_unit(const AttnArgs& a, UnitInfo* at) {
+  UnitInfo i = *at;
+  if (++i.u == i.run.units) {
+    i.u = 0;
+    if (++i.kvh == a.Hkv) {
+      i.kvh = 0;
+      do i.run = run_info(a, ++i.s); while (i.run.units == 0);  // called only where a later unit exists
     }
   }
-  return unit_info(a, s, kvh, u);
+  i.tiles = tiles_of(a, i.run, i.u);
+  __syncwarp();
+  *at = i;
+  __syncwarp();
+  return i.tiles << 1 | (halves_of(a, i.run, i.u) - 1);
 }
-
-// Where a role is in its CTA's range of tiles.
 struct Cursor {
-  UnitInfo at;
+  UnitInfo* at;
   int j, left;
+  int shape;   // tiles of the unit << 1 | both halves have rows
   bool first;  // the tile is the first of its piece
-  __device__ __forceinline__ void begin(const AttnArgs& a, const Tail* t) {
-    at = unit_info(a, t->start[0], t->start[1], t->start[2]);
+  __device__ __forceinline__ void begin(const AttnArgs& a, Tail* t) {
+    at = &t->unit[threadIdx.x >> 5];
+    shape = set_unit(a, at, t->start[0], t->start[1], t->start[2]);
     j = t->start[3];
     left = t->n;
     first = true;
   }
-  __device__ __forceinline__ bool last() const { return left == 1 || j + 1 == at.tiles; }
+  __device__ __forceinline__ int tiles() const { return shape >> 1; }
+  __device__ __forceinline__ int halves() const { return 1 + (shape & 1); }
+  __device__ __forceinline__ bool last() const { return left == 1 || j + 1 == tiles(); }
   __device__ __forceinline__ void advance(const AttnArgs& a) {
     first = false;
-    if (--left == 0 || ++j < at.tiles) return;
+    if (--left == 0 || ++j < tiles()) return;
     j = 0;
     first = true;
-    at = next_unit(a, at.s, at.kvh, at.u, at.run.units);
+    shape = next_unit(a, at);
   }
 };
-__device__ __forceinline__ int halves_of(const AttnArgs& a, const UnitInfo& i) { return i.run.n * a.G - i.u * kRows > 128 ? 2 : 1; }
 
 // The CTA's range: the sums over the batch in `cum` (shared memory that the ring takes over later).
 __device__ void plan(const AttnArgs& a, Tail* t, long long* cum) {
@@ -304,6 +316,8 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
     return page * kPage < len ? a.block_table[static_cast<size_t>(s) * a.max_pages + page] : 0;
   };
   auto absent = [&](int entry) { return entry < 0 || entry >= a.num_pages; };
+  const uint32_t page_bytes = a.Hkv * 2048;  // of one plane
+  const uint8_t *k_base = a.k + lane * 16, *v_base = a.v + (cw * 32 + lane) * 16;
   uint4 kr[8], vr[8];
   uint16_t ks = 0, vs = 0;  // lanes 0, 1: scales of the warp's key pages
   // pages 2 cw, 2 cw + 1 of the key tile, words of 512 bytes
@@ -311,7 +325,7 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int p = __shfl_sync(dec::kFull, phys, 2 * cw + i);
-      const uint8_t* src = a.k + ((static_cast<size_t>(p) * a.Hkv + kvh) * 2048 + lane * 16);
+      const uint8_t* src = k_base + kvh * 2048 + static_cast<uint64_t>(static_cast<uint32_t>(p)) * page_bytes;
 #pragma unroll
       for (int w = 0; w < 4; ++w) kr[4 * i + w] = ldg_codes(src + w * 512);
     }
@@ -327,7 +341,7 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int p = __shfl_sync(dec::kFull, phys, i ^ (2 * (g & 1)));
-      vr[i] = ldg_codes(a.v + ((static_cast<size_t>(p) * a.Hkv + kvh) * 2048 + (cw * 32 + lane) * 16));
+      vr[i] = ldg_codes(v_base + kvh * 2048 + static_cast<uint64_t>(static_cast<uint32_t>(p)) * page_bytes);
     }
   };
   int slot = 0;
@@ -341,26 +355,20 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
   // this lane's rows and chunks: token 8 h + g of page p goes to row 32 (p >> 1) + 8 (g >> 1) + 4 (p & 1) + 2 h + (g & 1)
   const int k_row = 32 * cw + 8 * (g >> 1) + (g & 1);
   const int v_row = 32 * cw + g;
-  int entry = load_entry(c.at.s, c.j, c.at.run.len), entry_next = 0;
+  int entry = load_entry(c.at->s, c.j, c.at->run.len), entry_next = 0;
   int phys = absent(entry) ? 0 : entry;
-  load_k(c.at.kvh, phys);
+  load_k(c.at->kvh, phys);
   for (int jj = 0; jj < total; ++jj) {
-    const int in_context = c.at.run.len - c.j * kKeys;  // tokens of the tile that the context has
+    const int in_context = c.at->run.len - c.j * kKeys;  // tokens of the tile that the context has
     const bool here = (lane & 7) * kPage < in_context;
     const unsigned lost = __ballot_sync(dec::kFull, !here || absent(entry));  // bits 0..7: absent pages
     if (here && absent(entry) && cw == 0 && lane < 8) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
-    load_v(c.at.kvh, phys);
+    load_v(c.at->kvh, phys);
     // the next tile's table entries
     const bool more = jj + 1 < total;
     c.advance(a);
-    if (more) entry_next = load_entry(c.at.s, c.j, c.at.run.len);
+    if (more) entry_next = load_entry(c.at->s, c.j, c.at->run.len);
     if (!wait_warp(&t->empty[slot], phase ^ 1u, &t->abort)) return;
-    if (lane < 2) {
-      const int ek = f16_to_exp(ks), ev = f16_to_exp(vs);
-      t->scale[jj % kScaleSlots][2 * cw + lane] =
-          (lost >> (2 * cw + lane)) & 1u ? make_float4(0.f, -INFINITY, 0.f, 0.f)
-                                         : make_float4(fabsf(a.sm_scale) * dec::kLog2e * exp2_int(ek), static_cast<float>(ev), exp2_int(-ev), 0.f);
-    }
     uint8_t* dst = ring + slot * kOperand + k_row * 128;
     if (lost & 0xFFu) {
 #pragma unroll
@@ -377,11 +385,17 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
       *reinterpret_cast<uint4*>(base + (((2 * q + 1) ^ (dr | (g & 1))) << 4)) =
           make_uint4(cvt_lo<INT8>(x.z), cvt_hi<INT8>(x.z), cvt_lo<INT8>(x.w), cvt_hi<INT8>(x.w));
     }
+    if (lane < 2) {
+      const int ek = f16_to_exp(ks), ev = f16_to_exp(vs);
+      t->scale[jj % kScaleSlots][2 * cw + lane] =
+          (lost >> (2 * cw + lane)) & 1u ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                                         : make_float4(fabsf(a.sm_scale) * dec::kLog2e * exp2_int(ek), static_cast<float>(ev), exp2_int(-ev), 0.f);
+    }
     publish();
     if (more) {
       entry = entry_next;
       phys = absent(entry) ? 0 : entry;
-      load_k(c.at.kvh, phys);
+      load_k(c.at->kvh, phys);
     }
     if (!wait_warp(&t->empty[slot], phase ^ 1u, &t->abort)) return;
     if (in_context < kKeys || (lost & 0xFFu)) {  // what lies behind the context may be anything, a NaN too
@@ -427,18 +441,26 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
   tmem = dec::uniform_u32(tmem);
   const uint64_t ring = smem_desc(smem_base + kOffRing);
   const uint64_t qd = smem_desc(smem_base + kOffQ);
-  auto k_step = [](int ks) { return static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4); };
+  // eight steps of 16: 32 bytes apart inside a 64-element column of rows, the second column 16 KB on
   auto qk = [&](int i, int slot) {
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-      mma_ss(tmem + kTmemS + 128 * i, qd + static_cast<uint64_t>(i * (kOperand >> 4)) + k_step(ks),
-             ring + static_cast<uint64_t>(slot * (kOperand >> 4)) + k_step(ks), ks > 0, leader);
+    uint64_t x = qd + static_cast<uint64_t>(i * (kOperand >> 4)), y = ring + static_cast<uint64_t>(slot * (kOperand >> 4));
+#pragma unroll 1
+    for (int ks = 0; ks < 8; ++ks) {
+      mma_ss(tmem + kTmemS + 128 * i, x, y, ks > 0, leader);
+      const uint64_t d = ks == 3 ? (16384 - 96) >> 4 : 32 >> 4;
+      x += d;
+      y += d;
+    }
   };
   auto pv = [&](int i, int slot, bool acc) {
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-      mma_ts(tmem + kTmemO + 128 * i, tmem + kTmemS + 128 * i + 8 * ks,
-             ring + static_cast<uint64_t>(slot * (kOperand >> 4)) + k_step(ks), acc || ks > 0, leader);
+    uint32_t x = tmem + kTmemS + 128 * i;
+    uint64_t y = ring + static_cast<uint64_t>(slot * (kOperand >> 4));
+#pragma unroll 1
+    for (int ks = 0; ks < 8; ++ks) {
+      mma_ts(tmem + kTmemO + 128 * i, x, y, acc || ks > 0, leader);
+      x += 8;
+      y += ks == 3 ? (16384 - 96) >> 4 : 32 >> 4;
+    }
   };
   int slot = 0;  // of the operand tile taken next
   uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
@@ -449,12 +471,12 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
   bool have_s = false;  // the current tile's S products are issued
   int from = 0;         // first tile of the current piece
   for (int jj = 0; jj < total; ++jj) {
-    const int nh = halves_of(a, c.at);
+    const int nh = c.halves();
     if (c.first) from = c.j;
-    if (leader && jj == total - 1 && from == 0 && c.j + 1 < c.at.tiles) {  // the unit began here and goes on in the next CTA
-      rec[1] = c.at.s;
-      rec[2] = c.at.kvh;
-      rec[3] = c.at.u;
+    if (leader && jj == total - 1 && from == 0 && c.j + 1 < c.tiles()) {  // the unit began here and goes on in the next CTA
+      rec[1] = c.at->s;
+      rec[2] = c.at->kvh;
+      rec[3] = c.at->u;
       rec[0] = 1;
     }
     if (!have_s) {  // first tile of a piece
@@ -499,65 +521,71 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
 // Column k of a 32-column chunk: page parity (k >> 2) & 1, token of the page.
 __device__ __forceinline__ constexpr int col_token(int k) { return 2 * (k >> 3) + (k & 1) + 8 * ((k >> 1) & 1); }
 
-// The row's softmax goes over S in TMEM twice, 32 columns at a time with the next ones on their way: the maximum, then the
-// weights.  (All 128 values in registers instead: 184 registers do not hold them with the rest, and what spills costs far
-// more than reading S again: 3.00 -> 2.76 ms on a prompt of 11996 tokens.)  Pages 2 i and 2 i + 1 lie in chunk i, their
-// columns in groups of four.  y = x log2 e + ev = S k + ev; since k >= 0 a page's largest S gives its largest y.
+// The row's softmax goes over S in TMEM twice: the maximum, then the weights, 64 columns at a time.  Pages 2 i and 2 i + 1
+// lie in columns 32 i .. 32 i + 31, in groups of four.  y = x log2 e + ev = S k + ev; since k >= 0 a page's largest S gives
+// its largest y.
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float chunk_max(const float* s, const float4* sc, float rk, float tm) {
+  float pm[2];
+#pragma unroll
+  for (int par = 0; par < 2; ++par) {
+    const float* x = s + 4 * par;  // columns 0..3, 8..11, 16..19, 24..27 from here
+    const float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[8], x[9]), m2 = max3(x[10], x[11], x[16]);
+    const float m3 = max3(x[17], x[18], x[19]), m4 = max3(x[24], x[25], x[26]);
+    pm[par] = fmaxf(max3(m0, m1, m2), max3(m3, m4, x[27]));
+  }
+  const float4 s0 = sc[0], s1 = sc[1];
+  return max3(tm, fmaf(pm[0], s0.x * rk, s0.y), fmaf(pm[1], s1.x * rk, s1.y));
+}
 __device__ __forceinline__ float row_max(uint32_t ts, const float4* scale, float rk) {
   float tm = -INFINITY;
-  float sb[2][32];
-  tmem_ld32(ts, sb[0]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float* s = sb[i & 1];
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    float s[64];
+    tmem_ld32(ts + 64 * i, s);
+    tmem_ld32(ts + 64 * i + 32, s + 32);
     wait_ld();
-    loaded<32>(s);
-    if (i < 3) tmem_ld32(ts + 32 * (i + 1), sb[(i + 1) & 1]);
-    float pm[2];
-#pragma unroll
-    for (int par = 0; par < 2; ++par) {
-      const float* x = s + 4 * par;  // columns 0..3, 8..11, 16..19, 24..27 from here
-      const float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[8], x[9]), m2 = max3(x[10], x[11], x[16]);
-      const float m3 = max3(x[17], x[18], x[19]), m4 = max3(x[24], x[25], x[26]);
-      pm[par] = fmaxf(max3(m0, m1, m2), max3(m3, m4, x[27]));
-    }
-    const float4 s0 = scale[2 * i], s1 = scale[2 * i + 1];
-    tm = max3(tm, fmaf(pm[0], s0.x * rk, s0.y), fmaf(pm[1], s1.x * rk, s1.y));
+    loaded<64>(s);
+    tm = chunk_max(s, scale + 4 * i, rk, tm);
+    tm = chunk_max(s + 32, scale + 4 * i + 2, rk, tm);
   }
   return tm;
 }
 // Weights 2^{y + base} as fp16 pairs over the columns that S leaves free, and their sum without the value scales.
+__device__ __forceinline__ float chunk_weights(const float* s, const float4* sc, float rk, float base, uint32_t* pk) {
+  const float4 s0 = sc[0], s1 = sc[1];
+  const dec::f2x k2[2] = {dec::f2_splat(s0.x * rk), dec::f2_splat(s1.x * rk)};
+  const dec::f2x b2[2] = {dec::f2_splat(s0.y + base), dec::f2_splat(s1.y + base)};
+  dec::f2x sum[2];
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const int par = (e >> 2) & 1;
+    float y0, y1;
+    dec::f2_unpack(dec::f2_fma(dec::f2_pack(s[e], s[e + 1]), k2[par], b2[par]), y0, y1);
+    const float p0 = ex2(y0), p1 = ex2(y1);
+    const dec::f2x p2 = dec::f2_pack(p0, p1);
+    sum[par] = (e & ~4) == 0 ? p2 : dec::f2_add(sum[par], p2);
+    pk[e >> 1] = dec::pack_f16(p0, p1);
+  }
+  float l0, l1, l2, l3;
+  dec::f2_unpack(sum[0], l0, l1);
+  dec::f2_unpack(sum[1], l2, l3);
+  return fmaf(l0 + l1, s0.z, (l2 + l3) * s1.z);
+}
 __device__ __forceinline__ float weights(uint32_t ts, const float4* scale, float rk, float base) {
   float l = 0.f;
-  float sb[2][32];
-  tmem_ld32(ts, sb[0]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float* s = sb[i & 1];
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    float s[64];
+    uint32_t pk[32];
+    tmem_ld32(ts + 64 * i, s);
+    tmem_ld32(ts + 64 * i + 32, s + 32);
     wait_ld();
-    loaded<32>(s);
-    if (i < 3) tmem_ld32(ts + 32 * (i + 1), sb[(i + 1) & 1]);
-    const float4 s0 = scale[2 * i], s1 = scale[2 * i + 1];
-    const dec::f2x k2[2] = {dec::f2_splat(s0.x * rk), dec::f2_splat(s1.x * rk)};
-    const dec::f2x b2[2] = {dec::f2_splat(s0.y + base), dec::f2_splat(s1.y + base)};
-    dec::f2x sum[2];
-    uint32_t pk[16];
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const int par = (e >> 2) & 1;
-      float y0, y1;
-      dec::f2_unpack(dec::f2_fma(dec::f2_pack(s[e], s[e + 1]), k2[par], b2[par]), y0, y1);
-      const float p0 = ex2(y0), p1 = ex2(y1);
-      const dec::f2x p2 = dec::f2_pack(p0, p1);
-      sum[par] = (e & ~4) == 0 ? p2 : dec::f2_add(sum[par], p2);
-      pk[e >> 1] = dec::pack_f16(p0, p1);
-    }
-    tmem_st16(ts + 16 * i, pk);
-    float l0, l1, l2, l3;
-    dec::f2_unpack(sum[0], l0, l1);
-    dec::f2_unpack(sum[1], l2, l3);
-    l = fmaf(l0 + l1, s0.z, fmaf(l2 + l3, s1.z, l));
+    loaded<64>(s);
+    l += chunk_weights(s, scale + 4 * i, rk, base, pk);
+    l += chunk_weights(s + 32, scale + 4 * i + 2, rk, base, pk + 16);
+    tmem_st16(ts + 32 * i, pk);
+    tmem_st16(ts + 32 * i + 16, pk + 16);
   }
   return l;
 }
@@ -681,6 +709,7 @@ __device__ __noinline__ void store_piece(uint32_t to, float* dst_row) {
   }
 }
 
+// At the end of a unit the next one's query is staged, so that its first S is issued, before O is stored.
 __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = warp >> 2;
@@ -689,29 +718,42 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
   const uint32_t ts = tmem + kTmemS + 128 * half + lanes, to = tmem + kTmemO + 128 * half + lanes;
   Cursor c;
   c.begin(a, t);
-  uint32_t s_phase = 0, pv_phase = 0;  // pv_phase: parity of the next PV to complete
-  float m = -INFINITY, l = 0.f, rk = 1.f;
-  int limit = 0;         // tokens that the row sees; 0 for a row past the run's last
-  long long out_at = 0;  // row and head of the output
-  bool valid = false, begins = false;
   const int total = c.left;
-  for (int jj = 0; jj < total; ++jj, c.advance(a)) {
-    if (half >= halves_of(a, c.at)) continue;
-    if (c.first) {
-      const int r = c.at.u * kRows + half * 128 + row;
-      valid = r < c.at.run.n * a.G;
-      const int tok = valid ? r / a.G : 0, head = c.at.kvh * a.G + (valid ? r - tok * a.G : 0);
-      const long long out_row = c.at.run.row0 + tok;
-      out_at = out_row * a.Hq + head;
-      limit = valid ? max(c.at.run.len - c.at.run.n + tok + 1, 0) : 0;
-      begins = c.j == 0;
-      rk = stage_query(static_cast<const uint16_t*>(a.q) + out_row * a.q_stride + head * kHeadDim, valid, a.sm_scale,
-                       smem + kOffQ + half * kOperand + row * 128, row);
-      __syncwarp();
-      if (lane == 0) arrive(&t->q_full[half]);
-      m = -INFINITY;
-      l = 0.f;
+  uint32_t s_phase = 0, pv_phase = 0;  // parities of the next completion of s_full and of pv_done
+  float m = -INFINITY, l = 0.f, rk = 1.f;
+  int limit = 0;  // tokens that the row sees; 0 for a row past the run's last
+  bool begins = false, staged = false;
+  auto locate = [&](bool& valid, int& tok, long long& out_at) {  // this thread's row of the unit
+    const UnitInfo u = *c.at;
+    const int r = u.u * kRows + half * 128 + row;
+    valid = r < u.run.n * a.G;
+    tok = valid ? r / a.G : 0;
+    out_at = static_cast<long long>(u.run.row0 + tok) * a.Hq + u.kvh * a.G + (valid ? r - tok * a.G : 0);
+  };
+  auto begin_unit = [&]() {
+    bool valid;
+    int tok;
+    long long out_at;
+    locate(valid, tok, out_at);
+    const RunInfo run = c.at->run;
+    limit = valid ? max(run.len - run.n + tok + 1, 0) : 0;
+    begins = c.j == 0;
+    m = -INFINITY;
+    l = 0.f;
+    const long long row_at = static_cast<long long>(run.row0 + tok);
+    rk = stage_query(static_cast<const uint16_t*>(a.q) + row_at * a.q_stride + (out_at - row_at * a.Hq) * kHeadDim, valid, a.sm_scale,
+                     smem + kOffQ + half * kOperand + row * 128, row);
+    __syncwarp();
+    if (lane == 0) arrive(&t->q_full[half]);
+    staged = true;
+  };
+#pragma unroll 1
+  for (int jj = 0; jj < total; ++jj) {
+    if (half >= c.halves()) {  // 128 rows or fewer: the other half's alone
+      c.advance(a);
+      continue;
     }
+    if (!staged) begin_unit();
     if (!wait_warp(&t->s_full[half], s_phase, &t->abort)) return;
     s_phase ^= 1u;
     fence_after();
@@ -721,7 +763,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     const float tm = masked ? row_max_masked(ts, scale, rk, seen) : row_max(ts, scale, rk);
     if (c.first) {
       m = tm;
-    } else {
+    } else {  // the running maximum moves only when a row outgrows it by 2^kSlack
       const bool move = tm > m + kSlack || (m == -INFINITY && tm > m);
       if (__any_sync(dec::kFull, move)) {
         if (!wait_warp(&t->pv_done[half], pv_phase ^ 1u, &t->abort)) return;  // O is the previous tiles' sum
@@ -738,20 +780,32 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     fence_before();
     __syncwarp();
     if (lane == 0) arrive(&t->p_full[half]);
-    pv_phase ^= 1u;  // this tile's PV is the next to complete
-    if (c.last()) {
-      if (!wait_warp(&t->pv_done[half], pv_phase ^ 1u, &t->abort)) return;
-      fence_after();
-      if (begins && c.j + 1 == c.at.tiles) {
-        store_out(to, l == 0.f ? 0.f : 1.f / l, static_cast<uint16_t*>(a.out) + out_at * kHeadDim, valid);
-        if (a.lse && valid) a.lse[out_at] = l == 0.f ? -INFINITY : (m + (log2f(l) - kTileShift)) * dec::kLn2;
-      } else {
-        const size_t at = static_cast<size_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kRows + half * 128 + row;
-        store_piece(to, a.tw_acc + at * kHeadDim);
-        *reinterpret_cast<float2*>(a.tw_stats + at * 2) = make_float2(m, l);
-      }
-      fence_before();
+    const uint32_t parity = pv_phase;  // of this tile's PV
+    pv_phase ^= 1u;
+    if (!c.last()) {
+      c.advance(a);
+      continue;
     }
+    const bool whole = begins && c.j + 1 == c.tiles();
+    const float m0 = m, l0 = l;
+    const size_t piece = static_cast<size_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kRows + half * 128 + row;
+    bool valid;
+    int tok;
+    long long out_at;
+    locate(valid, tok, out_at);
+    c.advance(a);
+    staged = false;
+    if (jj + 1 < total && half < c.halves()) begin_unit();
+    if (!wait_warp(&t->pv_done[half], parity, &t->abort)) return;
+    fence_after();
+    if (whole) {
+      store_out(to, l0 == 0.f ? 0.f : 1.f / l0, static_cast<uint16_t*>(a.out) + out_at * kHeadDim, valid);
+      if (a.lse && valid) a.lse[out_at] = l0 == 0.f ? -INFINITY : (m0 + (log2f(l0) - kTileShift)) * dec::kLn2;
+    } else {
+      store_piece(to, a.tw_acc + piece * kHeadDim);
+      *reinterpret_cast<float2*>(a.tw_stats + piece * 2) = make_float2(m0, l0);
+    }
+    fence_before();
   }
 }
 
@@ -784,9 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
     dec::fence_mbar_init();
     // which pieces of this CTA the merge has to look at
-    Cursor c;
-    c.begin(a, t);
-    rec[4] = c.j > 0 && c.j + c.left >= c.at.tiles;
+    const int first_tiles = tiles_of(a, run_info(a, t->start[0]), t->start[2]);
+    rec[4] = t->start[3] > 0 && t->start[3] + t->n >= first_tiles;
     rec[0] = 0;
   }
   if (warp == 12) {
@@ -797,13 +850,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   __syncthreads();
   fence_after();
   const uint32_t tmem = t->tmem;
-  if (warp < 8) {
-    softmax_role(a, t, smem, tmem);
-  } else if (warp < 12) {
-    convert_role<INT8>(a, t, smem + kOffRing);
-  } else {
-    mma_role(a, t, smem_u32(smem), tmem, rec);
-  }
+  if (warp < 8) softmax_role(a, t, smem, tmem);
+  else if (warp < 12) convert_role<INT8>(a, t, smem + kOffRing);
+  else mma_role(a, t, smem_u32(smem), tmem, rec);
   __syncwarp();
   fence_before();
   __syncthreads();
