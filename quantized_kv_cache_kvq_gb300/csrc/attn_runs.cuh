@@ -45,7 +45,8 @@ struct AttnArgs {
   float* tw_acc;    // [2 w][256][128]
   float* tw_stats;  // [2 w][256][2]
   int32_t* tw_rec;  // [w][8]
-  int tile_ctas, tile_min;  // CTAs, and the fewest tiles that are worth one
+  int tile_ctas;            // CTAs
+  int tile_min, unit_cost;  // the least cost that is worth a CTA; what a unit costs beside its tiles, in tiles
   int32_t* err;
 };
 

@@ -12,7 +12,8 @@
 // SM is kept below that: the codes go from global memory through registers to shared memory once for all 256 rows (four
 // converting warps), eight warps do the softmax of one half while the tensor core works on the other.
 //
-// Warps: 0-3 softmax of rows 0..127, 4-7 of rows 128..255, 8-11 convert, 12 issues the products.
+// Warps: 0-15 softmax (0-3 rows 0..127 and keys 0..63 of a tile, 4-7 rows 128..255, 8-15 the same rows and keys 64..127),
+// 16-19 convert, 20 issues the products.
 // The loops are kept rolled and what happens once a unit is called: all roles' code is live at once, and unrolled
 // (100 KB) it spent most of the time on instruction fetches (2.9 ms on a prompt of 11996 tokens).
 // Shared memory: Q 2 x 32 KB, then a ring of 32 KB slots taking K and V tiles in turn, every operand as 64-element
@@ -20,6 +21,7 @@
 // Key order inside a tile.  The value tiles hold tokens 2q, 2q+1, 2q+8, 2q+9 of a channel in one lane's word.  Two pages'
 // such words make one 16-byte chunk of the V operand, so key column 32 (p >> 1) + 8 q + 4 (p & 1) + i stands for token
 // 2 q + (i & 1) + 8 (i >> 1) of page p: K rows are placed accordingly and P's columns follow.
+#include <cstdlib>
 #include "attn_runs.cuh"
 
 namespace kvq {
@@ -34,13 +36,18 @@ constexpr int kKeys = 128;      // keys of a tile
 constexpr int kPagesPerTile = kKeys / kPage;
 constexpr int kSlots = 5;       // ring of operand tiles
 constexpr int kOperand = 32768;  // 128 x 128 fp16
-constexpr int kThreads = 13 * 32;
-constexpr int kScaleSlots = 4;  // a tile's scales are read until its weights are written, two tiles before slot reuse
+constexpr int kSoftmaxWarps = 16, kConvertWarp = 16, kMmaWarp = 20;  // first warps of the roles
+constexpr int kThreads = 24 * 32;
+// Registers: 80 a thread at launch; the converting warps, which hold two operand tiles in flight, take what the last
+// warpgroup (one warp of it issues the products) gives up.
+constexpr int kRegsConvert = 104, kRegsMma = 56;
+static_assert(16 * 80 + 4 * kRegsConvert + 4 * kRegsMma <= 24 * 80, "no more than the block was launched with");
+constexpr int kScaleSlots = 3;  // a tile's scales are read until its V slot is free, which the K of the third next tile waits for
 constexpr float kTileShift = 7.f;  // weights are held times 2^7 ..
 constexpr float kSlack = 8.f;      // .. and may grow to 2^15 before the running maximum (and O) is moved
 constexpr int kOffQ = 0, kOffRing = 2 * kOperand, kOffTail = kOffRing + kSlots * kOperand;
-constexpr int kTailBytes = 1536;
-constexpr int kSmemBytes = kOffTail + kTailBytes + 1024;  // + alignment of the base to 1024
+constexpr int kTailBytes = 3072;
+constexpr int kSmemBytes = kOffTail + kTailBytes;
 constexpr uint32_t kIdesc = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);  // fp16 x fp16 -> fp32, M = N = 128
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // columns: S (and P) of the two halves, then O
 
@@ -48,20 +55,20 @@ struct RunInfo {
   int len, n, row0, units;
 };
 struct UnitInfo {
-  int s, kvh, u, tiles;
+  int s, kvh, u;
   RunInfo run;
 };
 
 struct Tail {  // shared memory behind the operands
-  float4 scale[kScaleSlots][kPagesPerTile];  // 2^ek sm_scale log2 e, ev, 2^-ev, 0 (0, -inf, 0 for an absent page)
+  float2 scale[kScaleSlots][kPagesPerTile];  // 2^ek sm_scale log2 e, ev (0, -inf for an absent page)
+  float peer[kSoftmaxWarps][32];  // what the two warps of a row tell each other
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
   uint32_t tmem;
   int abort;
-  UnitInfo unit[kThreads / 32];  // where each warp is
+  UnitInfo unit[kMmaWarp + 1];  // where each warp is
   int start[4];  // request, kv head, unit, first tile of the CTA's range
-  long long T;
-  int n;
+  int n;         // its tiles
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
 
@@ -162,15 +169,15 @@ __device__ __forceinline__ int halves_of(const AttnArgs& a, const RunInfo& r, in
 
 // Where a warp is in its CTA's range of tiles.  The unit lives in shared memory: in registers it would be spilled, and
 // with 227 KB of shared memory the L1 that is left loses what is spilled to the L2 (~500 clocks a use).
-__device__ __noinline__ int set_unit(const AttnArgs& a, UnitInfo* at, int s, int kvh, int u) {
+__device__ __forceinline__ int set_unit(const AttnArgs& a, UnitInfo* at, int s, int kvh, int u) {
   const RunInfo r = run_info(a, s);
-  const UnitInfo i{s, kvh, u, tiles_of(a, r, u), r};
+  const UnitInfo i{s, kvh, u, r};
   __syncwarp();
   *at = i;  // every lane the same
   __syncwarp();
-  return i.tiles << 1 | (halves_of(a, r, u) - 1);
+  return tiles_of(a, r, u) << 1 | (halves_of(a, r, u) - 1);
 }
-__device__ __noinline__ int next_unit(const AttnArgs& a, UnitInfo* at) {
+__device__ __forceinline__ int next_unit(const AttnArgs& a, UnitInfo* at) {
   UnitInfo i = *at;
   if (++i.u == i.run.units) {
     i.u = 0;
@@ -179,11 +186,10 @@ __device__ __noinline__ int next_unit(const AttnArgs& a, UnitInfo* at) {
       do i.run = run_info(a, ++i.s); while (i.run.units == 0);  // called only where a later unit exists
     }
   }
-  i.tiles = tiles_of(a, i.run, i.u);
   __syncwarp();
   *at = i;
   __syncwarp();
-  return i.tiles << 1 | (halves_of(a, i.run, i.u) - 1);
+  return tiles_of(a, i.run, i.u) << 1 | (halves_of(a, i.run, i.u) - 1);
 }
 struct Cursor {
   UnitInfo* at;
@@ -209,78 +215,97 @@ struct Cursor {
   }
 };
 
-// The CTA's range: the sums over the batch in `cum` (shared memory that the ring takes over later).
-__device__ void plan(const AttnArgs& a, Tail* t, long long* cum) {
+// The CTA's range.  A unit costs its tiles and kUnitCost more (its query, the first S that nothing overlaps, its output), so
+// ranges are equal in tiles + kUnitCost units (kUnitCost: see launch_tile); a cut inside a unit's extra cost is a cut before
+// its first tile.
+struct Place {
+  int s, kvh, u, j;
+  long long tile;  // tiles before it
+};
+// Where x lies; all lanes of a warp.  cum[s], units[s]: cost and units of one kv head of the runs before s.
+__device__ Place find_place(const AttnArgs& a, const long long* cum, const int* units, long long x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = a.batch - 1;  // first s with Hkv cum[s + 1] > x
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.Hkv * cum[mid + 1] > x) hi = mid; else lo = mid + 1;
+  }
+  const RunInfo r = run_info(a, lo);
+  const long long per_head = cum[lo + 1] - cum[lo], rem = x - a.Hkv * cum[lo];
+  Place p{lo, static_cast<int>(rem / per_head), 0, 0, 0};
+  long long at = rem - p.kvh * per_head;
+  for (int u0 = 0; u0 < r.units; u0 += 32) {  // the unit of the head
+    const int n = u0 + lane < r.units ? tiles_of(a, r, u0 + lane) + a.unit_cost : 0;
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(dec::kFull, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const unsigned hit = __ballot_sync(dec::kFull, inc > at);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      p.u = u0 + l;
+      p.j = max(0, static_cast<int>(at - __shfl_sync(dec::kFull, inc - n, l)) - a.unit_cost);
+      const long long before = rem - at + __shfl_sync(dec::kFull, inc - n, l);  // cost of the run's units before
+      p.tile = a.Hkv * cum[lo] + before - a.unit_cost * (static_cast<long long>(a.Hkv) * units[lo] + static_cast<long long>(p.kvh) * r.units + p.u) + p.j;
+      return p;
+    }
+    at -= __shfl_sync(dec::kFull, inc, 31);
+  }
+  return p;  // cannot be: x < the total
+}
+// cum and units: shared memory that the ring takes over later.
+__device__ void plan(const AttnArgs& a, Tail* t, long long* cum, int* units) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int s = warp; s < a.batch; s += kThreads / 32) {
     const RunInfo r = run_info(a, s);
     if (r.row0 < 0 && blockIdx.x == 0 && lane == 0) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
     long long n = 0;
-    for (int u = lane; u < r.units; u += 32) n += tiles_of(a, r, u);
+    for (int u = lane; u < r.units; u += 32) n += tiles_of(a, r, u) + a.unit_cost;
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(dec::kFull, n, o);
-    if (lane == 0) cum[s + 1] = n;
+    if (lane == 0) {
+      cum[s + 1] = n;
+      units[s + 1] = r.units;
+    }
   }
   __syncthreads();
   if (warp == 0) {
     long long base = 0;
-    if (lane == 0) cum[0] = 0;
+    int ubase = 0;
+    if (lane == 0) cum[0] = units[0] = 0;
     for (int s0 = 0; s0 < a.batch; s0 += 32) {
       const int s = s0 + lane;
       long long v = s < a.batch ? cum[s + 1] : 0;
+      int w = s < a.batch ? units[s + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(dec::kFull, v, o);
-        if (lane >= o) v += x;
+        const int y = __shfl_up_sync(dec::kFull, w, o);
+        if (lane >= o) { v += x; w += y; }
       }
-      if (s < a.batch) cum[s + 1] = base + v;
+      if (s < a.batch) { cum[s + 1] = base + v; units[s + 1] = ubase + w; }
       base += __shfl_sync(dec::kFull, v, 31);
+      ubase += __shfl_sync(dec::kFull, w, 31);
     }
+    __syncwarp();
     const long long T = base * a.Hkv;
     const long long W = min(static_cast<long long>(gridDim.x), (T + a.tile_min - 1) / a.tile_min);
-    __syncwarp();
-    const long long x0 = W ? T * blockIdx.x / W : 0, x1 = W ? T * (blockIdx.x + 1) / W : 0;
-    const bool mine = blockIdx.x < W;
-    if (mine) {
-      int lo = 0, hi = a.batch - 1;  // first s with Hkv cum[s + 1] > x0
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.Hkv * cum[mid + 1] > x0) hi = mid; else lo = mid + 1;
-      }
-      const RunInfo r = run_info(a, lo);
-      const long long per_head = cum[lo + 1] - cum[lo], rem = x0 - a.Hkv * cum[lo];
-      const int kvh = static_cast<int>(rem / per_head);
-      long long at = rem - kvh * per_head;
-      int unit = 0, first = 0;
-      for (int u0 = 0;; u0 += 32) {  // the unit that holds tile `at` of the head
-        const int n = u0 + lane < r.units ? tiles_of(a, r, u0 + lane) : 0;
-        long long inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long x = __shfl_up_sync(dec::kFull, inc, o);
-          if (lane >= o) inc += x;
-        }
-        const unsigned hit = __ballot_sync(dec::kFull, inc > at);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          unit = u0 + l;
-          first = static_cast<int>(at - __shfl_sync(dec::kFull, inc - n, l));
-          break;
-        }
-        at -= __shfl_sync(dec::kFull, inc, 31);
-        if (u0 + 32 >= r.units) break;  // cannot be: at < per_head
-      }
+    int n = 0;
+    if (blockIdx.x < W) {
+      const long long x1 = T * (blockIdx.x + 1) / W;
+      const Place p = find_place(a, cum, units, T * blockIdx.x / W);
+      const long long end = x1 < T ? find_place(a, cum, units, x1).tile : T - a.unit_cost * (static_cast<long long>(a.Hkv) * ubase);
+      n = static_cast<int>(end - p.tile);
       if (lane == 0) {
-        t->start[0] = lo;
-        t->start[1] = kvh;
-        t->start[2] = unit;
-        t->start[3] = first;
+        t->start[0] = p.s;
+        t->start[1] = p.kvh;
+        t->start[2] = p.u;
+        t->start[3] = p.j;
       }
     }
-    if (lane == 0) {
-      t->T = T;
-      t->n = mine ? static_cast<int>(x1 - x0) : 0;
-    }
+    if (lane == 0) t->n = n;
   }
   __syncthreads();
 }
@@ -302,7 +327,7 @@ __device__ __forceinline__ uint4 ldg_codes(const uint8_t* p) {
 
 template <bool INT8>
 __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
-  const int cw = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int cw = (threadIdx.x >> 5) - kConvertWarp, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   constexpr uint32_t kZero = INT8 ? 0x80808080u : 0u;
   // Everything is loaded one step before its use and left untouched until then, so that no load is waited for where it is
   // issued: block-table entries a tile ahead, scales and codes half a tile.  An absent page (behind the context, or an
@@ -388,8 +413,8 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
     if (lane < 2) {
       const int ek = f16_to_exp(ks), ev = f16_to_exp(vs);
       t->scale[jj % kScaleSlots][2 * cw + lane] =
-          (lost >> (2 * cw + lane)) & 1u ? make_float4(0.f, -INFINITY, 0.f, 0.f)
-                                         : make_float4(fabsf(a.sm_scale) * dec::kLog2e * exp2_int(ek), static_cast<float>(ev), exp2_int(-ev), 0.f);
+          (lost >> (2 * cw + lane)) & 1u ? make_float2(0.f, -INFINITY)
+                                         : make_float2(fabsf(a.sm_scale) * dec::kLog2e * exp2_int(ek), static_cast<float>(ev));
     }
     publish();
     if (more) {
@@ -441,26 +466,19 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
   tmem = dec::uniform_u32(tmem);
   const uint64_t ring = smem_desc(smem_base + kOffRing);
   const uint64_t qd = smem_desc(smem_base + kOffQ);
-  // eight steps of 16: 32 bytes apart inside a 64-element column of rows, the second column 16 KB on
+  // Eight steps of 16: 32 bytes apart inside a 64-element column of rows, the second column 16 KB on; the weights of keys
+  // 64.. lie in those columns of S.  Unrolled: in a loop a product took ~90 clocks to issue, more than to run.
+  auto k_step = [](int ks) { return static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4); };
   auto qk = [&](int i, int slot) {
-    uint64_t x = qd + static_cast<uint64_t>(i * (kOperand >> 4)), y = ring + static_cast<uint64_t>(slot * (kOperand >> 4));
-#pragma unroll 1
-    for (int ks = 0; ks < 8; ++ks) {
-      mma_ss(tmem + kTmemS + 128 * i, x, y, ks > 0, leader);
-      const uint64_t d = ks == 3 ? (16384 - 96) >> 4 : 32 >> 4;
-      x += d;
-      y += d;
-    }
+    const uint64_t x = qd + static_cast<uint64_t>(i * (kOperand >> 4)), y = ring + static_cast<uint64_t>(slot * (kOperand >> 4));
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) mma_ss(tmem + kTmemS + 128 * i, x + k_step(ks), y + k_step(ks), ks > 0, leader);
   };
   auto pv = [&](int i, int slot, bool acc) {
-    uint32_t x = tmem + kTmemS + 128 * i;
-    uint64_t y = ring + static_cast<uint64_t>(slot * (kOperand >> 4));
-#pragma unroll 1
-    for (int ks = 0; ks < 8; ++ks) {
-      mma_ts(tmem + kTmemO + 128 * i, x, y, acc || ks > 0, leader);
-      x += 8;
-      y += ks == 3 ? (16384 - 96) >> 4 : 32 >> 4;
-    }
+    const uint64_t y = ring + static_cast<uint64_t>(slot * (kOperand >> 4));
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+      mma_ts(tmem + kTmemO + 128 * i, tmem + kTmemS + 128 * i + (ks >> 2) * 64 + (ks & 3) * 8, y + k_step(ks), acc || ks > 0, leader);
   };
   int slot = 0;  // of the operand tile taken next
   uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
@@ -521,168 +539,143 @@ __device__ void mma_role(const AttnArgs& a, Tail* t, uint32_t smem_base, uint32_
 // Column k of a 32-column chunk: page parity (k >> 2) & 1, token of the page.
 __device__ __forceinline__ constexpr int col_token(int k) { return 2 * (k >> 3) + (k & 1) + 8 * ((k >> 1) & 1); }
 
-// The row's softmax goes over S in TMEM twice: the maximum, then the weights, 64 columns at a time.  Pages 2 i and 2 i + 1
-// lie in columns 32 i .. 32 i + 31, in groups of four.  y = x log2 e + ev = S k + ev; since k >= 0 a page's largest S gives
-// its largest y.
+// Two threads have a row: one the keys 0..63 of a tile and the output's channels 0..63, its peer (8 warps on) the others.
+// Each goes over its columns of S in TMEM twice, the maximum, then the weights, 32 columns (pages 2 i and 2 i + 1, in groups
+// of four columns) at a time.  y = x log2 e + ev = S k + ev; since k >= 0 a page's largest S gives its largest y.  Keys that
+// the row does not see (token >= seen of the tile) have -inf, whatever S holds there.
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-__device__ __forceinline__ float chunk_max(const float* s, const float4* sc, float rk, float tm) {
-  float pm[2];
-#pragma unroll
-  for (int par = 0; par < 2; ++par) {
-    const float* x = s + 4 * par;  // columns 0..3, 8..11, 16..19, 24..27 from here
-    const float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[8], x[9]), m2 = max3(x[10], x[11], x[16]);
-    const float m3 = max3(x[17], x[18], x[19]), m4 = max3(x[24], x[25], x[26]);
-    pm[par] = fmaxf(max3(m0, m1, m2), max3(m3, m4, x[27]));
-  }
-  const float4 s0 = sc[0], s1 = sc[1];
-  return max3(tm, fmaf(pm[0], s0.x * rk, s0.y), fmaf(pm[1], s1.x * rk, s1.y));
-}
-__device__ __forceinline__ float row_max(uint32_t ts, const float4* scale, float rk) {
+__device__ __forceinline__ float row_max(uint32_t ts, const float2* scale, float rk) {
   float tm = -INFINITY;
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
-    float s[64];
-    tmem_ld32(ts + 64 * i, s);
-    tmem_ld32(ts + 64 * i + 32, s + 32);
+    float s[32];
+    tmem_ld32(ts + 32 * i, s);
+    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
     wait_ld();
-    loaded<64>(s);
-    tm = chunk_max(s, scale + 4 * i, rk, tm);
-    tm = chunk_max(s + 32, scale + 4 * i + 2, rk, tm);
+    loaded<32>(s);
+    float pm[2];
+#pragma unroll
+    for (int par = 0; par < 2; ++par) {
+      const float* x = s + 4 * par;  // columns 0..3, 8..11, 16..19, 24..27 from here
+      const float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[8], x[9]), m2 = max3(x[10], x[11], x[16]);
+      const float m3 = max3(x[17], x[18], x[19]), m4 = max3(x[24], x[25], x[26]);
+      pm[par] = fmaxf(max3(m0, m1, m2), max3(m3, m4, x[27]));
+    }
+    tm = max3(tm, fmaf(pm[0], sc.x * rk, sc.y), fmaf(pm[1], sc.z * rk, sc.w));
   }
   return tm;
 }
-// Weights 2^{y + base} as fp16 pairs over the columns that S leaves free, and their sum without the value scales.
-__device__ __forceinline__ float chunk_weights(const float* s, const float4* sc, float rk, float base, uint32_t* pk) {
-  const float4 s0 = sc[0], s1 = sc[1];
-  const dec::f2x k2[2] = {dec::f2_splat(s0.x * rk), dec::f2_splat(s1.x * rk)};
-  const dec::f2x b2[2] = {dec::f2_splat(s0.y + base), dec::f2_splat(s1.y + base)};
-  dec::f2x sum[2];
-#pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    const int par = (e >> 2) & 1;
-    float y0, y1;
-    dec::f2_unpack(dec::f2_fma(dec::f2_pack(s[e], s[e + 1]), k2[par], b2[par]), y0, y1);
-    const float p0 = ex2(y0), p1 = ex2(y1);
-    const dec::f2x p2 = dec::f2_pack(p0, p1);
-    sum[par] = (e & ~4) == 0 ? p2 : dec::f2_add(sum[par], p2);
-    pk[e >> 1] = dec::pack_f16(p0, p1);
-  }
-  float l0, l1, l2, l3;
-  dec::f2_unpack(sum[0], l0, l1);
-  dec::f2_unpack(sum[1], l2, l3);
-  return fmaf(l0 + l1, s0.z, (l2 + l3) * s1.z);
-}
-__device__ __forceinline__ float weights(uint32_t ts, const float4* scale, float rk, float base) {
-  float l = 0.f;
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    float s[64];
-    uint32_t pk[32];
-    tmem_ld32(ts + 64 * i, s);
-    tmem_ld32(ts + 64 * i + 32, s + 32);
-    wait_ld();
-    loaded<64>(s);
-    l += chunk_weights(s, scale + 4 * i, rk, base, pk);
-    l += chunk_weights(s + 32, scale + 4 * i + 2, rk, base, pk + 16);
-    tmem_st16(ts + 32 * i, pk);
-    tmem_st16(ts + 32 * i + 16, pk + 16);
-  }
-  return l;
-}
-// The same where a row does not see all 128 keys (token < seen of the tile): the tiles on the diagonal.  Hidden logits are
-// -inf whatever the scale, and whatever S holds there.
-__device__ __noinline__ float row_max_masked(uint32_t ts, const float4* scale, float rk, int seen) {
+__device__ __forceinline__ float row_max_masked(uint32_t ts, const float2* scale, float rk, int seen) {
   float tm = -INFINITY;
 #pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     float s[32];
     tmem_ld32(ts + 32 * i, s);
+    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
+    const float k0 = sc.x * rk, k1 = sc.z * rk;
     wait_ld();
     loaded<32>(s);
-    const float4 s0 = scale[2 * i], s1 = scale[2 * i + 1];
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-      const float y = (e >> 2) & 1 ? fmaf(s[e], s1.x * rk, s1.y) : fmaf(s[e], s0.x * rk, s0.y);
+      const float y = (e >> 2) & 1 ? fmaf(s[e], k1, sc.w) : fmaf(s[e], k0, sc.y);
       tm = fmaxf(tm, kPage * (2 * i + ((e >> 2) & 1)) + col_token(e) < seen ? y : -INFINITY);
     }
   }
   return tm;
 }
-__device__ __noinline__ float weights_masked(uint32_t ts, const float4* scale, float rk, float base, int seen) {
+// Weights 2^{y + base} as fp16 pairs over the columns of S, and their sum without the value scales.
+template <bool MASKED>
+__device__ __forceinline__ float weights(uint32_t ts, const float2* scale, float rk, float base, int seen) {
   float l = 0.f;
 #pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     float s[32];
+    uint32_t pk[16];
     tmem_ld32(ts + 32 * i, s);
+    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
+    const dec::f2x k2[2] = {dec::f2_splat(sc.x * rk), dec::f2_splat(sc.z * rk)};
+    const dec::f2x b2[2] = {dec::f2_splat(sc.y + base), dec::f2_splat(sc.w + base)};
+    const float un[2] = {sc.y == -INFINITY ? 0.f : ex2(-sc.y), sc.w == -INFINITY ? 0.f : ex2(-sc.w)};
     wait_ld();
     loaded<32>(s);
-    const float4 s0 = scale[2 * i], s1 = scale[2 * i + 1];
-    float sum[2] = {0.f, 0.f};
-    uint32_t pk[16];
+    dec::f2x sum[2];
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
       const int par = (e >> 2) & 1;
-      float p[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float y = par ? fmaf(s[e + h], s1.x * rk, s1.y + base) : fmaf(s[e + h], s0.x * rk, s0.y + base);
-        p[h] = kPage * (2 * i + par) + col_token(e + h) < seen ? ex2(y) : 0.f;
-        sum[par] += p[h];
+      float y0, y1;
+      dec::f2_unpack(dec::f2_fma(dec::f2_pack(s[e], s[e + 1]), k2[par], b2[par]), y0, y1);
+      if (MASKED) {
+        y0 = kPage * (2 * i + par) + col_token(e) < seen ? y0 : -INFINITY;
+        y1 = kPage * (2 * i + par) + col_token(e + 1) < seen ? y1 : -INFINITY;
       }
-      pk[e >> 1] = dec::pack_f16(p[0], p[1]);
+      const float p0 = ex2(y0), p1 = ex2(y1);
+      const dec::f2x p2 = dec::f2_pack(p0, p1);
+      sum[par] = (e & ~4) == 0 ? p2 : dec::f2_add(sum[par], p2);
+      pk[e >> 1] = dec::pack_f16(p0, p1);
     }
-    l = fmaf(sum[0], s0.z, fmaf(sum[1], s1.z, l));
     tmem_st16(ts + 16 * i, pk);
+    float l0, l1, l2, l3;
+    dec::f2_unpack(sum[0], l0, l1);
+    dec::f2_unpack(sum[1], l2, l3);
+    l = fmaf(l0 + l1, un[0], fmaf(l2 + l3, un[1], l));
   }
   return l;
 }
-// O times alpha, row by row.
+// This thread's channels of O times alpha.
 __device__ __noinline__ void rescale_o(uint32_t to, float alpha) {
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
-    float o[32];
-    tmem_ld32(to + 32 * i, o);
+    float o[16];
+    uint32_t* u = reinterpret_cast<uint32_t*>(o);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(to + 16 * i));
     wait_ld();
-    loaded<32>(o);
+    loaded<16>(o);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] *= alpha;
-    tmem_st16(to + 32 * i, reinterpret_cast<const uint32_t*>(o));
-    tmem_st16(to + 32 * i + 16, reinterpret_cast<const uint32_t*>(o) + 16);
+    for (int e = 0; e < 16; ++e) o[e] *= alpha;
+    tmem_st16(to + 16 * i, u);
   }
 }
-// This thread's row of the unit: its query times a power of two in shared memory, the factor returned.
-__device__ __noinline__ float stage_query(const uint16_t* src_row, bool valid, float sm_scale, uint8_t* qs, int row) {
+// The row's query times a power of two, this thread's 64 channels of it to shared memory (qs); the factor is returned.
+__device__ __noinline__ float stage_query(const uint16_t* src_row, bool valid, float sm_scale, uint8_t* qs, int row, int part) {
   const uint4* src = reinterpret_cast<const uint4*>(src_row);
-  uint4 w[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
   uint32_t top = 0;
+  uint4 w[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+  for (int p = 0; p < 2; ++p) {  // the peer's channels first: only their largest exponent matters here
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max((u[e] >> 7) & 0xFFu, (u[e] >> 23) & 0xFFu));  // largest exponent field
+    for (int i = 0; i < 8; ++i) w[i] = valid ? src[8 * (p ^ part ^ 1) + i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max((u[e] >> 7) & 0xFFu, (u[e] >> 23) & 0xFFu));  // largest exponent field
+    }
   }
   // largest element in [2^8, 2^9): bf16 elements are then exact in fp16 down to 2^-22 of it
   const int er = min(max(static_cast<int>(top) - 127 - 8, -100), 120);
   const float f = copysignf(exp2_int(-er), sm_scale);  // a negative scale goes into the query
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
     uint32_t h[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       h[e] = dec::pack_f16(__uint_as_float(u[e] << 16) * f, __uint_as_float(u[e] & 0xFFFF0000u) * f);
-    *reinterpret_cast<uint4*>(qs + (i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(qs + ((i ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
   }
   dec::fence_proxy_async();
   return exp2_int(er);
 }
-// The row's O, divided and rounded, to the output.
+// This thread's channels of O, divided and rounded, to the output.
 __device__ __noinline__ void store_out(uint32_t to, float inv, uint16_t* dst_row, bool valid) {
   uint4* dst = reinterpret_cast<uint4*>(dst_row);
 #pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     float o[32];
     tmem_ld32(to + 32 * i, o);
     wait_ld();
@@ -695,11 +688,11 @@ __device__ __noinline__ void store_out(uint32_t to, float inv, uint16_t* dst_row
     }
   }
 }
-// The row's O as it is, for the merge.
+// The same as they are, for the merge.
 __device__ __noinline__ void store_piece(uint32_t to, float* dst_row) {
   float4* dst = reinterpret_cast<float4*>(dst_row);
 #pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     float o[32];
     tmem_ld32(to + 32 * i, o);
     wait_ld();
@@ -712,10 +705,20 @@ __device__ __noinline__ void store_piece(uint32_t to, float* dst_row) {
 // At the end of a unit the next one's query is staged, so that its first S is issued, before O is stored.
 __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int half = warp >> 2;
-  const int row = (warp & 3) * 32 + lane;  // of the half
+  const int half = (warp >> 2) & 1, part = warp >> 3;  // rows, columns
+  const int row = (warp & 3) * 32 + lane;              // of the half
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp & 3)
-  const uint32_t ts = tmem + kTmemS + 128 * half + lanes, to = tmem + kTmemO + 128 * half + lanes;
+  const uint32_t ts = tmem + kTmemS + 128 * half + 64 * part + lanes, to = tmem + kTmemO + 128 * half + 64 * part + lanes;
+  // A value for the peer and the peer's for this thread.  A warp that gives up releases its peer (leave) once, which then
+  // gives up at its next wait.
+  const int bar = 1 + (warp & 7);
+  auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory"); };
+  auto leave = [&]() { asm volatile("bar.arrive %0, 64;" ::"r"(bar) : "memory"); };
+  auto exchange = [&](float x) {
+    t->peer[warp][lane] = x;
+    meet();
+    return t->peer[warp ^ 8][lane];
+  };
   Cursor c;
   c.begin(a, t);
   const int total = c.left;
@@ -742,7 +745,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     l = 0.f;
     const long long row_at = static_cast<long long>(run.row0 + tok);
     rk = stage_query(static_cast<const uint16_t*>(a.q) + row_at * a.q_stride + (out_at - row_at * a.Hq) * kHeadDim, valid, a.sm_scale,
-                     smem + kOffQ + half * kOperand + row * 128, row);
+                     smem + kOffQ + half * kOperand + part * 16384 + row * 128, row, part);
     __syncwarp();
     if (lane == 0) arrive(&t->q_full[half]);
     staged = true;
@@ -754,19 +757,20 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
       continue;
     }
     if (!staged) begin_unit();
-    if (!wait_warp(&t->s_full[half], s_phase, &t->abort)) return;
+    if (!wait_warp(&t->s_full[half], s_phase, &t->abort)) return leave();
     s_phase ^= 1u;
     fence_after();
-    const float4* scale = t->scale[jj % kScaleSlots];
-    const int seen = limit - c.j * kKeys;
-    const bool masked = __any_sync(dec::kFull, seen < kKeys);
-    const float tm = masked ? row_max_masked(ts, scale, rk, seen) : row_max(ts, scale, rk);
+    const float2* scale = t->scale[jj % kScaleSlots] + 4 * part;
+    const int seen = limit - c.j * kKeys - 64 * part;  // of this thread's 64 keys
+    const bool masked = __any_sync(dec::kFull, seen < 64);
+    float tm = masked ? row_max_masked(ts, scale, rk, seen) : row_max(ts, scale, rk);
+    tm = fmaxf(tm, exchange(tm));
     if (c.first) {
       m = tm;
     } else {  // the running maximum moves only when a row outgrows it by 2^kSlack
       const bool move = tm > m + kSlack || (m == -INFINITY && tm > m);
       if (__any_sync(dec::kFull, move)) {
-        if (!wait_warp(&t->pv_done[half], pv_phase ^ 1u, &t->abort)) return;  // O is the previous tiles' sum
+        if (!wait_warp(&t->pv_done[half], pv_phase ^ 1u, &t->abort)) return leave();  // O is the previous tiles' sum
         fence_after();
         const float alpha = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - tm);
         m = move ? tm : m;
@@ -775,7 +779,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
       }
     }
     const float base = kTileShift - (m == -INFINITY ? 0.f : m);
-    l += masked ? weights_masked(ts, scale, rk, base, seen) : weights(ts, scale, rk, base);
+    l += masked ? weights<true>(ts, scale, rk, base, seen) : weights<false>(ts, scale, rk, base, 0);
     wait_st();
     fence_before();
     __syncwarp();
@@ -787,7 +791,9 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
       continue;
     }
     const bool whole = begins && c.j + 1 == c.tiles();
-    const float m0 = m, l0 = l;
+    const float m0 = m;
+    meet();  // the peer has read the tile's maximum
+    const float l0 = l + exchange(l);
     const size_t piece = static_cast<size_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kRows + half * 128 + row;
     bool valid;
     int tok;
@@ -796,14 +802,14 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     c.advance(a);
     staged = false;
     if (jj + 1 < total && half < c.halves()) begin_unit();
-    if (!wait_warp(&t->pv_done[half], parity, &t->abort)) return;
+    if (!wait_warp(&t->pv_done[half], parity, &t->abort)) return leave();
     fence_after();
     if (whole) {
-      store_out(to, l0 == 0.f ? 0.f : 1.f / l0, static_cast<uint16_t*>(a.out) + out_at * kHeadDim, valid);
-      if (a.lse && valid) a.lse[out_at] = l0 == 0.f ? -INFINITY : (m0 + (log2f(l0) - kTileShift)) * dec::kLn2;
+      store_out(to, l0 == 0.f ? 0.f : 1.f / l0, static_cast<uint16_t*>(a.out) + out_at * kHeadDim + 64 * part, valid);
+      if (a.lse && valid && part == 0) a.lse[out_at] = l0 == 0.f ? -INFINITY : (m0 + (log2f(l0) - kTileShift)) * dec::kLn2;
     } else {
-      store_piece(to, a.tw_acc + piece * kHeadDim);
-      *reinterpret_cast<float2*>(a.tw_stats + piece * 2) = make_float2(m0, l0);
+      store_piece(to, a.tw_acc + piece * kHeadDim + 64 * part);
+      if (part == 0) *reinterpret_cast<float2*>(a.tw_stats + piece * 2) = make_float2(m0, l0);
     }
     fence_before();
   }
@@ -813,13 +819,13 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
 // earlier CTA ends here.
 template <bool INT8>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ AttnArgs a) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* smem = smem_raw;
   Tail* t = reinterpret_cast<Tail*>(smem + kOffTail);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) t->abort = 0;
-  plan(a, t, reinterpret_cast<long long*>(smem + kOffRing));
+  plan(a, t, reinterpret_cast<long long*>(smem + kOffRing), reinterpret_cast<int*>(smem + kOffRing + 8 * (kMaxBatch + 1)));
   int32_t* rec = a.tw_rec + 8 * blockIdx.x;
   if (t->n == 0) {  // fewer tiles than CTAs
     if (threadIdx.x == 0) rec[0] = rec[4] = 0;
@@ -831,9 +837,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       dec::mbar_init(&t->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      dec::mbar_init(&t->q_full[i], 4);
+      dec::mbar_init(&t->q_full[i], 8);
       dec::mbar_init(&t->s_full[i], 1);
-      dec::mbar_init(&t->p_full[i], 4);
+      dec::mbar_init(&t->p_full[i], 8);
       dec::mbar_init(&t->pv_done[i], 1);
     }
     dec::fence_mbar_init();
@@ -842,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     rec[4] = t->start[3] > 0 && t->start[3] + t->n >= first_tiles;
     rec[0] = 0;
   }
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&t->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -850,14 +856,20 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   __syncthreads();
   fence_after();
   const uint32_t tmem = t->tmem;
-  if (warp < 8) softmax_role(a, t, smem, tmem);
-  else if (warp < 12) convert_role<INT8>(a, t, smem + kOffRing);
-  else mma_role(a, t, smem_u32(smem), tmem, rec);
+  if (warp < kSoftmaxWarps) {
+    softmax_role(a, t, smem, tmem);
+  } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    convert_role<INT8>(a, t, smem + kOffRing);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (warp == kMmaWarp) mma_role(a, t, smem_u32(smem), tmem, rec);
+  }
   __syncwarp();
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   if (threadIdx.x == 0 && t->abort) report(a.err, KVQ_ERR_TIMEOUT);
 }
 
@@ -919,7 +931,9 @@ cudaError_t launch_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s) {
     if (dev >= 0 && dev < kMaxDevices) configured[int8][dev] = true;
   }
   a.tile_ctas = sms;
-  a.tile_min = 1;
+  a.tile_min = 4;
+  a.unit_cost = std::getenv("UC") ? std::atoi(std::getenv("UC")) : 3;
+  if (std::getenv("TM")) a.tile_min = std::atoi(std::getenv("TM"));
   kern<<<sms, kThreads, kSmemBytes, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
