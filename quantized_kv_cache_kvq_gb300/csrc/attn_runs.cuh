@@ -46,7 +46,7 @@ struct AttnArgs {
   float* tw_stats;  // [2 w][256][2]
   int32_t* tw_rec;  // [w][8]
   int tile_ctas;            // CTAs
-  int tile_min, unit_cost;  // the least cost that is worth a CTA; what a unit costs beside its tiles, in tiles
+  int unit_cost;            // what a unit costs beside its tiles, in tiles
   int32_t* err;
 };
 
