@@ -313,25 +313,50 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
       if (s < a.batch) {
         cum[s + 1] = rp += cum[s + 1];
         cumt[s + 1] = rt += cumt[s + 1];
-        if (blockIdx.x == 0) { a.ws_cum_pages[s + 1] = rp; a.ws_cum_tiles[s + 1] = rt; }
       }
     }
     if (threadIdx.x == 0) {
       cum[0] = 0;
       cumt[0] = 0;
-      if (blockIdx.x == 0) { a.ws_cum_pages[0] = 0; a.ws_cum_tiles[0] = 0; }
     }
     __syncthreads();
   }
   if (cumt[a.batch] > a.max_tiles || cumt[a.batch] < 0) {  // runs that overlap: more tiles than the rows can make
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       report(a.err, KVQ_ERR_DEVICE_BOUNDS);
-      a.ws_cum_tiles[a.batch] = -1;  // nothing for the merge
+      *a.ws_units = 0;  // nothing for the merge
     }
     return;
   }
   const long long T = a.Hkv * cum[a.batch];
   const long long W = min(static_cast<long long>(a.w_max), T);
+  // What the merge needs to know of each unit: it then starts with one load.
+  const int n_units = a.Hkv * cumt[a.batch];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ws_units = n_units;
+  for (int u = blockIdx.x * blockDim.x + threadIdx.x; u < n_units; u += gridDim.x * blockDim.x) {
+    int lo_s = 0, hi_s = a.batch - 1;  // first s with Hkv cumt[s + 1] > u
+    while (lo_s < hi_s) {
+      const int mid = (lo_s + hi_s) >> 1;
+      if (a.Hkv * cumt[mid + 1] > u) hi_s = mid; else lo_s = mid + 1;
+    }
+    const Run r = load_run(a.run_starts, a.seq_lens, lo_s, a.num_rows, a.max_run, a.max_pages);
+    const int tiles = cumt[lo_s + 1] - cumt[lo_s], local = u - a.Hkv * cumt[lo_s], kvh = local / tiles, tile = local - kvh * tiles;
+    const int P = (r.len + kPage - 1) / kPage;
+    UnitRecord rec{r.row0, r.n * a.G - tile * 8 * NT, tile * 8 * NT, kvh, 0, 0};
+    if (P > 0) {
+      const long long b = a.Hkv * cum[lo_s] + static_cast<long long>(local) * P;
+      // warp w covers pages [T w / W, T (w + 1) / W): the warp that holds page x
+      auto warp_of = [&](long long x) {
+        long long w = x * W / T;
+        while (w + 1 < W && T * (w + 1) / W <= x) ++w;
+        while (w > 0 && T * w / W > x) --w;
+        return static_cast<int>(w);
+      };
+      rec.w0 = warp_of(b);
+      rec.pieces = warp_of(b + P - 1) - rec.w0 + 1;
+    }
+    a.ws_rec[u] = rec;
+  }
   if (warp >= a.nwa) return;
   const long long wid = static_cast<long long>(blockIdx.x) * a.nwa + warp;
   if (wid >= W) return;
@@ -463,75 +488,73 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
   if (unit >= 0) write_piece(a, wid + unit, s);
 }
 
-// One warp per (row, query head) of the split kernel's runs: the pieces of its unit under log-sum-exp weights.
+// One warp per row of a unit: its pieces under log-sum-exp weights.  The unit's record, then everything it points to in one
+// round of loads; what it costs is the latency of those two (a first version looked the row up from the lengths:
+// 8.5 us alone on 64 requests of 28 heads).
 template <int NT, bool F32>
 __global__ void __launch_bounds__(256) merge_kernel(const AttnArgs a) {
   const int lane = threadIdx.x & 31;
   const long long gw = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (gw >= static_cast<long long>(a.num_rows) * a.Hq) return;
-  const int row = static_cast<int>(gw / a.Hq), qh = static_cast<int>(gw % a.Hq);
-  int s = row;
-  if (a.run_starts) {  // last s with run_starts[s] <= row
-    int lo = 0, hi = a.batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.run_starts[mid] <= row) lo = mid; else hi = mid - 1;
-    }
-    s = lo;
-  }
-  const Run run = load_run(a.run_starts, a.seq_lens, s, a.num_rows, a.max_run, a.max_pages);
-  const int tiles = tiles_of(a, run, 8 * NT);
-  if (run.row0 < 0 || row < run.row0 || row >= run.row0 + run.n || tiles == 0) return;  // not this kernel's row
-  const int kvh = qh / a.G, r = (row - run.row0) * a.G + qh % a.G;
-  const int tile = r / (8 * NT);
-  const int P = (run.len + kPage - 1) / kPage;
+  const long long unit = gw / (8 * NT);
+  const int r = static_cast<int>(gw % (8 * NT));
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (a.ws_cum_tiles[a.batch] < 0) return;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
+  const int n_units = *a.ws_units;
+  const UnitRecord rec = a.ws_rec[unit];  // the grid has no more units than there are records
+  if (unit >= n_units || r >= rec.rows) return;
+  const long long first = (rec.w0 + unit) * (8 * NT) + r;  // of the row's pieces, 8 NT rows apart
+  const float* stats = a.ws_stats + first * 2;
+  const float* accs = a.ws_acc + first * kHeadDim + 4 * lane;
+  constexpr int kU = 8;
+  float4 v[kU];
+#pragma unroll
+  for (int k = 0; k < kU; ++k)
+    if (k < rec.pieces) v[k] = *reinterpret_cast<const float4*>(accs + static_cast<long long>(k) * (8 * NT * kHeadDim));
+  float m = -INFINITY, l = 0.f, m_mine = -INFINITY;  // m_mine: of piece `lane`
   bool nan = false;  // of a query that is not finite
-  if (P > 0) {
-    const long long T = a.Hkv * a.ws_cum_pages[a.batch], W = min(static_cast<long long>(a.w_max), T);
-    const long long b = a.Hkv * a.ws_cum_pages[s] + static_cast<long long>(kvh * tiles + tile) * P;
-    const long long unit = static_cast<long long>(a.Hkv) * a.ws_cum_tiles[s] + kvh * tiles + tile;
-    // warp w covers pages [T w / W, T (w + 1) / W): the warp that holds page x
-    auto warp_of = [&](long long x) {
-      long long w = x * W / T;
-      while (w + 1 < W && T * (w + 1) / W <= x) ++w;
-      while (w > 0 && T * w / W > x) --w;
-      return w;
-    };
-    const long long w0 = warp_of(b), w1 = warp_of(b + P - 1);
-    for (long long w = w0 + lane; w <= w1; w += 32) {
-      const float2 st = *reinterpret_cast<const float2*>(a.ws_stats + ((w + unit) * (8 * NT) + r % (8 * NT)) * 2);
-      const float mm = fmaxf(m, st.x);
-      nan |= st.y != st.y;
-      if (mm != -INFINITY) {
-        l = (m == -INFINITY ? 0.f : l * ex2(m - mm)) + (st.x == -INFINITY ? 0.f : st.y * ex2(st.x - mm));
-        m = mm;
-      }
+  for (int i = lane; i < rec.pieces; i += 32) {
+    const float2 st = *reinterpret_cast<const float2*>(stats + static_cast<long long>(i) * (8 * NT * 2));
+    if (i < 32) m_mine = st.x;
+    const float mm = fmaxf(m, st.x);
+    nan |= st.y != st.y;
+    if (mm != -INFINITY) {
+      l = (m == -INFINITY ? 0.f : l * ex2(m - mm)) + (st.x == -INFINITY ? 0.f : st.y * ex2(st.x - mm));
+      m = mm;
     }
-    float gm = m;
+  }
+  float gm = m;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, o));
-    l = m == -INFINITY ? 0.f : l * ex2(m - gm);
+  for (int o = 16; o; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(kFull, gm, o));
+  l = m == -INFINITY ? 0.f : l * ex2(m - gm);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-    m = gm;
-    if (m != -INFINITY) {
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+  m = gm;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float wt_mine = m_mine == -INFINITY ? 0.f : ex2(m_mine - m);
+#pragma unroll
+  for (int k = 0; k < kU; ++k) {
+    const float wt = __shfl_sync(kFull, wt_mine, k);
+    if (k < rec.pieces && wt != 0.f) {
+      acc.x += v[k].x * wt; acc.y += v[k].y * wt; acc.z += v[k].z * wt; acc.w += v[k].w * wt;
+    }
+  }
 #pragma unroll 8
-      for (long long w = w0; w <= w1; ++w) {
-        const long long at = (w + unit) * (8 * NT) + r % (8 * NT);
-        const float mi = a.ws_stats[at * 2];
-        const float4 v = *reinterpret_cast<const float4*>(a.ws_acc + at * kHeadDim + 4 * lane);
-        const float wt = mi == -INFINITY ? 0.f : ex2(mi - m);
-        acc.x += v.x * wt; acc.y += v.y * wt; acc.z += v.z * wt; acc.w += v.w * wt;
-      }
+  for (int k = kU; k < rec.pieces; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(accs + static_cast<long long>(k) * (8 * NT * kHeadDim));
+    float wt;
+    if (k < 32) {
+      wt = __shfl_sync(kFull, wt_mine, k);
+    } else {
+      const float mi = stats[static_cast<long long>(k) * (8 * NT * 2)];
+      wt = mi == -INFINITY ? 0.f : ex2(mi - m);
     }
+    if (wt != 0.f) { acc.x += x.x * wt; acc.y += x.y * wt; acc.z += x.z * wt; acc.w += x.w * wt; }
   }
   if (__any_sync(kFull, nan)) l = NAN;
   const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is 0
-  const long long at = gw * kHeadDim + 4 * lane;
+  const int in_run = rec.row_in_run + r;
+  const long long row = static_cast<long long>(rec.row0 + in_run / a.G) * a.Hq + rec.kvh * a.G + in_run % a.G;
+  const long long at = row * kHeadDim + 4 * lane;
   if (F32) {
     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   } else {
@@ -539,7 +562,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const AttnArgs a) {
         make_uint2(dec::pack_bf16(acc.x * inv, acc.y * inv), dec::pack_bf16(acc.z * inv, acc.w * inv));
   }
   if (a.lse && lane == 0)
-    a.lse[gw] = l == 0.f ? -INFINITY : (m + (log2f(l) - static_cast<float>(kWeightShift))) * dec::kLn2;
+    a.lse[row] = l == 0.f ? -INFINITY : (m + (log2f(l) - static_cast<float>(kWeightShift))) * dec::kLn2;
 }
 
 // ------------------------------------------------------------------------------------------------ host
@@ -576,7 +599,7 @@ constexpr int kSplitWarps = 16;  // the most that any variant uses (sizes the wo
 int row_blocks(long long max_rows) { return max_rows <= 8 ? 1 : 2; }
 
 struct Workspace {
-  size_t cum_pages, cum_tiles, stats, acc, tw_acc, tw_stats, tw_rec, total;
+  size_t units, rec, stats, acc, tw_acc, tw_stats, tw_rec, total;
   int nt;        // row tiles of 8 nt rows
   int few_rows;  // runs with more rows go to the tile kernel
   bool tile;     // there may be such runs
@@ -597,9 +620,9 @@ Workspace workspace(int batch, int num_rows, int max_run, int hkv, int hq, int q
   const size_t tiles = w.tile ? batch : (static_cast<size_t>(num_rows) * G) / (8 * nt) + batch;
   w.tiles = static_cast<long long>(tiles);
   const size_t slots = static_cast<size_t>(sms) * kSplitWarps + tiles * hkv;
-  w.cum_pages = 0;
-  w.cum_tiles = align256((batch + 1) * sizeof(long long));
-  w.stats = w.cum_tiles + align256((batch + 1) * sizeof(int));
+  w.units = 0;
+  w.rec = 256;
+  w.stats = w.rec + align256(tiles * hkv * sizeof(UnitRecord));
   w.acc = w.stats + align256(slots * 8 * nt * 2 * sizeof(float));
   w.total = w.acc + align256(slots * 8 * nt * kHeadDim * sizeof(float));
   if (w.tile) {
@@ -632,7 +655,7 @@ cudaError_t launch_split(AttnArgs& a, int sms, int smem_max, cudaStream_t s) {
   }
   kern<<<sms, NW * 32, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long threads = static_cast<long long>(a.num_rows) * a.Hq * 32;
+  const long long threads = static_cast<long long>(a.max_tiles) * a.Hkv * (8 * NT) * 32;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((threads + 255) / 256));
   cfg.blockDim = dim3(256);
@@ -718,8 +741,8 @@ extern "C" kvq_status kvq_attn_runs(const kvq_cache* cache, const void* q, int64
   a.lse = lse;
   a.few_rows = w.few_rows;
   a.max_tiles = static_cast<int>(std::min<long long>(w.tiles, 0x7FFFFFFF));
-  a.ws_cum_pages = reinterpret_cast<long long*>(ws + w.cum_pages);
-  a.ws_cum_tiles = reinterpret_cast<int*>(ws + w.cum_tiles);
+  a.ws_units = reinterpret_cast<int*>(ws + w.units);
+  a.ws_rec = reinterpret_cast<UnitRecord*>(ws + w.rec);
   a.ws_stats = reinterpret_cast<float*>(ws + w.stats);
   a.ws_acc = reinterpret_cast<float*>(ws + w.acc);
   a.err = err_word;

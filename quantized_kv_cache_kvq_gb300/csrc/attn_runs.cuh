@@ -17,6 +17,12 @@ namespace runs {
 // 2^-26 of the largest weight; numerator and denominator carry the same factor.
 constexpr int kWeightShift = 12;
 
+// A unit of the split kernel: its rows are rows row_in_run .. of a run (row0: the run's first row in the step), at most
+// `rows` of them; its pieces are those of warps w0 .. w0 + pieces - 1.
+struct UnitRecord {
+  int row0, rows, row_in_run, kvh, w0, pieces;
+};
+
 struct AttnArgs {
   const uint8_t* k;
   const uint8_t* v;
@@ -35,8 +41,8 @@ struct AttnArgs {
   float* lse;  // [num_rows][Hq] or nullptr
   int few_rows;  // runs of at most this many (token, head) rows are the split kernel's, the others the tile kernel's
   // split kernel
-  long long* ws_cum_pages;  // [batch + 1] pages of all tiles of the runs before
-  int* ws_cum_tiles;        // [batch + 1] row tiles of the runs before
+  int* ws_units;            // number of units
+  UnitRecord* ws_rec;       // [units]
   float* ws_stats;          // [slots][rows][2]: m, l
   float* ws_acc;            // [slots][rows][128]
   int max_tiles;            // row tiles that the workspace has room for

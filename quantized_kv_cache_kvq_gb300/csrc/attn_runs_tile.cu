@@ -845,7 +845,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   plan(a, t, reinterpret_cast<long long*>(smem + kOffRing), reinterpret_cast<int*>(smem + kOffRing + 8 * (kMaxBatch + 1)));
   int32_t* rec = a.tw_rec + 8 * blockIdx.x;
   if (t->n == 0) {  // fewer tiles than CTAs
-    if (threadIdx.x == 0) rec[0] = rec[4] = 0;
+    if (threadIdx.x == 0) {
+      rec[0] = rec[4] = 0;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
     return;
   }
   if (threadIdx.x == 0) {
@@ -888,43 +891,56 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   __syncthreads();
   fence_after();
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-  if (threadIdx.x == 0 && t->abort) report(a.err, KVQ_ERR_TIMEOUT);
+  if (threadIdx.x == 0) {
+    if (t->abort) report(a.err, KVQ_ERR_TIMEOUT);
+    // This grid may have run beside the short runs' kernels; it does not end before they do, so that whatever waits for it
+    // waits for them.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
 }
 
-// The units that more than one CTA worked on: block (c, i) merges rows 32 i .. of the unit that began in CTA c.
+// The units that more than one CTA worked on: warp i of block (c, .) merges row i of the unit that began in CTA c.
 __global__ void __launch_bounds__(256) tile_merge_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int in_unit = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int32_t* rec = a.tw_rec + 8 * c;
-  if (!rec[0]) return;
-  const RunInfo run = run_info(a, rec[1]);
-  int end = c + 1;  // the last CTA with a piece
-  while (end + 1 < a.tile_ctas && !a.tw_rec[8 * end + 4]) ++end;
-  for (int i = warp; i < 32; i += 8) {
-    const int in_unit = 32 * blockIdx.y + i, r = rec[3] * kRows + in_unit;
-    if (r >= run.n * a.G) continue;
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = c; k <= end; ++k) {
-      const size_t at = static_cast<size_t>(k == c ? 2 * c + 1 : 2 * k) * kRows + in_unit;
-      const float2 st = *reinterpret_cast<const float2*>(a.tw_stats + at * 2);
-      const float4 v = *reinterpret_cast<const float4*>(a.tw_acc + at * kHeadDim + 4 * lane);
-      const float mn = fmaxf(m, st.x);
-      const float f0 = m == -INFINITY ? 0.f : ex2(m - mn), f1 = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : ex2(st.x - mn);
-      m = mn;
-      l = l * f0 + st.y * f1;
-      acc.x = acc.x * f0 + v.x * f1;
-      acc.y = acc.y * f0 + v.y * f1;
-      acc.z = acc.z * f0 + v.z * f1;
-      acc.w = acc.w * f0 + v.w * f1;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int head = rec[2] * a.G + r % a.G;
-    const long long at = static_cast<long long>(run.row0 + r / a.G) * a.Hq + head;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * kHeadDim + 4 * lane) =
-        make_uint2(dec::pack_bf16(acc.x * inv, acc.y * inv), dec::pack_bf16(acc.z * inv, acc.w * inv));
-    if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + (log2f(l) - kTileShift)) * dec::kLn2;
+  // loads that do not wait for each other: the record, the next CTAs' ends, the first two pieces
+  const int4 unit = *reinterpret_cast<const int4*>(rec);
+  const bool ends = c + 1 + lane < a.tile_ctas && a.tw_rec[8 * (c + 1 + lane) + 4];
+  auto stats_of = [&](int k) { return *reinterpret_cast<const float2*>(a.tw_stats + (static_cast<size_t>(k == c ? 2 * c + 1 : 2 * k) * kRows + in_unit) * 2); };
+  auto acc_of = [&](int k) { return *reinterpret_cast<const float4*>(a.tw_acc + (static_cast<size_t>(k == c ? 2 * c + 1 : 2 * k) * kRows + in_unit) * kHeadDim + 4 * lane); };
+  if (!unit.x) return;
+  const RunInfo run = run_info(a, unit.y);
+  const int r = unit.w * kRows + in_unit;
+  if (r >= run.n * a.G) return;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const unsigned hit = __ballot_sync(dec::kFull, ends);
+  int end = c + __ffs(hit);  // the last CTA with a piece
+  if (!hit) {
+    end = c + 33;
+    while (end + 1 < a.tile_ctas && !a.tw_rec[8 * end + 4]) ++end;
   }
+#pragma unroll 4
+  for (int k = c; k <= end; ++k) {
+    const float2 st = stats_of(k);
+    const float4 v = acc_of(k);
+    const float mn = fmaxf(m, st.x);
+    const float f0 = m == -INFINITY ? 0.f : ex2(m - mn), f1 = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : ex2(st.x - mn);
+    m = mn;
+    l = l * f0 + st.y * f1;
+    acc.x = acc.x * f0 + v.x * f1;
+    acc.y = acc.y * f0 + v.y * f1;
+    acc.z = acc.z * f0 + v.z * f1;
+    acc.w = acc.w * f0 + v.w * f1;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int head = unit.z * a.G + r % a.G;
+  const long long at = static_cast<long long>(run.row0 + r / a.G) * a.Hq + head;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * kHeadDim + 4 * lane) =
+      make_uint2(dec::pack_bf16(acc.x * inv, acc.y * inv), dec::pack_bf16(acc.z * inv, acc.w * inv));
+  if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + (log2f(l) - kTileShift)) * dec::kLn2;
 }
 
 }  // namespace
@@ -952,17 +968,20 @@ cudaError_t launch_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s) {
   // A unit's own cost in tiles, by ranges ending together on a prompt of 2000 tokens (85.3, 83.9, 82.9 us with 2, 3, 4) and of
   // 11996 (1192, 1188, 1186 us); with a unit counted as nothing the ranges of short units ended 40 % behind the others.
   a.unit_cost = 4;
-  kern<<<sms, kThreads, kSmemBytes, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms), kRows / 32);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, a)) != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = dim3(static_cast<unsigned>(sms), kRows / 8);
+  cfg.blockDim = dim3(256);
   return cudaLaunchKernelEx(&cfg, tile_merge_kernel, a);
 }
 
