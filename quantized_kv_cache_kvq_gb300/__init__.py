@@ -53,6 +53,7 @@ DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 TIER_A, TIER_B, TIER_V, TIER_S = 1, 2, 4, 8
 METER_STATE_FLOATS = 8  # floats per (sequence, query head) cell of meter_state
 HEAD_DIM, PAGE, N_BANDS = 128, 16, 16
+_SM_SCALE = 1.0 / math.sqrt(HEAD_DIM)
 
 STATUS = {
     0: "KVQ_OK",
@@ -254,10 +255,14 @@ class PagedCache:
             self.outlier_pairs = outlier_pairs.to(device).contiguous()
             self.k_outlier = torch.zeros((n, 256 if self.n_out <= 4 else 512), **z)
 
+    _page_desc = None  # a page-scaled cache's descriptor, made once: its planes stay the ones it was made over
+
     def _page_scaled(self, k, v, k_scale, v_scale):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.witness = self.v_witness = self.outlier_pairs = self.k_outlier = None
         self.n_out = 0
+        self._page_desc = _Cache(FMT[self.k_fmt], FMT[self.v_fmt], self.num_kv_heads, self.num_pages, self.layer, 0, 0,
+                                 _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale))
 
     @classmethod
     def over(cls, k_fmt: str, v_fmt: str, num_kv_heads: int, num_pages: int, *, k: torch.Tensor, v: torch.Tensor,
@@ -277,6 +282,8 @@ class PagedCache:
         return c
 
     def desc(self) -> _Cache:
+        if self._page_desc is not None:
+            return self._page_desc
         return _Cache(FMT[self.k_fmt], FMT[self.v_fmt], self.num_kv_heads, self.num_pages, self.layer, 0,
                       self.seed & 0xFFFFFFFFFFFFFFFF, _ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
                       _ptr(self.v_scale), _ptr(self.witness), _ptr(self.v_witness), _ptr(self.outlier_pairs),
@@ -445,8 +452,28 @@ def meter(meter_state: torch.Tensor, n_layers: int, batch: int, num_q_heads: int
 
 def _rows(x: torch.Tensor):
     """Row stride of a [rows, heads, 128] tensor whose rows are dense: a slice of a fused projection is taken as it is."""
-    assert x.dim() == 3 and x.shape[2] == HEAD_DIM and x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == HEAD_DIM)
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * HEAD_DIM
+    rows, heads, d = x.shape
+    if rows <= 1 and heads <= 1:
+        assert d == HEAD_DIM and x.stride(2) == 1
+        return HEAD_DIM
+    s0, s1, s2 = x.stride()
+    assert d == HEAD_DIM and s2 == 1 and (heads == 1 or s1 == HEAD_DIM)
+    return s0 if rows > 1 else heads * HEAD_DIM
+
+
+def _i32(*tensors):
+    for t in tensors:
+        assert t is None or (t.dtype is torch.int32 and t.is_contiguous()), "int32 and contiguous"
+
+
+def _launch(name: str, fn, device: int, stream, *args):
+    """The call fn(*args, stream) with ``device`` current, on ``stream`` or that device's current stream."""
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(name, fn, device, stream, *args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+    if status:
+        raise KvqError(status, name)
 
 
 def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
@@ -458,35 +485,35 @@ def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.T
     free_pages [capacity] is the stack of free pages with free_count [1] in use, block_table [B, max_pages]; run_starts
     [B + 1], seq_lens_out [B] and free_count_out [1] are written (the latter two may be the inputs), and slot_mapping and
     positions [max_rows] where given.  All int32 and contiguous."""
-    for t in (new_lens, seq_lens, free_pages, free_count, block_table, run_starts, seq_lens_out, free_count_out,
-              slot_mapping, positions):
-        assert t is None or (t.dtype == torch.int32 and t.is_contiguous())
-    B = new_lens.shape[0]
-    assert seq_lens.shape[0] == B and seq_lens_out.shape[0] == B and run_starts.shape[0] == B + 1
-    assert block_table.dim() == 2 and block_table.shape[0] == B
-    rows = slot_mapping.shape[0] if slot_mapping is not None else positions.shape[0] if positions is not None else 0x7FFFFFFF
-    assert positions is None or positions.shape[0] == rows
-    _check(lib().kvq_map_runs(new_lens.data_ptr(), seq_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.shape[0],
-                              free_count.data_ptr(), block_table.data_ptr(), block_table.shape[1], run_starts.data_ptr(),
-                              seq_lens_out.data_ptr(), free_count_out.data_ptr(), _ptr(slot_mapping), _ptr(positions), rows,
-                              _ptr(err), _stream(stream)), "kvq_map_runs")
+    _i32(new_lens, seq_lens, free_pages, free_count, block_table, run_starts, seq_lens_out, free_count_out, slot_mapping,
+         positions)
+    B, width = block_table.shape
+    assert new_lens.numel() == B and seq_lens.numel() == B and seq_lens_out.numel() == B and run_starts.numel() == B + 1
+    assert free_count.numel() == 1 and free_count_out.numel() == 1
+    rows = 0x7FFFFFFF
+    if slot_mapping is not None:
+        rows = slot_mapping.numel()
+        assert positions is None or positions.numel() == rows
+    elif positions is not None:
+        rows = positions.numel()
+    _launch("kvq_map_runs", lib().kvq_map_runs, run_starts.get_device(), stream, new_lens.data_ptr(), seq_lens.data_ptr(), B,
+            free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), block_table.data_ptr(), width,
+            run_starts.data_ptr(), seq_lens_out.data_ptr(), free_count_out.data_ptr(), _ptr(slot_mapping), _ptr(positions),
+            rows, _ptr(err))
 
 
 def append_runs(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
                 *, run_starts: torch.Tensor | None = None, err: torch.Tensor | None = None, stream=None):
     """kvq_append_runs: quantize the runs' keys and values k, v [rows, Hkv, 128] (fp32 or bf16; rows may be strided) into
     a page-scaled cache.  run_starts [B + 1]; None: one new token for each request."""
-    assert k.dtype == v.dtype and k.shape == v.shape and k.shape[1] == cache.num_kv_heads
-    assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous()
-    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2
-    B = block_table.shape[0]
-    assert seq_lens.shape[0] == B
-    if run_starts is not None:
-        assert run_starts.dtype == torch.int32 and run_starts.is_contiguous() and run_starts.shape[0] == B + 1
-    d = cache.desc()
-    _check(lib().kvq_append_runs(ctypes.byref(d), k.data_ptr(), _rows(k), v.data_ptr(), _rows(v), DTYPE[k.dtype],
-                                 _ptr(run_starts), B, k.shape[0], block_table.data_ptr(), block_table.shape[1],
-                                 seq_lens.data_ptr(), _ptr(err), _stream(stream)), "kvq_append_runs")
+    rows, heads, _ = k.shape
+    assert k.dtype == v.dtype and k.shape == v.shape and heads == cache.num_kv_heads
+    _i32(seq_lens, block_table, run_starts)
+    B, width = block_table.shape
+    assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)
+    _launch("kvq_append_runs", lib().kvq_append_runs, k.get_device(), stream, ctypes.byref(cache.desc()), k.data_ptr(), _rows(k),
+            v.data_ptr(), _rows(v), DTYPE[k.dtype], _ptr(run_starts), B, rows, block_table.data_ptr(), width,
+            seq_lens.data_ptr(), _ptr(err))
 
 
 def attn_runs_workspace_size(batch: int, num_rows: int, max_run: int, num_kv_heads: int, num_q_heads: int,
@@ -502,21 +529,14 @@ def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_
     run_starts None: one query token for each request."""
     rows, Hq, _ = q.shape
     assert out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
-    assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous()
-    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2
-    B = block_table.shape[0]
-    assert seq_lens.shape[0] == B
-    if run_starts is not None:
-        assert run_starts.dtype == torch.int32 and run_starts.is_contiguous() and run_starts.shape[0] == B + 1
-    if lse is not None:
-        assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (rows, Hq)
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
-    d = cache.desc()
-    _check(lib().kvq_attn_runs(ctypes.byref(d), q.data_ptr(), _rows(q), DTYPE[q.dtype], Hq, _ptr(run_starts), B, rows,
-                               int(max_run), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
-                               float(sm_scale), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)), "kvq_attn_runs")
+    _i32(seq_lens, block_table, run_starts)
+    B, width = block_table.shape
+    assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)
+    assert lse is None or (lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() == rows * Hq)
+    _launch("kvq_attn_runs", lib().kvq_attn_runs, q.get_device(), stream, ctypes.byref(cache.desc()), q.data_ptr(), _rows(q),
+            DTYPE[q.dtype], Hq, _ptr(run_starts), B, rows, max_run, block_table.data_ptr(), width, seq_lens.data_ptr(),
+            _SM_SCALE if sm_scale is None else sm_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
+            _ptr(err))
 
 
 def debug_dither(seed: int, layer: int, kv_head: int, slots: torch.Tensor, out: torch.Tensor, stream=None):

@@ -9,6 +9,10 @@
 //
 // One block per (page, kv head) item: all tokens that a run brings to a page are reduced together, so there are no atomics
 // and the result does not depend on any order.
+//
+// Bound by memory: 512 (bf16) or 1024 (fp32) bytes read and 256 written for every token and kv head.  A value tile's 16-byte
+// words hold four tokens of four channels, which lie in eight threads: they are put together by shuffles (byte stores into
+// the staged tile, with their bank conflicts, took 27 us on 11996 tokens of 8 heads; WORDS us so).
 #include <algorithm>
 
 #include "runs.cuh"
@@ -46,13 +50,19 @@ __device__ __forceinline__ int exponent_for(float amax) {
   return min(max(e, kMinExp), kMaxExp);
 }
 
+// Four codes of x f, f = 2^-e.  INT8: the sum with 1.5 2^23 + 128 is rounded once, to an integer, and its low byte is
+// code + 128; the values are in range (the caller has clamped them where they need not be).
 template <bool INT8>
-__device__ __forceinline__ uint8_t encode(float x) {  // x = value 2^-e
+__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float f) {
   if (INT8) {
-    const int c = __float2int_rn(fminf(fmaxf(x, -127.f), 127.f));
-    return static_cast<uint8_t>(c + 128);
+    constexpr float kMagic = 12582912.f + 128.f;
+    const uint32_t a = __float_as_uint(__fmaf_rn(x0, f, kMagic)), b = __float_as_uint(__fmaf_rn(x1, f, kMagic));
+    const uint32_t c = __float_as_uint(__fmaf_rn(x2, f, kMagic)), d = __float_as_uint(__fmaf_rn(x3, f, kMagic));
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
   }
-  return f32_to_e4m3_bits(x);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 * f, x1 * f), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2 * f, x3 * f), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
 }
 template <bool INT8>
 __device__ __forceinline__ float decode(uint8_t b) {
@@ -64,10 +74,7 @@ __device__ __forceinline__ uint4 rescale(uint4 w, float f) {  // 16 codes times 
   uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t r = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r |= static_cast<uint32_t>(encode<INT8>(decode<INT8>(x[i] >> (8 * j)) * f)) << (8 * j);
-    x[i] = r;
+    x[i] = encode4<INT8>(decode<INT8>(x[i]), decode<INT8>(x[i] >> 8), decode<INT8>(x[i] >> 16), decode<INT8>(x[i] >> 24), f);
   }
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
@@ -108,7 +115,7 @@ __device__ __forceinline__ float amax8(float (&x)[8], bool& odd) {
 }
 
 template <bool INT8, bool BF16>
-__global__ void __launch_bounds__(kThreads) append_runs_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) append_runs_kernel(const AppendArgs a) {
   __shared__ int s_cum[kMaxBatch + 1];
   __shared__ int s_warp[kThreads / 32];
   __shared__ float s_max[2][kThreads / 32];
@@ -226,25 +233,86 @@ __global__ void __launch_bounds__(kThreads) append_runs_kernel(const AppendArgs 
       if (ek > ek0) wk = rescale<INT8>(wk, exp2_int(ek0 - ek));
       if (ev > ev0) wv = rescale<INT8>(wv, exp2_int(ev0 - ev));
     }
-    *reinterpret_cast<uint4*>(&s_tile[0][16 * tid]) = wk;
-    *reinterpret_cast<uint4*>(&s_tile[1][16 * tid]) = wv;
-    __syncthreads();
+    // The staged tiles, as 16-byte words in an order that spreads the stores over the banks.
+    auto k_word = [](int w) { return w ^ ((w >> 5 & 1) << 2); };
+    auto v_word = [](int w) { return w ^ ((w >> 3 & 1) | (w >> 5 & 1) << 1); };
+    uint4* tk = reinterpret_cast<uint4*>(s_tile[0]);
+    uint4* tv = reinterpret_cast<uint4*>(s_tile[1]);
+    if (from > 0) {
+      tk[k_word(tid)] = wk;
+      tv[v_word(tid)] = wv;
+      __syncthreads();
+    }
     const float fk = exp2_int(-ek), fv = exp2_int(-ev);
+    if (INT8 && (odd || mk > kTop || mv > kTop)) {  // beyond the largest code
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[0][i][e] = fminf(fmaxf(x[0][i][e], -127.f / fk), 127.f / fk);
+          x[1][i][e] = fminf(fmaxf(x[1][i][e], -127.f / fv), 127.f / fv);
+        }
+    }
+    // Keys: eight channels of a token are half a word.  Tokens behind the last get code 0.
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = t8 + 8 * i;
-      if (t >= from) {  // new tokens; behind the last one, code 0
-        uint32_t w[2] = {0u, 0u};
+      const float(&y)[8] = x[0][i];
+      if (t >= from)
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(tk + k_word(k8_offset(t, ch) >> 4)) + (ch & 8)) =
+            make_uint2(encode4<INT8>(y[0], y[1], y[2], y[3], fk), encode4<INT8>(y[4], y[5], y[6], y[7], fk));
+    }
+    // Values: the word of channels 32 b + g + {0, 8, 16, 24} (b = lane >> 2 & 3) and tokens t8 & ~1, + 1, + 8, + 9.
+    {
+      const int p = lane >> 4, u = lane & 3;
+      uint32_t v[2][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= static_cast<uint32_t>(encode<INT8>(x[0][i][e] * fk)) << (8 * (e & 3));
-        *reinterpret_cast<uint2*>(&s_tile[0][k8_offset(t, ch)]) = make_uint2(w[0], w[1]);
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s_tile[1][v8_offset(t, ch + e)] = encode<INT8>(x[1][i][e] * fv);
+        for (int h = 0; h < 2; ++h)
+          v[i][h] = encode4<INT8>(x[1][i][4 * h], x[1][i][4 * h + 1], x[1][i][4 * h + 2], x[1][i][4 * h + 3], fv);
+      // channels 4 p .. 4 p + 3 of both tokens of the pair
+      const uint32_t m0 = p ? v[0][1] : v[0][0], m1 = p ? v[1][1] : v[1][0];
+      const uint32_t o0 = __shfl_xor_sync(0xffffffffu, p ? v[0][0] : v[0][1], 16), o1 = __shfl_xor_sync(0xffffffffu, p ? v[1][0] : v[1][1], 16);
+      const uint32_t e0 = p ? o0 : m0, d0 = p ? m0 : o0, e1 = p ? o1 : m1, d1 = p ? m1 : o1;  // even, odd token
+      // w[i]: channel 4 p + i of this lane's eight: tokens t, t + 1, t + 8, t + 9
+      uint32_t w[4];
+      const uint32_t l01 = __byte_perm(e0, d0, 0x5140), l23 = __byte_perm(e0, d0, 0x7362);
+      const uint32_t h01 = __byte_perm(e1, d1, 0x5140), h23 = __byte_perm(e1, d1, 0x7362);
+      w[0] = __byte_perm(l01, h01, 0x5410);
+      w[1] = __byte_perm(l01, h01, 0x7632);
+      w[2] = __byte_perm(l23, h23, 0x5410);
+      w[3] = __byte_perm(l23, h23, 0x7632);
+      // 4 x 4 transpose over the lanes u: afterwards w[i] is channel 4 p + u of lane i's eight
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const bool up = u & 1;
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, up ? w[2 * b] : w[2 * b + 1], 1);
+        if (up) w[2 * b] = r; else w[2 * b + 1] = r;
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const bool up = u & 2;
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, up ? w[b] : w[b + 2], 2);
+        if (up) w[b] = r; else w[b + 2] = r;
+      }
+      const uint4 word = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x5410),
+                                    __byte_perm(w[2], w[3], 0x7632));
+      const int at = v_word(32 * (lane >> 2 & 3) + 4 * (4 * p + u) + warp);
+      const int t0 = 2 * warp;  // the pair's tokens t0, t0 + 1 (bytes 0, 1 of a half word), t0 + 8, t0 + 9
+      if (from == 0) {
+        tv[at] = word;
+      } else {  // keep the earlier tokens' bytes
+        const uint32_t lo = (t0 >= from ? 0x00FF00FFu : 0u) | (t0 + 1 >= from ? 0xFF00FF00u : 0u);
+        const uint32_t hi = (t0 + 8 >= from ? 0x00FF00FFu : 0u) | (t0 + 9 >= from ? 0xFF00FF00u : 0u);
+        const uint4 was = tv[at];
+        tv[at] = make_uint4((word.x & lo) | (was.x & ~lo), (word.y & hi) | (was.y & ~hi), (word.z & lo) | (was.z & ~lo),
+                            (word.w & hi) | (was.w & ~hi));
       }
     }
     __syncthreads();
-    *reinterpret_cast<uint4*>(a.k + tile + 16 * tid) = *reinterpret_cast<const uint4*>(&s_tile[0][16 * tid]);
-    *reinterpret_cast<uint4*>(a.v + tile + 16 * tid) = *reinterpret_cast<const uint4*>(&s_tile[1][16 * tid]);
+    *reinterpret_cast<uint4*>(a.k + tile + 16 * tid) = tk[k_word(tid)];
+    *reinterpret_cast<uint4*>(a.v + tile + 16 * tid) = tv[v_word(tid)];
     if (tid == 0) {
       a.ks[si] = exp_to_f16(ek);
       a.vs[si] = exp_to_f16(ev);
@@ -301,7 +369,7 @@ extern "C" kvq_status kvq_append_runs(const kvq_cache* cache, const void* k, int
   // pages touched: at most one per row, and a run of n tokens touches at most (n + 14) / 16 + 1
   const long long pages = std::min<long long>(num_rows, num_rows / kPage + 2ll * batch);
   const long long items = pages * cache->num_kv_heads;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(items, 152 * 12));
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(items, 152 * 8));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = in_dtype == KVQ_DTYPE_BF16;
   const cudaError_t e = cache->k_fmt == KVQ_FMT_INT8_PAGE ? launch<true>(a, bf16, grid, s) : launch<false>(a, bf16, grid, s);
