@@ -33,13 +33,14 @@ namespace {
 
 constexpr int kStageBytes = 4096;
 constexpr int kMaxStages = 8;
+constexpr int kMinPages = 2;  // pages a warp, so that short contexts leave the merge fewer pieces
 
 // Page descriptors, one per lane for 32 pages ahead.
 struct Desc {
   int32_t phys;    // -1: nothing to read (past the tile's last visible token, or reported as out of range)
   int32_t page;    // page index in the request
   int32_t unit;    // global unit index
-  uint32_t scale;  // the page's key and value scale exponents + 32 (bits 0..7, 8..15)
+  uint16_t ks, vs;  // the page's scales as stored
 };
 
 struct Unit {
@@ -146,14 +147,13 @@ __device__ void load_q(const AttnArgs& a, const Unit& u, Query<NT>& f, uint32_t*
   if (F32) __syncwarp();
 }
 
-template <bool INT8>
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {  // bytes 0, 1 as fp16
-  return INT8 ? dec::u8x2_to_f16x2(w, 0) : dec::e4m3x2_to_f16x2(w & 0xFFFFu);
-}
-template <bool INT8>
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {  // bytes 2, 3
-  return INT8 ? dec::u8x2_to_f16x2(w, 1) : dec::e4m3x2_to_f16x2(w >> 16);
-}
+// Weights are multiplied by 2^kShift before they are rounded to fp16, whose normal range then reaches down to 2^-(14 + kShift)
+// of the largest; numerator and denominator carry the same factor.  The running maximum moves only when a logit exceeds it by
+// kSlack, so that most pages need no rescaling; the largest weight is then 2^(kShift + kSlack) < 65504.
+template <bool F32>
+struct Weight {
+  static constexpr float kShift = F32 ? 12.f : 8.f, kSlack = F32 ? 3.f : 7.f;
+};
 
 // One page: st holds its key tile and its value tile.
 template <bool INT8, int NT, bool F32>
@@ -192,8 +192,7 @@ __device__ __forceinline__ void process(const uint8_t* st, const Query<NT>& f, c
       for (int i = 0; i < 4; ++i)
         if (p0 + g + 8 * (i >> 1) >= f.limit[n][i & 1]) y[i] = -INFINITY;
     }
-    // the maximum moves seldom: the column reduction and the rescaling are taken only when some value exceeds it
-    if (__any_sync(kFull, fmaxf(y[0], y[2]) > s.m[n][0] || fmaxf(y[1], y[3]) > s.m[n][1])) {
+    if (__any_sync(kFull, fmaxf(y[0], y[2]) > s.m[n][0] + Weight<F32>::kSlack || fmaxf(y[1], y[3]) > s.m[n][1] + Weight<F32>::kSlack)) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float mn = fmaxf(s.m[n][h], col_max8(fmaxf(y[h], y[2 + h])));
@@ -211,7 +210,7 @@ __device__ __forceinline__ void process(const uint8_t* st, const Query<NT>& f, c
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float m = s.m[n][i & 1];
-      p[i] = ex2(y[i] - (m == -INFINITY ? 0.f : m) + static_cast<float>(kWeightShift));
+      p[i] = ex2(y[i] - (m == -INFINITY ? 0.f : m) + Weight<F32>::kShift);
     }
     s.l[n][0] = fmaf(p[0] + p[2], unscale, s.l[n][0]);
     s.l[n][1] = fmaf(p[1] + p[3], unscale, s.l[n][1]);
@@ -329,37 +328,38 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
     return;
   }
   const long long T = a.Hkv * cum[a.batch];
-  const long long W = min(static_cast<long long>(a.w_max), T);
+  const long long W = min(static_cast<long long>(a.w_max), (T + kMinPages - 1) / kMinPages);
   // What the merge needs to know of each unit: it then starts with one load.
   const int n_units = a.Hkv * cumt[a.batch];
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ws_units = n_units;
-  for (int u = blockIdx.x * blockDim.x + threadIdx.x; u < n_units; u += gridDim.x * blockDim.x) {
-    int lo_s = 0, hi_s = a.batch - 1;  // first s with Hkv cumt[s + 1] > u
-    while (lo_s < hi_s) {
-      const int mid = (lo_s + hi_s) >> 1;
-      if (a.Hkv * cumt[mid + 1] > u) hi_s = mid; else lo_s = mid + 1;
+  auto write_records = [&]() {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ws_units = n_units;
+    for (int u = blockIdx.x * blockDim.x + threadIdx.x; u < n_units; u += gridDim.x * blockDim.x) {
+      int lo_s = 0, hi_s = a.batch - 1;  // first s with Hkv cumt[s + 1] > u
+      while (lo_s < hi_s) {
+        const int mid = (lo_s + hi_s) >> 1;
+        if (a.Hkv * cumt[mid + 1] > u) hi_s = mid; else lo_s = mid + 1;
+      }
+      const Run r = load_run(a.run_starts, a.seq_lens, lo_s, a.num_rows, a.max_run, a.max_pages);
+      const int tiles = cumt[lo_s + 1] - cumt[lo_s], local = u - a.Hkv * cumt[lo_s], kvh = local / tiles, tile = local - kvh * tiles;
+      const int P = (r.len + kPage - 1) / kPage;
+      UnitRecord rec{r.row0, r.n * a.G - tile * 8 * NT, tile * 8 * NT, kvh, 0, 0};
+      if (P > 0) {
+        const long long b = a.Hkv * cum[lo_s] + static_cast<long long>(local) * P;
+        // warp w covers pages [T w / W, T (w + 1) / W): the warp that holds page x
+        auto warp_of = [&](long long x) {
+          long long w = x * W / T;
+          while (w + 1 < W && T * (w + 1) / W <= x) ++w;
+          while (w > 0 && T * w / W > x) --w;
+          return static_cast<int>(w);
+        };
+        rec.w0 = warp_of(b);
+        rec.pieces = warp_of(b + P - 1) - rec.w0 + 1;
+      }
+      a.ws_rec[u] = rec;
     }
-    const Run r = load_run(a.run_starts, a.seq_lens, lo_s, a.num_rows, a.max_run, a.max_pages);
-    const int tiles = cumt[lo_s + 1] - cumt[lo_s], local = u - a.Hkv * cumt[lo_s], kvh = local / tiles, tile = local - kvh * tiles;
-    const int P = (r.len + kPage - 1) / kPage;
-    UnitRecord rec{r.row0, r.n * a.G - tile * 8 * NT, tile * 8 * NT, kvh, 0, 0};
-    if (P > 0) {
-      const long long b = a.Hkv * cum[lo_s] + static_cast<long long>(local) * P;
-      // warp w covers pages [T w / W, T (w + 1) / W): the warp that holds page x
-      auto warp_of = [&](long long x) {
-        long long w = x * W / T;
-        while (w + 1 < W && T * (w + 1) / W <= x) ++w;
-        while (w > 0 && T * w / W > x) --w;
-        return static_cast<int>(w);
-      };
-      rec.w0 = warp_of(b);
-      rec.pieces = warp_of(b + P - 1) - rec.w0 + 1;
-    }
-    a.ws_rec[u] = rec;
-  }
-  if (warp >= a.nwa) return;
+  };
   const long long wid = static_cast<long long>(blockIdx.x) * a.nwa + warp;
-  if (wid >= W) return;
+  if (warp >= a.nwa || wid >= W) return write_records();
   const long long x_begin = T * wid / W, x_end = T * (wid + 1) / W;
   const long long n = x_end - x_begin;
 
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
   __syncwarp();
 
   auto make_desc = [&](long long x) {
-    Desc d{-1, 0, 0, 0u};
+    Desc d{-1, 0, 0, 0, 0};
     if (x >= x_end) return d;
     int lo_s = 0, hi_s = a.batch - 1;  // first s with Hkv cum[s + 1] > x
     while (lo_s < hi_s) {
@@ -399,7 +399,8 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
     }
     d.phys = phys;
     const size_t si = static_cast<size_t>(kvh) * a.num_pages + phys;
-    d.scale = static_cast<uint32_t>(f16_to_exp(a.ks[si]) + 32) | static_cast<uint32_t>(f16_to_exp(a.vs[si]) + 32) << 8;
+    d.ks = a.ks[si];
+    d.vs = a.vs[si];
     return d;
   };
   auto unit_of = [&](int unit) {
@@ -424,11 +425,20 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
     bulk_g2s_hint(dst + 2048, a.v + tile, 2048, &bars[st], pol, leader);
   };
   auto kvh_of = [&](int unit) { return unit_of(unit).kvh; };
+  // exponents + 32 of a descriptor's scales (bits 0..7 key, 8..15 value); apart from the descriptor, so that nothing waits
+  // for the loads before they are needed
+  auto exponents = [](const Desc& d) {
+    return static_cast<uint32_t>(f16_to_exp(d.ks) + 32) | static_cast<uint32_t>(f16_to_exp(d.vs) + 32) << 8;
+  };
 
-  Desc cur = make_desc(x_begin + lane), nxt = make_desc(x_begin + 32 + lane);
-  int cur_kvh = cur.phys >= 0 ? kvh_of(cur.unit) : 0, nxt_kvh = nxt.phys >= 0 ? kvh_of(nxt.unit) : 0;
+  Desc cur = make_desc(x_begin + lane);
+  int cur_kvh = cur.phys >= 0 ? kvh_of(cur.unit) : 0;
   for (int j = 0; j < a.stages && j < n; ++j)
     issue(j, __shfl_sync(kFull, cur.phys, j), __shfl_sync(kFull, cur_kvh, j), dec::elect_one());
+  write_records();
+  Desc nxt = make_desc(x_begin + 32 + lane);
+  int nxt_kvh = nxt.phys >= 0 ? kvh_of(nxt.unit) : 0;
+  uint32_t cur_scale = exponents(cur);
 
   Query<NT> f;
   State<NT> s;
@@ -444,12 +454,13 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
     if (j > 0 && jl == 0) {
       cur = nxt;
       cur_kvh = nxt_kvh;
+      cur_scale = exponents(cur);
       nxt = make_desc(x_begin + j + 32 + lane);
       nxt_kvh = nxt.phys >= 0 ? kvh_of(nxt.unit) : 0;
     }
     const int phys = __shfl_sync(kFull, cur.phys, jl), page = __shfl_sync(kFull, cur.page, jl);
     const int u = __shfl_sync(kFull, cur.unit, jl);
-    const uint32_t scale = __shfl_sync(kFull, cur.scale, jl);
+    const uint32_t scale = __shfl_sync(kFull, cur_scale, jl);
     if (u != unit) {
       if (unit >= 0) { write_piece(a, wid + unit, s); reset(s); }
       unit = u;
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const AttnArgs a) {
   const long long first = (rec.w0 + unit) * (8 * NT) + r;  // of the row's pieces, 8 NT rows apart
   const float* stats = a.ws_stats + first * 2;
   const float* accs = a.ws_acc + first * kHeadDim + 4 * lane;
-  constexpr int kU = 8;
+  constexpr int kU = 16;
   float4 v[kU];
 #pragma unroll
   for (int k = 0; k < kU; ++k)
@@ -562,7 +573,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const AttnArgs a) {
         make_uint2(dec::pack_bf16(acc.x * inv, acc.y * inv), dec::pack_bf16(acc.z * inv, acc.w * inv));
   }
   if (a.lse && lane == 0)
-    a.lse[row] = l == 0.f ? -INFINITY : (m + (log2f(l) - static_cast<float>(kWeightShift))) * dec::kLn2;
+    a.lse[row] = l == 0.f ? -INFINITY : (m + (log2f(l) - Weight<F32>::kShift)) * dec::kLn2;
 }
 
 // ------------------------------------------------------------------------------------------------ host

@@ -13,9 +13,21 @@
 namespace kvq {
 namespace runs {
 
-// Weights are multiplied by 2^kWeightShift before they are rounded to fp16, whose normal range then reaches down to
-// 2^-26 of the largest weight; numerator and denominator carry the same factor.
-constexpr int kWeightShift = 12;
+// Two codes as fp16: bytes 0, 1 (lo) or 2, 3 (hi) of a word, exact in either format.
+template <bool INT8>
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  if (INT8) return dec::u8x2_to_f16x2(w, 0);
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+template <bool INT8>
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  if (INT8) return dec::u8x2_to_f16x2(w, 1);
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
 
 // A unit of the split kernel: its rows are rows row_in_run .. of a run (row0: the run's first row in the step), at most
 // `rows` of them; its pieces are those of warps w0 .. w0 + pieces - 1.

@@ -318,14 +318,6 @@ __device__ void plan(const AttnArgs& a, Tail* t, long long* cum, int* units) {
 }
 
 // ------------------------------------------------------------------------------------------------ converting warps
-template <bool INT8>
-__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) {
-  return INT8 ? dec::u8x2_to_f16x2(w, 0) : dec::e4m3x2_to_f16x2(w & 0xFFFFu);
-}
-template <bool INT8>
-__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) {
-  return INT8 ? dec::u8x2_to_f16x2(w, 1) : dec::e4m3x2_to_f16x2(w >> 16);
-}
 __device__ __forceinline__ uint4 ldg_codes(const uint8_t* p) {
   uint4 r;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
@@ -412,9 +404,9 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
         const int low = k_low + 2 * (i >> 1);
         uint8_t* base = dst + (i & 1) * 16384 + 2 * (i >> 1) * 128;
         *reinterpret_cast<uint4*>(base + (((2 * q) ^ low) << 4)) =
-            make_uint4(cvt_lo<INT8>(x.x), cvt_hi<INT8>(x.x), cvt_lo<INT8>(x.y), cvt_hi<INT8>(x.y));
+            make_uint4(codes_lo<INT8>(x.x), codes_hi<INT8>(x.x), codes_lo<INT8>(x.y), codes_hi<INT8>(x.y));
         *reinterpret_cast<uint4*>(base + (((2 * q + 1) ^ low) << 4)) =
-            make_uint4(cvt_lo<INT8>(x.z), cvt_hi<INT8>(x.z), cvt_lo<INT8>(x.w), cvt_hi<INT8>(x.w));
+            make_uint4(codes_lo<INT8>(x.z), codes_hi<INT8>(x.z), codes_lo<INT8>(x.w), codes_hi<INT8>(x.w));
         load_v(plane, phys, i);
       }
     }
@@ -454,10 +446,10 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
         const uint4 x = buf[2 * pp], y = buf[2 * pp + 1];
         // pair of pages 2 quad + (pp ^ (g & 1)): column 32 pair + 8 q + {its first page: 0..3, its second: 4..7}
         uint8_t* base = dst + (((4 * ((pp ^ g) & 1) + q) ^ g) << 4);
-        *reinterpret_cast<uint4*>(base) = make_uint4(cvt_lo<INT8>(x.x), cvt_lo<INT8>(x.y), cvt_lo<INT8>(y.x), cvt_lo<INT8>(y.y));
-        *reinterpret_cast<uint4*>(base + 8 * 128) = make_uint4(cvt_hi<INT8>(x.x), cvt_hi<INT8>(x.y), cvt_hi<INT8>(y.x), cvt_hi<INT8>(y.y));
-        *reinterpret_cast<uint4*>(base + 16 * 128) = make_uint4(cvt_lo<INT8>(x.z), cvt_lo<INT8>(x.w), cvt_lo<INT8>(y.z), cvt_lo<INT8>(y.w));
-        *reinterpret_cast<uint4*>(base + 24 * 128) = make_uint4(cvt_hi<INT8>(x.z), cvt_hi<INT8>(x.w), cvt_hi<INT8>(y.z), cvt_hi<INT8>(y.w));
+        *reinterpret_cast<uint4*>(base) = make_uint4(codes_lo<INT8>(x.x), codes_lo<INT8>(x.y), codes_lo<INT8>(y.x), codes_lo<INT8>(y.y));
+        *reinterpret_cast<uint4*>(base + 8 * 128) = make_uint4(codes_hi<INT8>(x.x), codes_hi<INT8>(x.y), codes_hi<INT8>(y.x), codes_hi<INT8>(y.y));
+        *reinterpret_cast<uint4*>(base + 16 * 128) = make_uint4(codes_lo<INT8>(x.z), codes_lo<INT8>(x.w), codes_lo<INT8>(y.z), codes_lo<INT8>(y.w));
+        *reinterpret_cast<uint4*>(base + 24 * 128) = make_uint4(codes_hi<INT8>(x.z), codes_hi<INT8>(x.w), codes_hi<INT8>(y.z), codes_hi<INT8>(y.w));
         load_k(plane, phys, 2 * pp);  // behind the last tile: read again and thrown away
         load_k(plane, phys, 2 * pp + 1);
       }

@@ -43,7 +43,7 @@ __device__ __forceinline__ int find_segment(const int* a, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) map_runs_kernel(const MapArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) {
   __shared__ int s_start[kMaxBatch + 1], s_want[kMaxBatch + 1], s_back[kMaxBatch + 1];
   __shared__ int s_old[kMaxBatch];
   __shared__ long long s_tot[3][kThreads / 32];
@@ -128,19 +128,31 @@ __global__ void __launch_bounds__(kThreads) map_runs_kernel(const MapArgs a) {
   }
   for (int i = first; i < R - A; i += stride) a.free_pages[fc + i] = handed_back(i);
   if (a.slots || a.positions) {
-    for (int r = first; r < a.max_rows; r += stride) {
-      int slot = -1, pos = 0;
-      if (r < n_rows) {
-        const int s = find_segment(s_start, a.batch, r);
-        const int o = s_old[s], h = (o + kPage - 1) / kPage;
-        pos = o + (r - s_start[s]);
-        const int j = pos / kPage;
-        const int page = j < h ? a.block_table[static_cast<size_t>(s) * a.max_pages + j] : page_of(s_want[s] + j - h);
-        if (page < 0 || page > 0x7FFFFFF) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
-        else slot = page * kPage + pos % kPage;
+    // four rows in a row to a thread: one search, and mostly one page, for them
+    for (int r0 = 4 * first; r0 < a.max_rows; r0 += 4 * stride) {
+      int s = r0 < n_rows ? find_segment(s_start, a.batch, r0) : 0, j = -1, page = -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i;
+        if (r >= a.max_rows) break;
+        int slot = -1, pos = 0;
+        if (r < n_rows) {
+          while (r >= s_start[s + 1]) {
+            ++s;
+            j = -1;
+          }
+          const int o = s_old[s], h = (o + kPage - 1) / kPage;
+          pos = o + (r - s_start[s]);
+          if (pos / kPage != j) {
+            j = pos / kPage;
+            page = j < h ? a.block_table[static_cast<size_t>(s) * a.max_pages + j] : page_of(s_want[s] + j - h);
+          }
+          if (page < 0 || page > 0x7FFFFFF) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
+          else slot = page * kPage + pos % kPage;
+        }
+        if (a.slots) a.slots[r] = slot;
+        if (a.positions) a.positions[r] = pos;
       }
-      if (a.slots) a.slots[r] = slot;
-      if (a.positions) a.positions[r] = pos;
     }
   }
   asm volatile("barrier.cluster.wait;" ::: "memory");
@@ -168,18 +180,22 @@ extern "C" kvq_status kvq_map_runs(const int32_t* new_lens, const int32_t* seq_l
                                    int32_t* err_word, kvq_stream_t stream) {
   using namespace kvq::runs;
   if (batch < 0 || batch > kMaxBatch || free_capacity < 0 || max_pages_per_seq < 0 || max_rows < 0) return KVQ_ERR_INVALID_ARG;
+  if ((slot_mapping || positions) && max_rows > 1 << 30) return KVQ_ERR_INVALID_ARG;  // rows are indexed with 32-bit integers
   if (!free_count || !run_starts || !free_count_out || (free_capacity > 0 && !free_pages)) return KVQ_ERR_INVALID_ARG;
   if (batch > 0 && (!new_lens || !seq_lens || !seq_lens_out || (max_pages_per_seq > 0 && !block_table)))
     return KVQ_ERR_INVALID_ARG;
   MapArgs a{new_lens,   seq_lens,     batch,          free_pages,   free_capacity, free_count, block_table, max_pages_per_seq,
             run_starts, seq_lens_out, free_count_out, slot_mapping, positions,     max_rows,   err_word};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(8);
+  // one block while its threads have a few rows each: a cluster of eight starts later (SMALL)
+  const long long work = batch + (slot_mapping || positions ? max_rows : 0ll);
+  const unsigned blocks = work <= 2 * kThreads ? 1 : 8;
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 8;
+  attr[0].val.clusterDim.x = blocks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
