@@ -12,7 +12,8 @@
 //
 // Bound by memory: 512 (bf16) or 1024 (fp32) bytes read and 256 written for every token and kv head.  A value tile's 16-byte
 // words hold four tokens of four channels, which lie in eight threads: they are put together by shuffles (byte stores into
-// the staged tile, with their bank conflicts, took 27 us on 11996 tokens of 8 heads; WORDS us so).
+// the staged tile, with their bank conflicts, took 27 us on 11996 tokens of 8 heads).  A block fetches its next item while it
+// quantizes one: 18.5 us there, of which 10.9 are its bytes at the copy rate and about 10 its instructions.
 #include <algorithm>
 
 #include "runs.cuh"
@@ -79,24 +80,50 @@ __device__ __forceinline__ uint4 rescale(uint4 w, float f) {  // 16 codes times 
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// eight channels of one row
+// eight channels of one row, as loaded and as values
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, long long at, float (&x)[8]) {
-  if (BF16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+  uint4 w[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* base, long long at) {
+    const uint4* p = BF16 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at)
+                          : reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = p[i];
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  // Largest magnitude, as binary32 bits: as integers, a NaN is above infinity and that above what is finite.
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (BF16) asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(u[e] & 0x7FFF7FFFu));
+        else m = max(m, u[e] & 0x7FFFFFFFu);
+      }
+    }
+    return BF16 ? max(m & 0xFFFF0000u, m << 16) : m;
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (BF16) {
+          x[2 * e] = __uint_as_float(u[e] << 16);
+          x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+        } else {
+          x[4 * i + e] = __uint_as_float(u[e]);
+        }
+      }
+    }
+  }
+};
 
 // the largest finite magnitude of 8 values; a NaN becomes 0, an infinity stays (it saturates) and is not counted
 __device__ __forceinline__ float amax8(float (&x)[8], bool& odd) {
@@ -115,10 +142,11 @@ __device__ __forceinline__ float amax8(float (&x)[8], bool& odd) {
 }
 
 template <bool INT8, bool BF16>
-__global__ void __launch_bounds__(kThreads, 8) append_runs_kernel(const AppendArgs a) {
-  __shared__ int s_cum[kMaxBatch + 1];
+__global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) append_runs_kernel(const AppendArgs a) {
+  __shared__ int s_cum[kMaxBatch + 1];                 // pages of the runs before
+  __shared__ int s_first[kMaxBatch], s_len[kMaxBatch], s_row[kMaxBatch];  // the run's first position, its context, its first row
   __shared__ int s_warp[kThreads / 32];
-  __shared__ float s_max[2][kThreads / 32];
+  __shared__ uint32_t s_max[2][kThreads / 32];
   __shared__ __align__(16) uint8_t s_tile[2][kTile];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -128,6 +156,9 @@ __global__ void __launch_bounds__(kThreads, 8) append_runs_kernel(const AppendAr
     int loc = 0;
     auto pages = [&](int s) {
       const Run r = load_run(a.run_starts, a.seq_lens, s, a.num_rows, a.num_rows, a.max_pages);
+      s_first[s] = r.len - r.n;
+      s_len[s] = r.len;
+      s_row[s] = r.row0;
       if (!a.run_starts && r.n && r.len == 0) return 0;  // nothing to append
       if (r.row0 < 0 || r.n > r.len) {
         if (blockIdx.x == 0) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
@@ -159,21 +190,65 @@ __global__ void __launch_bounds__(kThreads, 8) append_runs_kernel(const AppendAr
 
   const long long items = static_cast<long long>(s_cum[a.batch]) * a.H;
   const int t8 = tid >> 4, ch = (tid & 15) * 8;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int pi = static_cast<int>(item / a.H), h = static_cast<int>(item % a.H);
-    int lo = 0, hi = a.batch - 1;  // last s with cum[s] <= pi
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_cum[mid] <= pi) lo = mid; else hi = mid - 1;
+  struct Item {
+    int h, p0, from, to, phys;  // kv head, the page's first position, its new tokens [from, to), physical page
+    Raw<BF16> k[2], v[2];       // this thread's tokens t8, t8 + 8
+  };
+  // Everything that an item reads without waiting for it: it is the next one's while this one is quantized.
+  int pi = blockIdx.x / a.H, next_h = blockIdx.x % a.H, run = 0;  // page and kv head of the item to fetch, run of the page
+  const int step_pi = gridDim.x / a.H, step_h = gridDim.x % a.H;
+  {
+    int hi = a.batch - 1;  // last run with cum <= pi
+    while (run < hi) {
+      const int mid = (run + hi + 1) >> 1;
+      if (s_cum[mid] <= pi) run = mid; else hi = mid - 1;
     }
-    const int s = lo;
-    const Run r = load_run(a.run_starts, a.seq_lens, s, a.num_rows, a.num_rows, a.max_pages);
-    const int first = r.len - r.n;                       // position of the run's first token
-    const int page = first / kPage + (pi - s_cum[s]);
-    const int p0 = page * kPage;
-    if (page < first / kPage || p0 >= r.len) continue;  // runs that overlap (reported where they are read)
-    const int from = max(first - p0, 0), to = min(r.len - p0, kPage);  // the page's tokens that are new
-    const int phys = a.block_table[static_cast<size_t>(s) * a.max_pages + page];
+  }
+  auto fetch = [&](Item& it) {
+    while (run + 1 < a.batch && s_cum[run + 1] <= pi) ++run;
+    const int first = s_first[run], len = s_len[run], page = first / kPage + (pi - s_cum[run]);
+    it.h = next_h;
+    it.p0 = page * kPage;
+    it.from = max(first - it.p0, 0);
+    it.to = min(len - it.p0, kPage);
+    if (page < first / kPage || it.p0 >= len) {  // runs that overlap (reported where they are read)
+      it.from = it.to = 0;
+    } else {
+      it.phys = a.block_table[static_cast<size_t>(run) * a.max_pages + page];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = t8 + 8 * i;
+        if (t >= it.from && t < it.to) {
+          const long long row = s_row[run] + (it.p0 + t - first);
+          it.k[i].load(a.kin, row * a.k_stride + it.h * kHeadDim + ch);
+          it.v[i].load(a.vin, row * a.v_stride + it.h * kHeadDim + ch);
+        } else {
+          it.k[i].zero();
+          it.v[i].zero();
+        }
+      }
+    }
+    pi += step_pi;
+    next_h += step_h;
+    if (next_h >= a.H) {
+      next_h -= a.H;
+      ++pi;
+    }
+  };
+  Item it;
+  if (blockIdx.x < items) fetch(it);
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int h = it.h, from = it.from, phys = it.phys;
+    const bool here = it.to > from;
+    float x[2][2][8];  // [plane][token t8, t8 + 8][channel]
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      it.k[i].values(x[0][i]);
+      it.v[i].values(x[1][i]);
+    }
+    uint32_t top_k = max(it.k[0].top(), it.k[1].top()), top_v = max(it.v[0].top(), it.v[1].top());
+    if (item + gridDim.x < items) fetch(it);
+    if (!here) continue;
     if (phys < 0 || phys >= a.num_pages) {
       if (tid == 0) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
       continue;
@@ -181,21 +256,6 @@ __global__ void __launch_bounds__(kThreads, 8) append_runs_kernel(const AppendAr
     const size_t tile = (static_cast<size_t>(phys) * a.H + h) * kTile;
     const size_t si = static_cast<size_t>(h) * a.num_pages + phys;
 
-    float x[2][2][8];  // [plane][token t8, t8 + 8][channel]
-    bool odd = false;
-    float mk = 0.f, mv = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = t8 + 8 * i;
-      if (t >= from && t < to) {
-        const long long row = r.row0 + (p0 + t - first);
-        load8<BF16>(a.kin, row * a.k_stride + h * kHeadDim + ch, x[0][i]);
-        load8<BF16>(a.vin, row * a.v_stride + h * kHeadDim + ch, x[1][i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[0][i][e] = x[1][i][e] = 0.f;
-      }
-    }
     int ek0 = kMinExp, ev0 = kMinExp;
     constexpr uint32_t kZero = INT8 ? 0x80808080u : 0u;
     uint4 wk = make_uint4(kZero, kZero, kZero, kZero), wv = wk;
@@ -205,27 +265,31 @@ __global__ void __launch_bounds__(kThreads, 8) append_runs_kernel(const AppendAr
       wk = *reinterpret_cast<const uint4*>(a.k + tile + 16 * tid);
       wv = *reinterpret_cast<const uint4*>(a.v + tile + 16 * tid);
     }
+    bool odd = false;
+    if (max(top_k, top_v) >= 0x7F800000u) {  // something is not finite here
+      float mk = 0.f, mv = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      mk = fmaxf(mk, amax8(x[0][i], odd));
-      mv = fmaxf(mv, amax8(x[1][i], odd));
+      for (int i = 0; i < 2; ++i) {
+        mk = fmaxf(mk, amax8(x[0][i], odd));
+        mv = fmaxf(mv, amax8(x[1][i], odd));
+      }
+      top_k = __float_as_uint(mk);
+      top_v = __float_as_uint(mv);
+      report(a.err, KVQ_ERR_NONFINITE_INPUT);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-    }
+    top_k = __reduce_max_sync(0xffffffffu, top_k);
+    top_v = __reduce_max_sync(0xffffffffu, top_v);
     if (lane == 0) {
-      s_max[0][warp] = mk;
-      s_max[1][warp] = mv;
+      s_max[0][warp] = top_k;
+      s_max[1][warp] = top_v;
     }
-    if (odd) report(a.err, KVQ_ERR_NONFINITE_INPUT);
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      mk = fmaxf(mk, s_max[0][w]);
-      mv = fmaxf(mv, s_max[1][w]);
+      top_k = max(top_k, s_max[0][w]);
+      top_v = max(top_v, s_max[1][w]);
     }
+    const float mk = __uint_as_float(top_k), mv = __uint_as_float(top_v);
     constexpr float kTop = (INT8 ? 127.f : 448.f) * 32768.f;
     if (tid == 0 && (mk > kTop || mv > kTop)) report(a.err, KVQ_ERR_RANGE);
     const int ek = max(exponent_for<INT8>(mk), ek0), ev = max(exponent_for<INT8>(mv), ev0);
@@ -369,7 +433,7 @@ extern "C" kvq_status kvq_append_runs(const kvq_cache* cache, const void* k, int
   // pages touched: at most one per row, and a run of n tokens touches at most (n + 14) / 16 + 1
   const long long pages = std::min<long long>(num_rows, num_rows / kPage + 2ll * batch);
   const long long items = pages * cache->num_kv_heads;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(items, 152 * 8));
+  const unsigned grid = static_cast<unsigned>(std::min<long long>(items, 152 * 6));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = in_dtype == KVQ_DTYPE_BF16;
   const cudaError_t e = cache->k_fmt == KVQ_FMT_INT8_PAGE ? launch<true>(a, bf16, grid, s) : launch<false>(a, bf16, grid, s);
