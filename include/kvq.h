@@ -44,6 +44,8 @@ extern "C" {
 /* Largest num_kv_heads and batch kvq_decode_attn accepts (larger values: KVQ_ERR_INVALID_ARG). */
 #define KVQ_MAX_KV_HEADS 128
 #define KVQ_MAX_BATCH 1024
+/* Longest context (tokens) of the runs' calls: kvq_map_runs, kvq_append_runs, kvq_attn_runs. */
+#define KVQ_MAX_CONTEXT (1 << 30)
 #define KVQ_VERSION 1
 
 /* A cudaStream_t, declared without the CUDA headers. */
@@ -432,7 +434,7 @@ kvq_status kvq_meter(const float* meter_state_dev, int32_t n_layers, int32_t bat
  * run_starts_dev == NULL: every request brings one token (num_rows == batch, row s is request s).  Rows behind the
  * last run are left as they are, so num_rows can be the fixed size of a captured step.  A run that cannot be (outside
  * [0, num_rows], longer than max_run, a length outside [0, 16 max_pages_per_seq]) is reported as
- * KVQ_ERR_DEVICE_BOUNDS and skipped.  batch <= KVQ_MAX_BATCH.  Two runs of one call must not overlap or share a page that
+ * KVQ_ERR_DEVICE_BOUNDS and skipped.  batch <= KVQ_MAX_BATCH, contexts <= KVQ_MAX_CONTEXT tokens.  Two runs of one call must not overlap or share a page that
  * either of them writes.
  */
 
@@ -495,8 +497,11 @@ size_t kvq_attn_runs_workspace_size(int32_t batch, int32_t num_rows, int32_t max
  * max_run: no run of the call is longer; it chooses the kernels and sizes the workspace.
  * out_dev: [num_rows][num_q_heads][128] in the queries' type.  lse_dev (nullable): [num_rows][num_q_heads] fp32,
  *   ln sum_t e^{x_t}.  A row that sees no token (an empty context) gives 0 and -inf.
- * BF16 queries: the softmax weights are rounded to fp16 (11 bits) before the value product, everything else is exact or
- *   binary32.  F32 queries: queries and weights are carried in two fp16 parts (22 bits).
+ * BF16 queries: the softmax weights are rounded to fp16 (11 bits; weights below 2^-21 of the largest, page scale included,
+ *   to a step of 2^-31 of it) before the value product, everything else is exact or binary32.  F32 queries: queries and
+ *   weights are carried in two fp16 parts (22 bits).  Products are summed in binary32; the same call gives the same bits.
+ * Device errors: KVQ_ERR_DEVICE_BOUNDS (a run that cannot be; a page outside the cache, which is left out of its request's
+ *   sums), KVQ_ERR_TIMEOUT.
  * workspace_dev: at least kvq_attn_runs_workspace_size() bytes, 16-byte aligned; calls that can run at the same time
  *   need one each.
  */

@@ -206,12 +206,12 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) append_runs_kernel(con
   }
   auto fetch = [&](Item& it) {
     while (run + 1 < a.batch && s_cum[run + 1] <= pi) ++run;
-    const int first = s_first[run], len = s_len[run], page = first / kPage + (pi - s_cum[run]);
+    const int first = s_first[run], len = s_len[run], nth = pi - s_cum[run], page = first / kPage + nth;
     it.h = next_h;
     it.p0 = page * kPage;
     it.from = max(first - it.p0, 0);
     it.to = min(len - it.p0, kPage);
-    if (page < first / kPage || it.p0 >= len) {  // runs that overlap (reported where they are read)
+    if (nth < 0 || len <= 0 || nth > (len - 1) / kPage - first / kPage) {  // sums that overlapping runs have wrapped
       it.from = it.to = 0;
     } else {
       it.phys = a.block_table[static_cast<size_t>(run) * a.max_pages + page];

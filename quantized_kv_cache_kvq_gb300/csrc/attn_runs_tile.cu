@@ -878,6 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == kMmaWarp) mma_role(t, smem_u32(smem), tmem);
   }
+  if (*reinterpret_cast<volatile int*>(&t->abort)) __nanosleep(1000000);  // products already issued come to their end
   __syncwarp();
   fence_before();
   __syncthreads();

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     add = a.new_lens[tid];
     gone = add < 0;
     if (gone) add = 0;
-    const long long cap = static_cast<long long>(a.max_pages) * kPage;
+    const long long cap = min(static_cast<long long>(a.max_pages) * kPage, static_cast<long long>(kMaxContext));
     bad = old < 0 || old > cap || static_cast<long long>(old) + add > cap;
   }
   const int held = bad ? 0 : (old + kPage - 1) / kPage;

@@ -9,6 +9,7 @@ namespace kvq {
 namespace runs {
 
 constexpr int kMaxBatch = KVQ_MAX_BATCH;
+constexpr int kMaxContext = KVQ_MAX_CONTEXT;  // positions and their sums with a tile stay below 2^31
 // Exponents of the page scales 2^e: the powers of two that fp16 holds (2^-24 is its smallest subnormal).
 constexpr int kMinExp = -24, kMaxExp = 15;
 
@@ -20,7 +21,8 @@ __device__ __forceinline__ Run load_run(const int32_t* run_starts, const int32_t
                                         int max_pages) {
   const int a = run_starts ? run_starts[s] : s, b = run_starts ? run_starts[s + 1] : s + 1;
   const int len = seq_lens[s];
-  if (a < 0 || b < a || b > num_rows || b - a > max_run || len < 0 || len > static_cast<long long>(max_pages) * kPage)
+  if (a < 0 || b < a || b > num_rows || b - a > max_run || len < 0 || len > kMaxContext ||
+      len > static_cast<long long>(max_pages) * kPage)
     return Run{-1, 0, 0};
   return Run{a, b - a, len};
 }

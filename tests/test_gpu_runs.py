@@ -356,6 +356,17 @@ def test_a_page_outside_the_cache_is_reported_and_the_others_are_right(kvq, new,
         assert kw["err"].item() == 5
         starts = starts_of(new)
         assert torch.equal(out[:starts[bad]], ref[:starts[bad]]) and torch.equal(out[starts[bad + 1]:], ref[starts[bad + 1]:])
+        # the request itself: its other tokens
+        codes = [unpack(p.cpu().numpy(), 2, "e4m3p", n) for p, n in ((cache.k, "k"), (cache.v, "v"))]
+        pages = table[bad, 1:4].cpu().numpy()
+        k, v = ((R.values(c[pages], "e4m3p") * sc.cpu().double().numpy().T[pages][:, :, None, None]).transpose(1, 0, 2, 3).reshape(2, -1, 128)
+                for c, sc in zip(codes, (cache.k_scale, cache.v_scale)))
+        row, pos = starts[bad + 1] - 1, 60 - 16  # its last query sees tokens 16 .. 59
+        for h in range(8):
+            x = k[h // 4, :pos] @ q[row, h].double().cpu().numpy() / 128 ** 0.5
+            w = np.exp(x - x.max())
+            want = w @ v[h // 4, :pos] / w.sum()
+            assert np.linalg.norm(out[row, h].double().cpu().numpy() - want) <= 0.01 * np.linalg.norm(want)
 
 
 def test_runs_that_cannot_be_are_skipped(kvq):
@@ -504,3 +515,94 @@ def test_two_streams_with_a_workspace_each(kvq):
     torch.cuda.synchronize()
     for (a, _), ref in zip(cases, refs):
         assert torch.equal(a[4], ref)
+
+# ------------------------------------------------------------------------------------------------ limits
+def test_offsets_past_32_bits(kvq):
+    """Pages whose tiles lie beyond 4 GB of their plane, written and read."""
+    H, G, pages = 8, 2, (1 << 32) // (8 * 2048) + 40
+    for fmt in FMTS:
+        cache = kvq.PagedCache(fmt, fmt, H, pages)
+        assert cache.k.numel() > 1 << 32
+        n = 50
+        real = pages - 1 - np.arange(4)
+        table, local = dev([real]), np.array([[0, 1, 2, 3]], dtype=np.int32)
+        x = torch.randn(n, 2 * H + H * G, 128, device="cuda").bfloat16()
+        y = x.double().cpu().numpy()
+        err = err_word()
+        kvq.append_runs(cache, x[:, :H], x[:, H:2 * H], dev([n]), table, run_starts=dev([0, n]), err=err)
+        ck, cv = np.zeros((4, H, 16, 128), np.int64), np.zeros((4, H, 16, 128), np.int64)
+        ek, ev = np.zeros((4, H), np.int64), np.zeros((4, H), np.int64)
+        R.append_runs(ck, ek, y[:, :H], [0, n], [n], local, fmt)
+        R.append_runs(cv, ev, y[:, H:2 * H], [0, n], [n], local, fmt)
+        tiles = cache.k.view(pages, H, 2048)[torch.as_tensor(real.copy())].cpu().numpy()
+        assert np.array_equal(unpack(tiles.reshape(-1, 2048), H, fmt, "k"), ck)
+        q = x[:, 2 * H:]
+        for rows in (n, 1):  # as a prompt and as one token
+            out = torch.empty(rows, H * G, 128, dtype=torch.bfloat16, device="cuda")
+            ws = torch.empty(kvq.attn_runs_workspace_size(1, rows, rows, H, H * G, q.dtype), dtype=torch.uint8, device="cuda")
+            kvq.attn_runs(cache, q[n - rows:], dev([n]), table, out, ws, run_starts=dev([0, rows]), max_run=rows, err=err)
+            want, _, pv, xa, low = R.attend(ck, ek, cv, ev, y[n - rows:, 2 * H:], [0, rows], [n], local, 128 ** -0.5, fmt)
+            assert np.all(np.abs(out.double().cpu().numpy() - want) <= attn_tolerance(want, pv, xa, low, True))
+        assert err.item() == 0
+        del cache, tiles
+
+
+def test_a_context_past_the_limit_is_refused(kvq):
+    wide = torch.zeros(1, (1 << 26) + 1, dtype=torch.int32, device="cuda")
+    cache = kvq.PagedCache("int8p", "int8p", 1, 1)
+    x = torch.randn(1, 4, 128, device="cuda").bfloat16()
+    out = torch.full((1, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(kvq.attn_runs_workspace_size(1, 1, 1, 1, 4, x.dtype), dtype=torch.uint8, device="cuda")
+    err = err_word()
+    kvq.attn_runs(cache, x, dev([(1 << 30) + 1]), wide, out, ws, err=err)
+    assert err.item() == 5 and torch.all(out == 7)
+    err.zero_()
+    before = cache.k.clone()
+    kvq.append_runs(cache, x[:, :1], x[:, 1:2], dev([(1 << 30) + 1]), wide, err=err)
+    assert err.item() == 5 and torch.equal(cache.k, before)
+    err.zero_()
+    lens, count, starts = dev([1 << 30]), dev([2]), dev([9, 9])
+    kvq.map_runs(dev([1]), lens, dev([0, 0]), count, wide, starts, lens, count, err=err)
+    assert err.item() == 5 and lens.tolist() == [1 << 30] and starts.tolist() == [0, 0] and count.tolist() == [2]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_batch(kvq, dtype):
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 40, 1024)
+    attention_case(kvq, "int8p", dtype, lens, [1] * 1024, 1, 2)
+    new = np.minimum(lens, rng.integers(0, 4, 1024))
+    new[[3, 700]] = np.minimum(lens[[3, 700]], 30)
+    attention_case(kvq, "e4m3p", dtype, lens, new, 1, 2, max_run=30)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [2, 1], [90, 200]])
+def test_the_same_call_gives_the_same_bits(kvq, new):
+    (cache, q, lens, table, out, ws), kw = attention_case(kvq, "e4m3p", "bf16", [3000, 700], new, 4, 4)
+    ref, ref_lse = out.clone(), kw["lse"].clone()
+    for fill in (0, 255, 127):  # whatever the workspace holds
+        ws.fill_(fill)
+        out.fill_(0)
+        kvq.attn_runs(cache, q, lens, table, out, ws, **kw)
+        assert torch.equal(out, ref) and torch.equal(kw["lse"], ref_lse)
+
+
+def test_a_cache_without_pages(kvq):
+    """Nothing can be read: every entry is outside the cache."""
+    cache = kvq.PagedCache.over("int8p", "int8p", 1, 0, k=torch.empty(0, 2048, dtype=torch.uint8, device="cuda"),
+                                v=torch.empty(0, 2048, dtype=torch.uint8, device="cuda"),
+                                k_scale=torch.empty(1, 0, dtype=torch.float16, device="cuda"),
+                                v_scale=torch.empty(1, 0, dtype=torch.float16, device="cuda"))
+    q = torch.randn(40, 4, 128, device="cuda").bfloat16()
+    ws = torch.empty(kvq.attn_runs_workspace_size(1, 40, 40, 1, 4, q.dtype), dtype=torch.uint8, device="cuda")
+    with pytest.raises(kvq.KvqError):  # planes of nothing have no address
+        kvq.attn_runs(cache, q, dev([40]), dev([[0, 0, 0]]), torch.empty_like(q), ws, run_starts=dev([0, 40]), max_run=40)
+
+
+def test_empty_calls(kvq):
+    cache = kvq.PagedCache("int8p", "int8p", 2, 2)
+    x = torch.empty(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    kvq.append_runs(cache, x, x, dev([]), dev(np.zeros((0, 1))))
+    kvq.attn_runs(cache, x, dev([]), dev(np.zeros((0, 1))), torch.empty_like(x), ws)
+    torch.cuda.synchronize()
