@@ -13,7 +13,8 @@
 // Bound by memory: 512 (bf16) or 1024 (fp32) bytes read and 256 written for every token and kv head.  A value tile's 16-byte
 // words hold four tokens of four channels, which lie in eight threads: they are put together by shuffles (byte stores into
 // the staged tile, with their bank conflicts, took 27 us on 11996 tokens of 8 heads).  A block fetches its next item while it
-// quantizes one: 18.5 us there, of which 10.9 are its bytes at the copy rate and about 10 its instructions.
+// quantizes one: 20.6 us there with inputs that are not in the L2, against 10.9 for the bytes at the copy rate; about 10 us
+// are issue slots (2,100 instructions of a warp for an item).
 #include <algorithm>
 
 #include "runs.cuh"
@@ -83,16 +84,12 @@ __device__ __forceinline__ uint4 rescale(uint4 w, float f) {  // 16 codes times 
 // eight channels of one row, as loaded and as values
 template <bool BF16>
 struct Raw {
-  uint4 w[BF16 ? 1 : 2];
-  __device__ __forceinline__ void load(const void* base, long long at) {
-    const uint4* p = BF16 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at)
-                          : reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
+  static constexpr int kWords = BF16 ? 1 : 2;
+  uint4 w[kWords];
+  // from this thread's words of a stage, kThreads words apart
+  __device__ __forceinline__ void load(const uint4* stage) {
 #pragma unroll
-    for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = p[i];
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kWords; ++i) w[i] = stage[i * kThreads];
   }
   // Largest magnitude, as binary32 bits: as integers, a NaN is above infinity and that above what is finite.
   __device__ __forceinline__ uint32_t top() const {
@@ -141,10 +138,38 @@ __device__ __forceinline__ float amax8(float (&x)[8], bool& odd) {
   return m;
 }
 
+// Asynchronous copies to the issuing thread's own words of shared memory (nothing but their wait is needed to read them back).
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, bool there) {  // zeros where there is nothing
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(int* dst, const int* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int kStages = 2;  // an item on its way while one is quantized
+// Blocks on an SM.  11996 tokens of 8 heads, bf16, inputs not in the L2: 20.6 us with 6 blocks and 2 stages, 22.4 with 7 and
+// 2, 22.3 with 6 and 3, 21.5 with 5 and 3, 28.6 with 8 and 3 (64 registers do not hold the loop).
+constexpr int kBlocksBf16 = 6, kBlocksF32 = 4;
+template <bool BF16>
+__host__ __device__ constexpr int stage_bytes() {
+  return kThreads * (4 * Raw<BF16>::kWords * 16 + 4);  // [plane][token][word][thread] and the page's table entry
+}
+
 template <bool INT8, bool BF16>
-__global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) append_runs_kernel(const AppendArgs a) {
-  __shared__ int s_cum[kMaxBatch + 1];                 // pages of the runs before
-  __shared__ int s_first[kMaxBatch], s_len[kMaxBatch], s_row[kMaxBatch];  // the run's first position, its context, its first row
+__global__ void __launch_bounds__(kThreads, BF16 ? kBlocksBf16 : kBlocksF32) append_runs_kernel(const AppendArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* stages = smem;
+  int* s_cum = reinterpret_cast<int*>(smem + kStages * stage_bytes<BF16>());  // [batch + 1] pages of the runs before
+  int* s_first = s_cum + a.batch + 1;                                         // the run's first position,
+  int* s_len = s_first + a.batch;                                             // its context,
+  int* s_row = s_len + a.batch;                                               // its first row
   __shared__ int s_warp[kThreads / 32];
   __shared__ uint32_t s_max[2][kThreads / 32];
   __shared__ __align__(16) uint8_t s_tile[2][kTile];
@@ -190,65 +215,89 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) append_runs_kernel(con
 
   const long long items = static_cast<long long>(s_cum[a.batch]) * a.H;
   const int t8 = tid >> 4, ch = (tid & 15) * 8;
-  struct Item {
-    int h, p0, from, to, phys;  // kv head, the page's first position, its new tokens [from, to), physical page
-    Raw<BF16> k[2], v[2];       // this thread's tokens t8, t8 + 8
+  // Where an item lies; blocks go through the items in steps of the grid.
+  struct Walk {
+    int pi, h, run;  // page (of all runs'), kv head, run
   };
-  // Everything that an item reads without waiting for it: it is the next one's while this one is quantized.
-  int pi = blockIdx.x / a.H, next_h = blockIdx.x % a.H, run = 0;  // page and kv head of the item to fetch, run of the page
   const int step_pi = gridDim.x / a.H, step_h = gridDim.x % a.H;
+  auto advance = [&](Walk& w) {
+    w.pi += step_pi;
+    w.h += step_h;
+    if (w.h >= a.H) {
+      w.h -= a.H;
+      ++w.pi;
+    }
+    while (w.run + 1 < a.batch && s_cum[w.run + 1] <= w.pi) ++w.run;
+  };
+  struct Page {
+    int first, p0, from, to, page;  // the run's first position, the page's, its new tokens [from, to), its index
+  };
+  auto page_at = [&](const Walk& w) {
+    const int first = s_first[w.run], len = s_len[w.run], nth = w.pi - s_cum[w.run], page = first / kPage + nth;
+    if (nth < 0 || len <= 0 || nth > (len - 1) / kPage - first / kPage) return Page{0, 0, 0, 0, 0};  // wrapped sums of overlapping runs
+    return Page{first, page * kPage, max(first - page * kPage, 0), min(len - page * kPage, kPage), page};
+  };
+  Walk ahead{static_cast<int>(blockIdx.x / a.H), static_cast<int>(blockIdx.x % a.H), 0};
   {
     int hi = a.batch - 1;  // last run with cum <= pi
-    while (run < hi) {
-      const int mid = (run + hi + 1) >> 1;
-      if (s_cum[mid] <= pi) run = mid; else hi = mid - 1;
+    while (ahead.run < hi) {
+      const int mid = (ahead.run + hi + 1) >> 1;
+      if (s_cum[mid] <= ahead.pi) ahead.run = mid; else hi = mid - 1;
     }
   }
-  auto fetch = [&](Item& it) {
-    while (run + 1 < a.batch && s_cum[run + 1] <= pi) ++run;
-    const int first = s_first[run], len = s_len[run], nth = pi - s_cum[run], page = first / kPage + nth;
-    it.h = next_h;
-    it.p0 = page * kPage;
-    it.from = max(first - it.p0, 0);
-    it.to = min(len - it.p0, kPage);
-    if (nth < 0 || len <= 0 || nth > (len - 1) / kPage - first / kPage) {  // sums that overlapping runs have wrapped
-      it.from = it.to = 0;
-    } else {
-      it.phys = a.block_table[static_cast<size_t>(run) * a.max_pages + page];
+  Walk here = ahead;
+  constexpr int kWords = Raw<BF16>::kWords;
+  auto words_of = [&](int stage) { return reinterpret_cast<uint4*>(stages + stage * stage_bytes<BF16>()) + tid; };
+  auto entry_of = [&](int stage) { return reinterpret_cast<int*>(stages + stage * stage_bytes<BF16>() + kThreads * 4 * kWords * 16) + tid; };
+  auto fetch = [&](long long item, int stage) {
+    if (item < items) {
+      const Page p = page_at(ahead);
+      uint4* dst = words_of(stage);
+      copy4(entry_of(stage), a.block_table + static_cast<size_t>(ahead.run) * a.max_pages + p.page);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = t8 + 8 * i;
-        if (t >= it.from && t < it.to) {
-          const long long row = s_row[run] + (it.p0 + t - first);
-          it.k[i].load(a.kin, row * a.k_stride + it.h * kHeadDim + ch);
-          it.v[i].load(a.vin, row * a.v_stride + it.h * kHeadDim + ch);
-        } else {
-          it.k[i].zero();
-          it.v[i].zero();
+        const bool there = t >= p.from && t < p.to;
+        const long long row = there ? s_row[ahead.run] + (p.p0 + t - p.first) : 0;
+        const int col = ahead.h * kHeadDim + ch;
+        constexpr int kSize = BF16 ? 2 : 4;
+        const uint8_t* ks = static_cast<const uint8_t*>(a.kin) + (row * a.k_stride + col) * kSize;
+        const uint8_t* vs = static_cast<const uint8_t*>(a.vin) + (row * a.v_stride + col) * kSize;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          copy16(dst + (i * kWords + w) * kThreads, ks + 16 * w, there);
+          copy16(dst + ((2 + i) * kWords + w) * kThreads, vs + 16 * w, there);
         }
       }
+      advance(ahead);
     }
-    pi += step_pi;
-    next_h += step_h;
-    if (next_h >= a.H) {
-      next_h -= a.H;
-      ++pi;
-    }
+    copies_commit();
   };
-  Item it;
-  if (blockIdx.x < items) fetch(it);
+  for (int i = 0; i < kStages - 1; ++i) fetch(blockIdx.x + static_cast<long long>(i) * gridDim.x, i);
+  int stage = 0;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int h = it.h, from = it.from, phys = it.phys;
-    const bool here = it.to > from;
+    fetch(item + static_cast<long long>(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);
+    copies_wait<kStages - 1>();
+    const Page page = page_at(here);
+    const int h = here.h, from = page.from, phys = *entry_of(stage);
+    advance(here);
     float x[2][2][8];  // [plane][token t8, t8 + 8][channel]
+    uint32_t top_k = 0, top_v = 0;
+    {
+      const uint4* src = words_of(stage);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      it.k[i].values(x[0][i]);
-      it.v[i].values(x[1][i]);
+      for (int i = 0; i < 2; ++i) {
+        Raw<BF16> k, v;
+        k.load(src + i * kWords * kThreads);
+        v.load(src + (2 + i) * kWords * kThreads);
+        k.values(x[0][i]);
+        v.values(x[1][i]);
+        top_k = max(top_k, k.top());
+        top_v = max(top_v, v.top());
+      }
     }
-    uint32_t top_k = max(it.k[0].top(), it.k[1].top()), top_v = max(it.v[0].top(), it.v[1].top());
-    if (item + gridDim.x < items) fetch(it);
-    if (!here) continue;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    if (page.to <= from) continue;
     if (phys < 0 || phys >= a.num_pages) {
       if (tid == 0) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
       continue;
@@ -387,10 +436,21 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 6 : 5) append_runs_kernel(con
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <bool INT8>
-cudaError_t launch(const AppendArgs& a, bool bf16, unsigned grid, cudaStream_t s) {
-  if (bf16) append_runs_kernel<INT8, true><<<grid, kThreads, 0, s>>>(a);
-  else append_runs_kernel<INT8, false><<<grid, kThreads, 0, s>>>(a);
+template <bool INT8, bool BF16>
+cudaError_t launch(const AppendArgs& a, long long items, cudaStream_t s) {
+  auto kern = append_runs_kernel<INT8, BF16>;
+  const size_t smem = kStages * stage_bytes<BF16>() + (4 * static_cast<size_t>(a.batch) + 1) * sizeof(int);
+  static size_t configured[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices || smem > configured[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) configured[dev] = smem;
+  }
+  // as many blocks as the SMs hold (152 SMs), each going through its share of the items
+  kern<<<static_cast<unsigned>(std::min<long long>(items, 152 * (BF16 ? kBlocksBf16 : kBlocksF32))), kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -433,9 +493,9 @@ extern "C" kvq_status kvq_append_runs(const kvq_cache* cache, const void* k, int
   // pages touched: at most one per row, and a run of n tokens touches at most (n + 14) / 16 + 1
   const long long pages = std::min<long long>(num_rows, num_rows / kPage + 2ll * batch);
   const long long items = pages * cache->num_kv_heads;
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(items, 152 * 6));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = in_dtype == KVQ_DTYPE_BF16;
-  const cudaError_t e = cache->k_fmt == KVQ_FMT_INT8_PAGE ? launch<true>(a, bf16, grid, s) : launch<false>(a, bf16, grid, s);
+  const cudaError_t e = cache->k_fmt == KVQ_FMT_INT8_PAGE ? (bf16 ? launch<true, true>(a, items, s) : launch<true, false>(a, items, s))
+                                                          : (bf16 ? launch<false, true>(a, items, s) : launch<false, false>(a, items, s));
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
