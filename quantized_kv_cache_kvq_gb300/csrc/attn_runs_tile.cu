@@ -37,8 +37,7 @@ constexpr int kSlots = 5;       // ring of operand tiles
 constexpr int kOperand = 32768;  // 128 x 128 fp16
 constexpr int kSoftmaxWarps = 16, kConvertWarp = 16, kMmaWarp = 24;  // first warps of the roles
 constexpr int kThreads = 28 * 32;
-// Registers: 80 a thread at launch; the converting warps hold two operand tiles in flight, and of the last warpgroup only
-// one warp works, issuing products.  None of the loops may spill: with 227 KB of shared memory the L1 keeps nothing, and a
+// Registers: 72 a thread at launch; the softmax warps take what the last warpgroup, of which only one warp works, gives back.  None of the loops may spill: with 227 KB of shared memory the L1 keeps nothing, and a
 // spilled value costs ~500 clocks a use.
 constexpr int kRegsSoftmax = 80, kRegsConvert = 72, kRegsMma = 40;
 static_assert(16 * kRegsSoftmax + 8 * kRegsConvert + 4 * kRegsMma <= 28 * 72, "no more than the block was launched with");
@@ -46,7 +45,7 @@ constexpr int kScaleSlots = 3;  // a tile's scales are read until its V slot is 
 constexpr float kTileShift = 7.f;  // weights are held times 2^7 ..
 constexpr float kSlack = 8.f;      // .. and may grow to 2^15 before the running maximum (and O) is moved
 constexpr int kOffQ = 0, kOffRing = 2 * kOperand, kOffTail = kOffRing + kSlots * kOperand;
-constexpr int kTailBytes = 3072;
+constexpr int kTailBytes = 3 * 1024;
 constexpr int kSmemBytes = kOffTail + kTailBytes;
 constexpr uint32_t kIdesc = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);  // fp16 x fp16 -> fp32, M = N = 128
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // columns: S (and P) of the two halves, then O
