@@ -434,8 +434,8 @@ kvq_status kvq_meter(const float* meter_state_dev, int32_t n_layers, int32_t bat
  * run_starts_dev == NULL: every request brings one token (num_rows == batch, row s is request s).  Rows behind the
  * last run are left as they are, so num_rows can be the fixed size of a captured step.  A run that cannot be (outside
  * [0, num_rows], longer than max_run, a length outside [0, 16 max_pages_per_seq]) is reported as
- * KVQ_ERR_DEVICE_BOUNDS and skipped.  batch <= KVQ_MAX_BATCH, contexts <= KVQ_MAX_CONTEXT tokens.  Two runs of one call must not overlap or share a page that
- * either of them writes.
+ * KVQ_ERR_DEVICE_BOUNDS and skipped.  batch <= KVQ_MAX_BATCH, contexts <= KVQ_MAX_CONTEXT tokens.  Two runs of one call
+ * must not overlap or share a page that either of them writes; requests may share pages that are only read.
  */
 
 /*
@@ -453,6 +453,8 @@ kvq_status kvq_meter(const float* meter_state_dev, int32_t n_layers, int32_t bat
  *   needs it) or other buffers.  No other two buffers may overlap.
  * slot_mapping_dev, positions_dev (both nullable): [max_rows] int32; row r's slot (page 16 + offset, as kvq_append
  *   takes it) and position; rows behind the last run get slot -1 (which kvq_append skips) and position 0.
+ * A request that gives up its last tokens (a rejected draft) has its length set back by the caller; pages that lie wholly
+ *   behind the new length are the caller's to push back, or they are lost when the request grows again.
  * All or nothing: with too few pages (KVQ_ERR_NO_PAGES), more than max_rows tokens, a length outside
  *   [0, 16 max_pages_per_seq] before or after, or a stack height outside [0, free_capacity] (KVQ_ERR_DEVICE_BOUNDS) nothing
  *   is handed out or back: the state is copied, run_starts and positions are 0 and slots -1.
@@ -475,6 +477,7 @@ kvq_status kvq_map_runs(const int32_t* new_lens_dev, const int32_t* seq_lens_dev
  *   by d, the codes already in the page become rne(code 2^-d): exact for E4M3 down to its subnormals; for INT8 the errors
  *   of all such steps sum to less than one step of the final scale.  The page's slots behind the run get code 0.
  * A page that starts inside the run (or at its first token) is written whole, whatever it held before.
+ * A request whose length was set back goes on from there: the page's scale stays, the codes behind are cleared.
  * Device errors: KVQ_ERR_DEVICE_BOUNDS (a page outside the cache, a run longer than its context: skipped),
  *   KVQ_ERR_NONFINITE_INPUT (a NaN is stored as 0, an infinity as the largest code; neither counts in amax),
  *   KVQ_ERR_RANGE (amax > qmax 2^15: the codes saturate).

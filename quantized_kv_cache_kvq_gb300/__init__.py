@@ -7,8 +7,10 @@ works without a GPU (so the library can be inspected), but every compute call
 needs the built ``libkvq.so`` and a CUDA device, and raises otherwise.
 
 Entry points mirror the C names: ``append``, ``decode_attn``, ``meter``,
-``decode_workspace_size``, ``debug_dither``, ``debug_encode``, plus the
-``PagedCache`` helper that owns one layer's planes.
+``decode_workspace_size``, ``debug_dither``, ``debug_encode``, those of the
+runs (``map_runs``, ``append_runs``, ``attn_runs`` and
+``attn_runs_workspace_size``), plus the ``PagedCache`` helper that owns one
+layer's planes.
 """
 from __future__ import annotations
 
@@ -255,14 +257,10 @@ class PagedCache:
             self.outlier_pairs = outlier_pairs.to(device).contiguous()
             self.k_outlier = torch.zeros((n, 256 if self.n_out <= 4 else 512), **z)
 
-    _page_desc = None  # a page-scaled cache's descriptor, made once: its planes stay the ones it was made over
-
     def _page_scaled(self, k, v, k_scale, v_scale):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.witness = self.v_witness = self.outlier_pairs = self.k_outlier = None
         self.n_out = 0
-        self._page_desc = _Cache(FMT[self.k_fmt], FMT[self.v_fmt], self.num_kv_heads, self.num_pages, self.layer, 0, 0,
-                                 _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale))
 
     @classmethod
     def over(cls, k_fmt: str, v_fmt: str, num_kv_heads: int, num_pages: int, *, k: torch.Tensor, v: torch.Tensor,
@@ -282,8 +280,10 @@ class PagedCache:
         return c
 
     def desc(self) -> _Cache:
-        if self._page_desc is not None:
-            return self._page_desc
+        if self.k_fmt in PAGE_SCALED:
+            f = FMT[self.k_fmt]
+            return _Cache(f, f, self.num_kv_heads, self.num_pages, self.layer, 0, 0, self.k.data_ptr(), self.v.data_ptr(),
+                          self.k_scale.data_ptr(), self.v_scale.data_ptr())
         return _Cache(FMT[self.k_fmt], FMT[self.v_fmt], self.num_kv_heads, self.num_pages, self.layer, 0,
                       self.seed & 0xFFFFFFFFFFFFFFFF, _ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
                       _ptr(self.v_scale), _ptr(self.witness), _ptr(self.v_witness), _ptr(self.outlier_pairs),
@@ -461,13 +461,20 @@ def _rows(x: torch.Tensor):
     return s0 if rows > 1 else heads * HEAD_DIM
 
 
-def _i32(*tensors):
+def _on(device: int, *tensors):
     for t in tensors:
-        assert t is None or (t.dtype is torch.int32 and t.is_contiguous()), "int32 and contiguous"
+        assert t is None or t.get_device() == device, "one CUDA device"
+
+
+def _i32(device: int, *tensors):
+    for t in tensors:
+        assert t is None or (t.dtype is torch.int32 and t.is_contiguous() and t.get_device() == device), \
+            "int32, contiguous and on one CUDA device"
 
 
 def _launch(name: str, fn, device: int, stream, *args):
     """The call fn(*args, stream) with ``device`` current, on ``stream`` or that device's current stream."""
+    assert device >= 0, "CUDA tensors"
     if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _launch(name, fn, device, stream, *args)
@@ -485,8 +492,9 @@ def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.T
     free_pages [capacity] is the stack of free pages with free_count [1] in use, block_table [B, max_pages]; run_starts
     [B + 1], seq_lens_out [B] and free_count_out [1] are written (the latter two may be the inputs), and slot_mapping and
     positions [max_rows] where given.  All int32 and contiguous."""
-    _i32(new_lens, seq_lens, free_pages, free_count, block_table, run_starts, seq_lens_out, free_count_out, slot_mapping,
-         positions)
+    device = run_starts.get_device()
+    _i32(device, new_lens, seq_lens, free_pages, free_count, block_table, run_starts, seq_lens_out, free_count_out,
+         slot_mapping, positions, err)
     B, width = block_table.shape
     assert new_lens.numel() == B and seq_lens.numel() == B and seq_lens_out.numel() == B and run_starts.numel() == B + 1
     assert free_count.numel() == 1 and free_count_out.numel() == 1
@@ -496,7 +504,7 @@ def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.T
         assert positions is None or positions.numel() == rows
     elif positions is not None:
         rows = positions.numel()
-    _launch("kvq_map_runs", lib().kvq_map_runs, run_starts.get_device(), stream, new_lens.data_ptr(), seq_lens.data_ptr(), B,
+    _launch("kvq_map_runs", lib().kvq_map_runs, device, stream, new_lens.data_ptr(), seq_lens.data_ptr(), B,
             free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), block_table.data_ptr(), width,
             run_starts.data_ptr(), seq_lens_out.data_ptr(), free_count_out.data_ptr(), _ptr(slot_mapping), _ptr(positions),
             rows, _ptr(err))
@@ -508,10 +516,12 @@ def append_runs(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, seq_lens: t
     a page-scaled cache.  run_starts [B + 1]; None: one new token for each request."""
     rows, heads, _ = k.shape
     assert k.dtype == v.dtype and k.shape == v.shape and heads == cache.num_kv_heads
-    _i32(seq_lens, block_table, run_starts)
+    device = k.get_device()
+    _on(device, v, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    _i32(device, seq_lens, block_table, run_starts, err)
     B, width = block_table.shape
     assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)
-    _launch("kvq_append_runs", lib().kvq_append_runs, k.get_device(), stream, ctypes.byref(cache.desc()), k.data_ptr(), _rows(k),
+    _launch("kvq_append_runs", lib().kvq_append_runs, device, stream, ctypes.byref(cache.desc()), k.data_ptr(), _rows(k),
             v.data_ptr(), _rows(v), DTYPE[k.dtype], _ptr(run_starts), B, rows, block_table.data_ptr(), width,
             seq_lens.data_ptr(), _ptr(err))
 
@@ -529,11 +539,13 @@ def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_
     run_starts None: one query token for each request."""
     rows, Hq, _ = q.shape
     assert out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
-    _i32(seq_lens, block_table, run_starts)
+    device = q.get_device()
+    _on(device, out, workspace, lse, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    _i32(device, seq_lens, block_table, run_starts, err)
     B, width = block_table.shape
     assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)
     assert lse is None or (lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() == rows * Hq)
-    _launch("kvq_attn_runs", lib().kvq_attn_runs, q.get_device(), stream, ctypes.byref(cache.desc()), q.data_ptr(), _rows(q),
+    _launch("kvq_attn_runs", lib().kvq_attn_runs, device, stream, ctypes.byref(cache.desc()), q.data_ptr(), _rows(q),
             DTYPE[q.dtype], Hq, _ptr(run_starts), B, rows, max_run, block_table.data_ptr(), width, seq_lens.data_ptr(),
             _SM_SCALE if sm_scale is None else sm_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
             _ptr(err))

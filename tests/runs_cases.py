@@ -56,9 +56,8 @@ def attn_tolerance(out, pv, xa, low, bf16):
     exponent's own rounding adds 2^-22 of the weight (ex2.approx), so each weight is off by d = 2^-17 xa + 2^-21 relative.
     The numerator and the denominator carry it once each, and the value product's binary32 sums add 2^-21 more.
     bf16: weights rounded to fp16 (half a step, 2^-11) and the result to bf16 (2^-8).  fp32: weights in two fp16 parts (2^-22).
-    Weights that are subnormal in fp16 round to multiples of 2^-24: where the largest weight (page scale included) is held as
-    2^12 (single tokens and drafts), that is off by 2^-25-12 of the largest, times the value code; long runs hold it as 2^7
-    or more: 2^-25-7."""
+    Weights that are subnormal in fp16 round to multiples of 2^-24.  bf16: the largest weight (page scale included) is held as
+    2^7 or more, so that is off by 2^-25-7 of the largest, times the value code; fp32 holds it as 2^12 or more: 2^-25-12."""
     d = 2.0 ** -17 * xa[..., None] + 2.0 ** -21
     w = 2 * d + 2.0 ** -21 + (2.0 ** -11 if bf16 else 2.0 ** -22)
     return (2.0 ** -8 if bf16 else 2.0 ** -24) * np.abs(out) + 1.01 * w * pv + (2.0 ** -32 if bf16 else 2.0 ** -37) * low + 1e-30

@@ -176,6 +176,37 @@ def test_append_token_by_token_and_a_reused_page(kvq, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("back", [16, 17, 20, 32])
+def test_append_after_tokens_were_given_up(kvq, fmt, back):
+    """A draft of large values is rejected down to ``back`` tokens: inside a page its scale stays, at a page's start it does not."""
+    rng = np.random.default_rng(back)
+    ck, cv = random_codes(rng, 4, 2, fmt), random_codes(rng, 4, 2, fmt)
+    ek, ev = np.full((4, 2), -5), np.full((4, 2), -5)
+    cache = make_cache(kvq, fmt, 2, 4, ck, cv, ek, ev)
+    table = np.array([[2, 0, 3]], dtype=np.int32)
+    err = err_word()
+    for n, end, size in ((14, 14, 1.0), (21, 35, 40.0), (3, back + 3, 0.5), (1, back + 4, 0.01)):
+        x = (rng.standard_normal((n, 4, 128)) * size).astype(np.float32)
+        R.append_runs(ck, ek, x[:, :2], [0, n], [end], table, fmt)
+        R.append_runs(cv, ev, x[:, 2:], [0, n], [end], table, fmt)
+        d = torch.from_numpy(x).cuda()
+        kvq.append_runs(cache, d[:, :2], d[:, 2:], dev([end]), dev(table), run_starts=dev([0, n]), err=err)
+        check_cache(cache, fmt, 2, ck, cv, ek, ev)
+    assert err.item() == 0
+
+
+def test_a_cache_follows_its_planes(kvq):
+    """Planes put into a cache after it was made are the ones that the calls use."""
+    cache = kvq.PagedCache("int8p", "int8p", 1, 1)
+    old = cache.k, cache.v, cache.k_scale, cache.v_scale
+    cache.k, cache.v, cache.k_scale, cache.v_scale = (t.clone() for t in old)
+    x = torch.ones((1, 1, 128), device="cuda")
+    kvq.append_runs(cache, x, x, dev([1]), dev([[0]]))
+    assert all(t.count_nonzero() == 0 for t in old)
+    assert cache.k_scale.item() == cache.v_scale.item() == 2.0 ** -6  # 127 2^-7 < 1
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("kind,status", [("zeros", 0), ("tiny", 0), ("nan", 6), ("inf", 6), ("huge", 7), ("top", 0), ("bf16max", 7)])
 def test_append_special_values(kvq, fmt, kind, status):
     rng = np.random.default_rng(4)

@@ -104,3 +104,18 @@ def test_empty_calls_do_nothing(kvq):
     assert attn(kvq, c, n=0) == 0 and attn(kvq, c, b=0) == 0
     assert kvq.lib().kvq_attn_runs_workspace_size(1, 1, 1, 2, 3, 1) == 0  # 3 % 2 != 0
     assert kvq.lib().kvq_attn_runs_workspace_size(1025, 1, 1, 2, 4, 1) == 0
+
+
+def test_host_tensors_are_refused(kvq):
+    """Before any pointer reaches the device."""
+    import torch
+
+    z = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    c = kvq.PagedCache("int8p", "int8p", 1, 4, device="cpu")
+    x = torch.zeros((2, 1, 128))
+    with pytest.raises(AssertionError):
+        kvq.map_runs(z(2), z(2), z(4), z(1), z(2, 2), z(3), z(2), z(1))
+    with pytest.raises(AssertionError):
+        kvq.append_runs(c, x, x, z(2), z(2, 2))
+    with pytest.raises(AssertionError):
+        kvq.attn_runs(c, x, z(2), z(2, 2), x.clone(), torch.zeros(4096))
