@@ -354,6 +354,23 @@ def test_sharp_flat_and_negative_scales(kvq, new):
     attention_case(kvq, "e4m3p", "bf16", lens, new, 2, 4, q_scale=1e30, sm_scale=1e-31)
 
 
+CHUNKS = [([20, 100, 129, 257, 384, 513, 641], [5, 20, 9, 17, 20, 32, 31], 2, 4), ([3000, 1000, 5000], [6, 17, 32], 8, 4),
+          ([3000, 900, 2500, 700, 50, 1], [6, 200, 32, 70, 1, 1], 4, 4), ([700, 2000, 300], [17, 128, 129], 3, 1),
+          ([600 + 9 * i for i in range(40)], [3 + i % 14 for i in range(40)], 8, 8)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens,new,heads,group", CHUNKS)
+def test_chunks_of_at_most_128_rows_among_others(kvq, fmt, lens, new, heads, group):
+    """Units of one half, whose key tiles go to the two places in turn: of one tile, of a few, cut anywhere, beside full ones."""
+    attention_case(kvq, fmt, "bf16", lens, new, heads, group, seed=len(lens))
+
+
+@pytest.mark.parametrize("q_scale", [30.0, 1e-3])
+def test_chunks_whose_places_differ_in_maximum(kvq, q_scale):
+    attention_case(kvq, "int8p", "bf16", [2000, 40, 900], [12, 30, 20], 2, 4, seed=5, q_scale=q_scale, exps=(-12, -3))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_several_tiles_and_units_for_every_block(kvq, fmt):
     attention_case(kvq, fmt, "bf16", [2100, 900, 40, 700], [700, 900, 1, 3], 4, 2, behind=5)
