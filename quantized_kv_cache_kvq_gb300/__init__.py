@@ -56,6 +56,7 @@ TIER_A, TIER_B, TIER_V, TIER_S = 1, 2, 4, 8
 METER_STATE_FLOATS = 8  # floats per (sequence, query head) cell of meter_state
 HEAD_DIM, PAGE, N_BANDS = 128, 16, 16
 _SM_SCALE = 1.0 / math.sqrt(HEAD_DIM)
+_INT32 = torch.int32
 
 STATUS = {
     0: "KVQ_OK",
@@ -258,6 +259,7 @@ class PagedCache:
             self.k_outlier = torch.zeros((n, 256 if self.n_out <= 4 else 512), **z)
 
     def _page_scaled(self, k, v, k_scale, v_scale):
+        _on(k.get_device(), v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.witness = self.v_witness = self.outlier_pairs = self.k_outlier = None
         self.n_out = 0
@@ -450,14 +452,12 @@ def meter(meter_state: torch.Tensor, n_layers: int, batch: int, num_q_heads: int
                            _ptr(det_tanh), counts.data_ptr(), _ptr(ranking), _stream(stream)), "kvq_meter")
 
 
-def _rows(x: torch.Tensor):
+def _rows(x: torch.Tensor, rows: int, heads: int) -> int:
     """Row stride of a [rows, heads, 128] tensor whose rows are dense: a slice of a fused projection is taken as it is."""
-    rows, heads, d = x.shape
-    if rows <= 1 and heads <= 1:
-        assert d == HEAD_DIM and x.stride(2) == 1
-        return HEAD_DIM
+    if x.is_contiguous():
+        return heads * HEAD_DIM
     s0, s1, s2 = x.stride()
-    assert d == HEAD_DIM and s2 == 1 and (heads == 1 or s1 == HEAD_DIM)
+    assert s2 == 1 and (heads == 1 or s1 == HEAD_DIM)
     return s0 if rows > 1 else heads * HEAD_DIM
 
 
@@ -468,14 +468,14 @@ def _on(device: int, *tensors):
 
 def _i32(device: int, *tensors):
     for t in tensors:
-        assert t is None or (t.dtype is torch.int32 and t.is_contiguous() and t.get_device() == device), \
+        assert t is None or (t.dtype is _INT32 and t.get_device() == device and t.is_contiguous()), \
             "int32, contiguous and on one CUDA device"
 
 
 def _launch(name: str, fn, device: int, stream, *args):
     """The call fn(*args, stream) with ``device`` current, on ``stream`` or that device's current stream."""
     assert device >= 0, "CUDA tensors"
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _launch(name, fn, device, stream, *args)
     status = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
@@ -514,15 +514,15 @@ def append_runs(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, seq_lens: t
                 *, run_starts: torch.Tensor | None = None, err: torch.Tensor | None = None, stream=None):
     """kvq_append_runs: quantize the runs' keys and values k, v [rows, Hkv, 128] (fp32 or bf16; rows may be strided) into
     a page-scaled cache.  run_starts [B + 1]; None: one new token for each request."""
-    rows, heads, _ = k.shape
-    assert k.dtype == v.dtype and k.shape == v.shape and heads == cache.num_kv_heads
+    rows, heads, d = k.shape
+    assert k.dtype == v.dtype and k.shape == v.shape and heads == cache.num_kv_heads and d == HEAD_DIM
     device = k.get_device()
-    _on(device, v, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    _on(device, v, cache.k)
     _i32(device, seq_lens, block_table, run_starts, err)
     B, width = block_table.shape
     assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)
-    _launch("kvq_append_runs", lib().kvq_append_runs, device, stream, ctypes.byref(cache.desc()), k.data_ptr(), _rows(k),
-            v.data_ptr(), _rows(v), DTYPE[k.dtype], _ptr(run_starts), B, rows, block_table.data_ptr(), width,
+    _launch("kvq_append_runs", lib().kvq_append_runs, device, stream, ctypes.byref(cache.desc()), k.data_ptr(), _rows(k, rows, heads),
+            v.data_ptr(), _rows(v, rows, heads), DTYPE[k.dtype], _ptr(run_starts), B, rows, block_table.data_ptr(), width,
             seq_lens.data_ptr(), _ptr(err))
 
 
@@ -537,15 +537,15 @@ def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_
     """kvq_attn_runs: causal attention of the runs' queries q [rows, Hq, 128] (fp32 or bf16; rows may be strided) over a
     page-scaled cache -> out [rows, Hq, 128] in q's type (+ lse [rows, Hq] fp32).  No run is longer than max_run;
     run_starts None: one query token for each request."""
-    rows, Hq, _ = q.shape
-    assert out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
+    rows, Hq, d = q.shape
+    assert d == HEAD_DIM and out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
     device = q.get_device()
-    _on(device, out, workspace, lse, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    _on(device, out, workspace, lse, cache.k)
     _i32(device, seq_lens, block_table, run_starts, err)
     B, width = block_table.shape
     assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)
     assert lse is None or (lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() == rows * Hq)
-    _launch("kvq_attn_runs", lib().kvq_attn_runs, device, stream, ctypes.byref(cache.desc()), q.data_ptr(), _rows(q),
+    _launch("kvq_attn_runs", lib().kvq_attn_runs, device, stream, ctypes.byref(cache.desc()), q.data_ptr(), _rows(q, rows, Hq),
             DTYPE[q.dtype], Hq, _ptr(run_starts), B, rows, max_run, block_table.data_ptr(), width, seq_lens.data_ptr(),
             _SM_SCALE if sm_scale is None else sm_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
             _ptr(err))

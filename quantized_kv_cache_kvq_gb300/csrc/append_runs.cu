@@ -14,7 +14,7 @@
 // words hold four tokens of four channels, which lie in eight threads: they are put together by shuffles (byte stores into
 // the staged tile, with their bank conflicts, took 27 us on 11996 tokens of 8 heads).  A block fetches its next item while it
 // quantizes one: 20.6 us there with inputs that are not in the L2, against 10.9 for the bytes at the copy rate; about 10 us
-// are issue slots (2,100 instructions of a warp for an item).
+// are issue slots (2,200 instructions of a warp for an item).
 #include <algorithm>
 
 #include "runs.cuh"

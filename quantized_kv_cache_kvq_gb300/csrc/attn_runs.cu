@@ -6,7 +6,9 @@
 // ranges, one per warp of a persistent grid, as in the single-token decode of the other layouts: pages stream through a
 // ring of bulk copies per warp, the page's 16 tokens are the M dimension of every tensor-core product (mma.sync: a page gives
 // each row 2 x 2048 multiply-adds for 4096 bytes, far below where the tensor rate matters), and the pieces are merged
-// with log-sum-exp weights.  Bound by HBM: 4,100 bytes a page and kv head.
+// with log-sum-exp weights.  Bound by HBM: 4,100 bytes a page and kv head.  64 requests of 32768 tokens, 4 kv and 28 query heads,
+// INT8: 349 us, 6,160 GB/s (91 % of the copy rate); 128 of 1024..16384, 8 and 32 heads, E4M3: 265 us, 5,940 GB/s; 16 drafts of
+// 2..4 tokens over 11000..11996, two row blocks a page: 79 us, 4,790 GB/s (dependent products that 12 warps do not hide).
 #include <algorithm>
 #include <cmath>
 

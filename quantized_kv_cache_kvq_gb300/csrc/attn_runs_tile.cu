@@ -5,12 +5,15 @@
 // of a grid of one CTA per SM, so that one long prompt, many short ones and a short chunk behind a long context load the
 // machine alike.  A range may begin or end inside a unit: such pieces leave (m, l, O) in the workspace for the merge.
 //
-// Per key tile and 128-row half of the unit:  S = Q K^T (both from shared memory, S in TMEM), the softmax of one row per
-// thread, P (fp16) over S's columns in TMEM,  O += P V (V from shared memory, O in TMEM).  fp16 operands: codes of either
+// Per key tile and 128-row half of the unit:  S = Q K^T (both from shared memory, S in TMEM), the softmax of a row by two
+// threads, P (fp16) over S's columns in TMEM,  O += P V (V from shared memory, O in TMEM).  fp16 operands: codes of either
 // format are exact in it, a bf16 query is exact after a power of two is taken from its row.  With
-// S = 128 x 128 x 128 at 8192 flop a clock the two halves cost 2048 clocks a tile on the tensor core; what else needs the
-// SM is kept below that: the codes go from global memory through registers to shared memory once for all 256 rows (four
-// converting warps), eight warps do the softmax of one half while the tensor core works on the other.
+// S = 128 x 128 x 128 at 8192 flop a clock the two halves cost 2048 clocks a tile on the tensor core.  The codes go from global
+// memory through registers to shared memory once for all 256 rows (eight converting warps), and eight warps do the softmax of
+// one half while the tensor core works on the other.
+// Bound by a half's chain of S, maximum, weights, products and the next S, ~4,000 clocks a tile (reads of TMEM take ~250 clocks
+// and 80 registers do not hold a half row, so S is read twice; there are no TMEM columns for a second S).  A causal prompt of
+// 11996 tokens, 32 query and 8 kv heads, E4M3: 1,030 us, 1,144 TFLOP/s.
 //
 // Warps: 0-15 softmax (0-3 rows 0..127 and keys 0..63 of a tile, 4-7 rows 128..255, 8-15 the same rows and keys 64..127),
 // 16-23 convert, 24 issues the products.

@@ -6,7 +6,8 @@
 // only ever taken from below fc once the handed-back ones are used up, no entry is both read and written: every
 // output follows from the inputs alone, and the blocks share nothing but the inputs.  The states that may be updated in
 // place (lengths, stack height) are written behind a cluster barrier that all blocks reach after their reads.
-// Bound by latency: one launch, two dependent rounds of loads.
+// Bound by latency: one launch, two dependent rounds of loads.  64 requests of one token 5.8 us in a graph (7.7 a call from Python),
+// 1024 prompts of 83,360 tokens 12.2 us (14.3).
 #include "runs.cuh"
 
 namespace kvq {
