@@ -362,12 +362,12 @@ CHUNKS = [([20, 100, 129, 257, 384, 513, 641], [5, 20, 9, 17, 20, 32, 31], 2, 4)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("lens,new,heads,group", CHUNKS)
 def test_chunks_of_at_most_128_rows_among_others(kvq, fmt, lens, new, heads, group):
-    """Units of one half, whose key tiles go to the two places in turn: of one tile, of a few, cut anywhere, beside full ones."""
+    """Units that fill one half of a tile's rows at most: of one key tile, of a few, cut anywhere, beside full ones."""
     attention_case(kvq, fmt, "bf16", lens, new, heads, group, seed=len(lens))
 
 
 @pytest.mark.parametrize("q_scale", [30.0, 1e-3])
-def test_chunks_whose_places_differ_in_maximum(kvq, q_scale):
+def test_chunks_with_sharp_and_flat_weights(kvq, q_scale):
     attention_case(kvq, "int8p", "bf16", [2000, 40, 900], [12, 30, 20], 2, 4, seed=5, q_scale=q_scale, exps=(-12, -3))
 
 
