@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kStageBytes = 4096;
 constexpr int kMaxStages = 8;
+constexpr int kMergeWarps = 16;  // of a block; with 8 the three calls at the merge kernel take 19, 35 and 55 us
 constexpr int kMinPages = 2;  // pages a warp, so that short contexts leave the merge fewer pieces
 
 // Page descriptors, one per lane for 32 pages ahead.
@@ -501,32 +502,47 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
   if (unit >= 0) write_piece(a, wid + unit, s);
 }
 
-// One warp per row of a unit: its pieces under log-sum-exp weights.  The unit's record, then everything it points to in one
-// round of loads; what it costs is the latency of those two (a first version looked the row up from the lengths:
-// 8.5 us alone on 64 requests of 28 heads).
+// The pieces of a row under log-sum-exp weights.  The unit's record, then everything it points to in one round of loads; what
+// it costs is the latency of those two (a first version looked the row up from the lengths: 8.5 us alone on 64 requests of 28
+// heads).  One warp to a row, or, where the grid has a block for every row (few requests, whose contexts are then cut into
+// hundreds of pieces), a block: its warps take the pieces in turn.  The whole call for 2 requests of up to 16723 tokens, 2 kv and 6
+// query heads: 146 us with a warp to a row, 17 with a block; one of 120000, one head: 622 and 31; 8 and 32 heads: 135 and 54.
 template <int NT, bool F32>
-__global__ void __launch_bounds__(256) merge_kernel(const AttnArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long gw = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const long long unit = gw / (8 * NT);
-  const int r = static_cast<int>(gw % (8 * NT));
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const AttnArgs a) {
+  constexpr int kU = 16, kRows = 8 * NT;
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ __align__(16) float s_acc[kMergeWarps][kHeadDim];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n_units = *a.ws_units;
-  const UnitRecord rec = a.ws_rec[unit];  // the grid has no more units than there are records
-  if (unit >= n_units || r >= rec.rows) return;
-  const long long first = (rec.w0 + unit) * (8 * NT) + r;  // of the row's pieces, 8 NT rows apart
+  long long gw = static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
+  UnitRecord rec = a.ws_rec[min(gw / kRows, static_cast<long long>(a.max_tiles) * a.Hkv - 1)];
+  const bool wide = static_cast<long long>(n_units) * kRows <= gridDim.x;
+  if (wide) gw = blockIdx.x;
+  const long long unit = gw / kRows;
+  const int r = static_cast<int>(gw % kRows);
+  if (unit >= n_units) return;
+  if (wide) rec = a.ws_rec[unit];
+  if (r >= rec.rows) return;
+  const bool split = wide && rec.pieces > kU;  // the same in all warps of a block
+  if (wide && !split && warp > 0) return;
+  // this warp's pieces: 8 NT rows of the workspace apart, or kMergeWarps times that
+  const long long first = (rec.w0 + unit) * kRows + r + (split ? warp * kRows : 0);
+  const long long step = split ? kMergeWarps * kRows : kRows;
+  const int pieces = split ? (rec.pieces - warp + kMergeWarps - 1) / kMergeWarps : rec.pieces;
   const float* stats = a.ws_stats + first * 2;
   const float* accs = a.ws_acc + first * kHeadDim + 4 * lane;
-  constexpr int kU = 16;
+  auto acc_of = [&](int k) { return *reinterpret_cast<const float4*>(accs + k * step * kHeadDim); };
+  auto stats_of = [&](int k) { return *reinterpret_cast<const float2*>(stats + k * step * 2); };
   float4 v[kU];
 #pragma unroll
   for (int k = 0; k < kU; ++k)
-    if (k < rec.pieces) v[k] = *reinterpret_cast<const float4*>(accs + static_cast<long long>(k) * (8 * NT * kHeadDim));
+    if (k < pieces) v[k] = acc_of(k);
   float m = -INFINITY, l = 0.f, m_mine = -INFINITY;  // m_mine: of piece `lane`
   bool nan = false;  // of a query that is not finite
-  for (int i = lane; i < rec.pieces; i += 32) {
-    const float2 st = *reinterpret_cast<const float2*>(stats + static_cast<long long>(i) * (8 * NT * 2));
+  for (int i = lane; i < pieces; i += 32) {
+    const float2 st = stats_of(i);
     if (i < 32) m_mine = st.x;
     const float mm = fmaxf(m, st.x);
     nan |= st.y != st.y;
@@ -543,27 +559,52 @@ __global__ void __launch_bounds__(256) merge_kernel(const AttnArgs a) {
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
   m = gm;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float wt_mine = m_mine == -INFINITY ? 0.f : ex2(m_mine - m);
+  float wt_mine = m_mine == -INFINITY ? 0.f : ex2(m_mine - m);  // of piece k0 + lane, k0 a multiple of 32
+#pragma unroll 1
+  for (int k0 = 0; k0 < pieces; k0 += kU) {
+    if (k0 > 0) {
 #pragma unroll
-  for (int k = 0; k < kU; ++k) {
-    const float wt = __shfl_sync(kFull, wt_mine, k);
-    if (k < rec.pieces && wt != 0.f) {
-      acc.x += v[k].x * wt; acc.y += v[k].y * wt; acc.z += v[k].z * wt; acc.w += v[k].w * wt;
+      for (int k = 0; k < kU; ++k)
+        if (k0 + k < pieces) v[k] = acc_of(k0 + k);
+      if (k0 % 32 == 0) {
+        const float mi = k0 + lane < pieces ? stats_of(k0 + lane).x : -INFINITY;
+        wt_mine = mi == -INFINITY ? 0.f : ex2(mi - m);
+      }
     }
-  }
-#pragma unroll 8
-  for (int k = kU; k < rec.pieces; ++k) {
-    const float4 x = *reinterpret_cast<const float4*>(accs + static_cast<long long>(k) * (8 * NT * kHeadDim));
-    float wt;
-    if (k < 32) {
-      wt = __shfl_sync(kFull, wt_mine, k);
-    } else {
-      const float mi = stats[static_cast<long long>(k) * (8 * NT * 2)];
-      wt = mi == -INFINITY ? 0.f : ex2(mi - m);
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const float wt = __shfl_sync(kFull, wt_mine, (k0 & 16) + k);
+      if (k0 + k < pieces && wt != 0.f) {
+        acc.x += v[k].x * wt; acc.y += v[k].y * wt; acc.z += v[k].z * wt; acc.w += v[k].w * wt;
+      }
     }
-    if (wt != 0.f) { acc.x += x.x * wt; acc.y += x.y * wt; acc.z += x.z * wt; acc.w += x.w * wt; }
   }
   if (__any_sync(kFull, nan)) l = NAN;
+  if (split) {
+    *reinterpret_cast<float4*>(&s_acc[warp][4 * lane]) = acc;
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    const float mk = lane < kMergeWarps ? s_m[lane] : -INFINITY, lk = lane < kMergeWarps ? s_l[lane] : 0.f;
+    m = mk;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    const float wk = mk == -INFINITY ? 0.f : ex2(mk - m);
+    l = wk == 0.f ? 0.f : lk * wk;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+    if (__any_sync(kFull, lk != lk)) l = NAN;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) {
+      const float wt = __shfl_sync(kFull, wk, k);
+      const float4 x = *reinterpret_cast<const float4*>(&s_acc[k][4 * lane]);
+      if (wt != 0.f) { acc.x += x.x * wt; acc.y += x.y * wt; acc.z += x.z * wt; acc.w += x.w * wt; }
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is 0
   const int in_run = rec.row_in_run + r;
   const long long row = static_cast<long long>(rec.row0 + in_run / a.G) * a.Hq + rec.kvh * a.G + in_run % a.G;
@@ -668,10 +709,11 @@ cudaError_t launch_split(AttnArgs& a, int sms, int smem_max, cudaStream_t s) {
   }
   kern<<<sms, NW * 32, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long threads = static_cast<long long>(a.max_tiles) * a.Hkv * (8 * NT) * 32;
+  const long long rows = static_cast<long long>(a.max_tiles) * a.Hkv * (8 * NT);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((threads + 255) / 256));
-  cfg.blockDim = dim3(256);
+  // a warp to a row; blocks for as many rows as the SMs hold two of, so that few rows have a block each
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max((rows + kMergeWarps - 1) / kMergeWarps, std::min<long long>(rows, 2 * sms))));
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

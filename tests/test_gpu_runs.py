@@ -259,8 +259,10 @@ def test_append_skips_what_cannot_be(kvq):
 
 # ------------------------------------------------------------------------------------------------ attention
 def attention_case(kvq, fmt, dtype, lens, new, heads, group, seed=0, exps=(-7, -4), sm_scale=None, q_scale=1.0, behind=0, max_run=None,
-                   spoil=True):
-    """Runs the call and checks every element; returns what it ran with."""
+                   spoil=True, bad_query=None):
+    """Runs the call and checks every element; returns what it ran with.  bad_query: a (row, head) whose query holds a NaN; its
+    output is NaN and every other row is as near to the formula as without it (not the same bits: the rows of a unit move
+    their running maxima together)."""
     rng = np.random.default_rng(seed)
     lens, new = np.array(lens), np.array(new)
     table, pages = tables(rng, lens)
@@ -277,6 +279,9 @@ def attention_case(kvq, fmt, dtype, lens, new, heads, group, seed=0, exps=(-7, -
     dt = torch.bfloat16 if dtype == "bf16" else torch.float32
     qkv = torch.as_tensor(rng.standard_normal((rows + behind, Hq + 3, 128)) * q_scale).to("cuda", dt)
     q = qkv[:, 1:Hq + 1] if Hq * 128 % 8 == 0 else qkv[:, 1:Hq + 1].contiguous()
+    clean = q[:rows].double().cpu().numpy()
+    if bad_query:
+        q[bad_query][5] = float("nan")
     out = torch.full((rows + behind, Hq, 128), 7.0, dtype=dt, device="cuda")
     lse = torch.full((rows + behind, Hq), 7.0, device="cuda")
     max_run = max_run or max(1, int(new.max()))
@@ -290,8 +295,11 @@ def attention_case(kvq, fmt, dtype, lens, new, heads, group, seed=0, exps=(-7, -
     torch.cuda.synchronize()
     assert err.item() == 0
     scale = 128 ** -0.5 if sm_scale is None else sm_scale
-    want, want_lse, pv, xa, low = R.attend(ck, ek, cv, ev, q[:rows].double().cpu().numpy(), starts, lens, table, scale, fmt)
+    want, want_lse, pv, xa, low = R.attend(ck, ek, cv, ev, clean, starts, lens, table, scale, fmt)
     got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    if bad_query:
+        assert np.all(np.isnan(got[bad_query])) and np.isnan(got_lse[bad_query])
+        got[bad_query], got_lse[bad_query] = want[bad_query], want_lse[bad_query]
     assert np.all(got[rows:] == 7) and np.all(got_lse[rows:] == 7)
     got, got_lse = got[:rows], got_lse[:rows]
     off = np.abs(got - want) - attn_tolerance(want, pv, xa, low, dtype == "bf16")
@@ -352,6 +360,15 @@ def test_sharp_flat_and_negative_scales(kvq, new):
     attention_case(kvq, "e4m3p", "bf16", lens, new, 2, 4, sm_scale=-0.2)
     attention_case(kvq, "e4m3p", "bf16", lens, new, 2, 4, q_scale=1e-30)
     attention_case(kvq, "e4m3p", "bf16", lens, new, 2, 4, q_scale=1e30, sm_scale=1e-31)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("e4m3p", "bf16"), ("int8p", "f32")])
+@pytest.mark.parametrize("lens,new,heads,group", [([20000, 300], [1, 1], 1, 1), ([9000, 40, 7000], [1, 1, 1], 2, 3),
+                                                  ([12000], [2], 1, 5), ([300, 11000], [0, 1], 4, 8)])
+def test_few_requests_of_long_contexts(kvq, fmt, dtype, lens, new, heads, group):
+    """Rows of hundreds of pieces, beside rows of a few; then with a query that is not finite."""
+    attention_case(kvq, fmt, dtype, lens, new, heads, group, seed=7, behind=1)
+    attention_case(kvq, fmt, dtype, lens, new, heads, group, seed=7, behind=1, bad_query=(0, 0))
 
 
 CHUNKS = [([20, 100, 129, 257, 384, 513, 641], [5, 20, 9, 17, 20, 32, 31], 2, 4), ([3000, 1000, 5000], [6, 17, 32], 8, 4),
