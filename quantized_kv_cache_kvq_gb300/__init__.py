@@ -292,8 +292,8 @@ class PagedCache:
                       self.n_out, 0, _ptr(self.k_outlier))
 
     def nbytes(self) -> int:
-        return sum(t.numel() for t in (self.k, self.v, self.k_scale, self.v_scale, self.witness, self.v_witness,
-                                       self.k_outlier) if t is not None)
+        return sum(t.nbytes for t in (self.k, self.v, self.k_scale, self.v_scale, self.witness, self.v_witness,
+                                      self.k_outlier) if t is not None)
 
 
 def read_err(err: torch.Tensor) -> int:
