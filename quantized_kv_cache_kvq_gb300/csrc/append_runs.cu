@@ -439,16 +439,11 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 template <bool INT8, bool BF16>
 cudaError_t launch(const AppendArgs& a, long long items, cudaStream_t s) {
   auto kern = append_runs_kernel<INT8, BF16>;
-  const size_t smem = kStages * stage_bytes<BF16>() + (4 * static_cast<size_t>(a.batch) + 1) * sizeof(int);
-  static size_t configured[kMaxDevices] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  auto smem_of = [](size_t batch) { return kStages * stage_bytes<BF16>() + (4 * batch + 1) * sizeof(int); };
+  const size_t smem = smem_of(a.batch);
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(kern, smem_of(kMaxBatch));
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices || smem > configured[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices) configured[dev] = smem;
-  }
   // as many blocks as the SMs hold (152 SMs), each going through its share of the items
   kern<<<static_cast<unsigned>(std::min<long long>(items, 152 * (BF16 ? kBlocksBf16 : kBlocksF32))), kThreads, smem, s>>>(a);
   return cudaGetLastError();

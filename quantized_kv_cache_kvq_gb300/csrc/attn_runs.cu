@@ -36,6 +36,7 @@ namespace {
 constexpr int kStageBytes = 4096;
 constexpr int kMaxStages = 8;
 constexpr int kMergeWarps = 16;  // of a block; with 8 the three calls at the merge kernel take 19, 35 and 55 us
+constexpr int kSmemStatic = 2048;  // of shared memory, left for what the kernel declares statically
 constexpr int kMinPages = 2;  // pages a warp, so that short contexts leave the merge fewer pieces
 
 // Page descriptors, one per lane for 32 pages ahead.
@@ -632,18 +633,6 @@ int sm_count() {
   return cache[dev];
 }
 
-int smem_optin() {
-  static int cache[kMaxDevices] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  if (!cache[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return 0;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -694,19 +683,13 @@ cudaError_t launch_split(AttnArgs& a, int sms, int smem_max, cudaStream_t s) {
   constexpr int lo_bytes = F32 ? NT * 8 * 2 * 32 * 4 : 0;
   const int cum_bytes = ((a.batch + 1) * 12 + 127) & ~127;
   a.nwa = NW;
-  a.stages = std::min(kMaxStages, (smem_max - 2048 - cum_bytes - NW * (lo_bytes + kMaxStages * 8)) / (NW * kStageBytes));
+  a.stages = std::min(kMaxStages, (smem_max - kSmemStatic - cum_bytes - NW * (lo_bytes + kMaxStages * 8)) / (NW * kStageBytes));
   a.w_max = sms * NW;
   const size_t smem = cum_bytes + static_cast<size_t>(NW) * (a.stages * kStageBytes + lo_bytes + kMaxStages * 8);
   auto kern = split_kernel<INT8, NT, F32, NW>;
-  static size_t configured[kMaxDevices] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(kern, smem_max - kSmemStatic);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices || smem > configured[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices) configured[dev] = smem;
-  }
   kern<<<sms, NW * 32, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(a.max_tiles) * a.Hkv * (8 * NT);
@@ -767,7 +750,7 @@ extern "C" kvq_status kvq_attn_runs(const kvq_cache* cache, const void* q, int64
   if (q_row_stride < static_cast<int64_t>(num_q_heads) * kHeadDim || q_row_stride % unit) return KVQ_ERR_INVALID_ARG;
   if (!q || !seq_lens || !out || !workspace_dev || (max_pages_per_seq > 0 && !block_table)) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace_dev)) return KVQ_ERR_INVALID_ARG;
-  const int sms = sm_count(), smem_max = smem_optin();
+  const int sms = sm_count(), smem_max = device_smem_optin();
   if (sms <= 0 || smem_max <= 0) return KVQ_ERR_CUDA;
   const int mr = std::min(max_run, num_rows);
   const Workspace w = workspace(batch, num_rows, mr, hkv, num_q_heads, q_dtype, sms);

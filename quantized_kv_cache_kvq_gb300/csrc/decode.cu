@@ -211,18 +211,6 @@ int device_sm_count() {
   return cache[dev];
 }
 
-int device_smem_optin() {
-  static int cache[kMaxDevices] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  if (!cache[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return 0;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct WsLayout {
@@ -450,7 +438,7 @@ kvq_status decode_impl(const kvq_cache* cache, const void* k_new, const void* v_
       (xi ? kXiScratch : 0) + lo_bytes + (ext ? kVStateBytes : 0) + (gs ? kGqBytes : 0) + kMaxStages * 8;
   int nwa = nw, stages = 0;
   for (; nwa >= 4; --nwa) {
-    stages = (smem_max - 1024 - cum_bytes - nwa * per_warp_fixed) / (nwa * sb);
+    stages = (smem_max - kSmemStatic - cum_bytes - nwa * per_warp_fixed) / (nwa * sb);
     if (stages >= 2) break;
   }
   if (stages < 2) return KVQ_ERR_UNSUPPORTED_LAYOUT;

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kvq.h"
 
 namespace kvq {
@@ -90,6 +92,38 @@ __host__ __device__ __forceinline__ int vw_offset(int t, int k) { return 8 * (t 
 
 // Devices a process can drive (per-device caches of attributes and of kernel settings).
 constexpr int kMaxDevices = 64;
+
+// Most shared memory that a block of the current device can have (static and dynamic); 0 when it cannot be told.
+inline int device_smem_optin() {
+  static std::atomic<int> cache[kMaxDevices] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  if ((n = cache[dev].load(std::memory_order_relaxed)) == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return 0;
+    cache[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// A kernel's dynamic shared memory limit: a setting of the device's context that all host threads share.  So it is always set to
+// the same value, the most that any call of the kernel needs, and threads whose first calls meet write the same thing.
+class SmemLimit {
+ public:
+  template <class Kernel>
+  cudaError_t raise(Kernel kern, size_t most) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kMaxDevices;
+    if (known && done_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e == cudaSuccess && known) done_[dev].store(true, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<bool> done_[kMaxDevices] = {};
+};
 
 // ---------------------------------------------------------------------------------------------
 // Device error word: the first error code wins.
