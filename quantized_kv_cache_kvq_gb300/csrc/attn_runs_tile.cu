@@ -729,11 +729,16 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
   const int row = (warp & 3) * 32 + lane;              // of the half
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp & 3)
   const uint32_t ts = tmem + kTmemS + 128 * half + 64 * part + lanes, to = tmem + kTmemO + 128 * half + 64 * part + lanes;
-  // A value for the peer and the peer's for this thread.  A warp that gives up releases its peer (leave) once, which then
-  // gives up at its next wait.
+  // A value for the peer and the peer's for this thread.  The meetings have no limit of their own, so a warp whose wait has given
+  // up goes on to the end of its range all the same, without waiting or handing anything on: the two take every meeting that
+  // the range has, wherever either of them gave up (one that left the loop would keep its peer waiting: the peer's own waits may
+  // have been over before).  What it computes from then on is thrown away with the call's error.
   const int bar = 1 + (warp & 7);
   auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory"); };
-  auto leave = [&]() { asm volatile("bar.arrive %0, 64;" ::"r"(bar) : "memory"); };
+  bool alive = true;
+  auto wait_for = [&](uint64_t* b, uint32_t parity) {
+    if (alive) alive = wait_warp(b, parity, &t->abort);
+  };
   auto exchange = [&](float x) {
     t->peer[warp][lane] = x;
     meet();
@@ -770,7 +775,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     meet();
     rk = t->peer[warp & 7][lane];
     __syncwarp();
-    if (lane == 0) arrive(&t->q_full[half]);
+    if (alive && lane == 0) arrive(&t->q_full[half]);
     staged = true;
   };
 #pragma unroll 1
@@ -780,7 +785,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
       continue;
     }
     if (!staged) begin_unit();
-    if (!wait_warp(&t->s_full[half], s_phase, &t->abort)) return leave();
+    wait_for(&t->s_full[half], s_phase);
     s_phase ^= 1u;
     fence_after();
     const float2* scale = t->scale[jj % kScaleSlots] + 4 * part;
@@ -793,7 +798,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     } else {  // the running maximum moves only when a row outgrows it by 2^kSlack
       const bool move = tm > m + kSlack || (m == -INFINITY && tm > m);
       if (__any_sync(dec::kFull, move)) {
-        if (!wait_warp(&t->pv_done[half], pv_phase ^ 1u, &t->abort)) return leave();  // O is the previous tiles' sum
+        wait_for(&t->pv_done[half], pv_phase ^ 1u);  // O is the previous tiles' sum
         fence_after();
         const float alpha = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - tm);
         m = move ? tm : m;
@@ -806,7 +811,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     wait_st();
     fence_before();
     __syncwarp();
-    if (lane == 0) arrive(&t->p_full[half]);
+    if (alive && lane == 0) arrive(&t->p_full[half]);
     const uint32_t parity = pv_phase;  // of this tile's PV
     pv_phase ^= 1u;
     if (!c.last()) {
@@ -831,8 +836,9 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     c.advance(a);
     staged = false;
     if (jj + 1 < total && half < c.halves()) begin_unit();
-    if (!wait_warp(&t->pv_done[half], parity, &t->abort)) return leave();
+    wait_for(&t->pv_done[half], parity);
     fence_after();
+    valid = valid && alive;
     if (whole) {
       store_out(to, l0 == 0.f ? 0.f : 1.f / l0, static_cast<uint16_t*>(a.out) + out_at * kHeadDim + 64 * part, valid);
       if (a.lse && valid && part == 0) a.lse[out_at] = l0 == 0.f ? -INFINITY : (m0 + (log2f(l0) - kTileShift)) * dec::kLn2;
