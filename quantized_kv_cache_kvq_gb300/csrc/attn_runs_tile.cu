@@ -72,6 +72,7 @@ struct Tail {  // shared memory behind the operands
   float peer[kSoftmaxWarps][32];  // what the two warps of a row tell each other
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t drained;  // every product of the CTA
   uint32_t tmem;
   int abort;
   UnitInfo unit[kMmaWarp];  // where each warp is
@@ -485,8 +486,7 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
 }
 
 // ------------------------------------------------------------------------------------------------ products
-__device__ void mma_role(Tail* t, uint32_t smem_base, uint32_t tmem) {
-  const uint32_t leader = dec::elect_one();
+__device__ void mma_role(Tail* t, uint32_t smem_base, uint32_t tmem, uint32_t leader) {
   tmem = dec::uniform_u32(tmem);
   const uint64_t ring = smem_desc(smem_base + kOffRing);
   const uint64_t qd = smem_desc(smem_base + kOffQ);
@@ -880,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       dec::mbar_init(&t->p_full[i], 8);
       dec::mbar_init(&t->pv_done[i], 1);
     }
+    dec::mbar_init(&t->drained, 1);
     dec::fence_mbar_init();
     // which pieces of this CTA the merge has to look at
     const int first_tiles = tiles_of(a, run_info(a, t->start[0]), t->start[2]);
@@ -902,9 +903,20 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     convert_role<INT8>(a, t, smem + kOffRing);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
-    if (warp == kMmaWarp) mma_role(t, smem_u32(smem), tmem);
+    if (warp == kMmaWarp) {
+      const uint32_t leader = dec::elect_one();
+      mma_role(t, smem_u32(smem), tmem, leader);
+      // However the role ended: TMEM and shared memory are given back when the last product that it issued is through with
+      // them (products wait for nothing; the limit is there all the same).
+      commit(&t->drained, leader);
+      const long long t0 = clock64();
+      while (!__all_sync(dec::kFull, dec::mbar_try_wait(&t->drained, 0)))
+        if (__any_sync(dec::kFull, clock64() - t0 > kWaitClocks)) {
+          *reinterpret_cast<volatile int*>(&t->abort) = 1;
+          break;
+        }
+    }
   }
-  if (*reinterpret_cast<volatile int*>(&t->abort)) __nanosleep(1000000);  // products already issued come to their end
   __syncwarp();
   fence_before();
   __syncthreads();

@@ -70,3 +70,15 @@ def test_the_role_has_no_way_out_but_its_end():
     role = re.sub(r"auto exchange = .*?\n  };", "", role, flags=re.S)
     assert "wait_for(" in role and "return" not in re.sub(r"//[^\n]*", "", role)
     assert "bar.arrive" not in role
+
+
+def test_tensor_memory_is_given_back_behind_the_last_product():
+    """On every path: the issuing warp's last commit is waited for before the block frees TMEM and ends, by no length of time."""
+    src = open(SRC).read()
+    assert "__nanosleep" not in src
+    kernel = src[src.index("tile_kernel(const __grid_constant__"):]
+    order = [kernel.index(x) for x in ("mma_role(", "commit(&t->drained", "mbar_try_wait(&t->drained", "__syncthreads();\n  fence_after();\n  if (warp == kMmaWarp)",
+                                       "tcgen05.dealloc")]
+    assert order == sorted(order)
+    role = src[src.index("__device__ void mma_role("):src.index("// ---", src.index("__device__ void mma_role("))]
+    assert "drained" not in role  # its early returns do not pass it by
