@@ -456,8 +456,9 @@ kvq_status kvq_meter(const float* meter_state_dev, int32_t n_layers, int32_t bat
  * A request that gives up its last tokens (a rejected draft) has its length set back by the caller; pages that lie wholly
  *   behind the new length are the caller's to push back, or they are lost when the request grows again.
  * All or nothing: with too few pages (KVQ_ERR_NO_PAGES), more than max_rows tokens, a length outside
- *   [0, 16 max_pages_per_seq] before or after, or a stack height outside [0, free_capacity] (KVQ_ERR_DEVICE_BOUNDS) nothing
- *   is handed out or back: the state is copied, run_starts and positions are 0 and slots -1.
+ *   [0, 16 max_pages_per_seq] before or after, a stack height outside [0, free_capacity], or a page number outside [0, 2^27)
+ *   among those handed back, handed out or gone on in (KVQ_ERR_DEVICE_BOUNDS) nothing is handed out or back: the state is
+ *   copied, run_starts and positions are 0 and slots -1.
  */
 kvq_status kvq_map_runs(const int32_t* new_lens_dev, const int32_t* seq_lens_dev, int32_t batch, int32_t* free_pages_dev,
                         int32_t free_capacity, const int32_t* free_count_dev, int32_t* block_table_dev,

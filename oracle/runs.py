@@ -11,9 +11,10 @@ import numpy as np
 
 from .encoders import e4m3_bits_rne_satfinite, e4m3_value
 
-__all__ = ["PAGE", "E_MIN", "E_MAX", "QMAX", "map_runs", "page_exponent", "encode", "values", "append_runs", "attend"]
+__all__ = ["PAGE", "MAX_PAGE", "E_MIN", "E_MAX", "QMAX", "map_runs", "page_exponent", "encode", "values", "append_runs", "attend"]
 
 PAGE = 16
+MAX_PAGE = (1 << 27) - 1  # the last page whose slots 16 page .. fit 31 bits
 E_MIN, E_MAX = -24, 15
 QMAX = {"e4m3p": 448.0, "int8p": 127.0}
 
@@ -35,6 +36,10 @@ def map_runs(new_lens, seq_lens, stack, count, table, max_rows):
     bad = any(e > width * PAGE or l < 0 or l > width * PAGE for l, e in zip(seq_lens, lens)) or rows > max_rows
     bad = bad or count < 0 or count > cap or len(cur) - sum(want) > cap
     if bad or sum(want) > len(cur):
+        return dict(out, ok=False)
+    moved = cur[min(count, len(cur) - sum(want)):]  # handed back or out
+    going_on = [int(table[s, l // PAGE]) for s, (n, l) in enumerate(zip(new_lens, seq_lens)) if n > 0 and l % PAGE]
+    if not all(0 <= p <= MAX_PAGE for p in moved + going_on):
         return dict(out, ok=False)
     r = 0
     for s in range(B):

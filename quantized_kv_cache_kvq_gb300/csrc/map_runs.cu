@@ -4,10 +4,11 @@
 // index arithmetic.  With fc pages on the stack, R handed back and A wanted, the i-th page handed out is entry F - 1 - i
 // of the stack with the handed-back pages on top (F = fc + R).  Since pages are only ever pushed at fc and above, and
 // only ever taken from below fc once the handed-back ones are used up, no entry is both read and written: every
-// output follows from the inputs alone, and the blocks share nothing but the inputs.  The states that may be updated in
-// place (lengths, stack height) are written behind a cluster barrier that all blocks reach after their reads.
-// Bound by latency: one launch, two dependent rounds of loads.  64 requests of one token 5.8 us in a graph (7.7 a call from Python),
-// 1024 prompts of 83,360 tokens 12.2 us (14.3).
+// output follows from the inputs alone, and the blocks share nothing but the inputs and whether one of them met a page number that
+// cannot be.  Everything is written behind a cluster barrier that all blocks reach after their reads of the states that may be
+// updated in place (lengths, stack height) and their look at the page numbers: a step is taken whole or not at all.
+// Bound by latency: one launch, two dependent rounds of loads.  64 requests of one token 5.5 us in a graph (8.0 a call from Python),
+// 256 requests with prompts and finished ones among them 10.2 (12.3), 1024 prompts of 83,360 tokens 13.3 (14.6).
 #include "runs.cuh"
 
 namespace kvq {
@@ -15,6 +16,8 @@ namespace runs {
 namespace {
 
 constexpr int kThreads = 1024;
+constexpr int kKept = 2;  // pages that a thread keeps from its look at them until it writes them
+constexpr int kMaxPage = 0x7FFFFFFF / kPage;  // the last page whose slots fit 31 bits
 
 struct MapArgs {
   const int32_t* new_lens;
@@ -48,9 +51,9 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
   __shared__ int s_start[kMaxBatch + 1], s_want[kMaxBatch + 1], s_back[kMaxBatch + 1];
   __shared__ int s_old[kMaxBatch];
   __shared__ long long s_tot[3][kThreads / 32];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_odd_page;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_odd_page = 0;
   const int fc = *a.free_count;
   int old = 0, add = 0;
   bool gone = false, bad = false;
@@ -77,6 +80,8 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
   if (lane == 31)
     for (int q = 0; q < 3; ++q) s_tot[q][warp] = inc[q];
   __syncthreads();
+  const bool alone = gridDim.x == 1;
+  if (!alone) asm volatile("barrier.cluster.arrive;" ::: "memory");  // this block's s_odd_page may be written by the others
   if (bad) s_bad = 1;
   long long total[3];
 #pragma unroll
@@ -96,23 +101,21 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     status = KVQ_ERR_DEVICE_BOUNDS;
   else if (total[1] > fc + total[2])
     status = KVQ_ERR_NO_PAGES;
-  const bool ok = status == KVQ_OK;
   if (tid < a.batch) {
     s_start[tid] = static_cast<int>(inc[0] - v[0]);
     s_want[tid] = static_cast<int>(inc[1] - v[1]);
     s_back[tid] = static_cast<int>(inc[2] - v[2]);
     s_old[tid] = old;
   }
-  const int n_rows = ok ? static_cast<int>(total[0]) : 0, A = ok ? static_cast<int>(total[1]) : 0,
-            R = ok ? static_cast<int>(total[2]) : 0, F = fc + R;
+  bool ok = status == KVQ_OK;
+  const int R = ok ? static_cast<int>(total[2]) : 0, F = fc + R;
+  int n_rows = ok ? static_cast<int>(total[0]) : 0, A = ok ? static_cast<int>(total[1]) : 0;
   if (tid == 0) {
     s_start[a.batch] = n_rows;
     s_want[a.batch] = A;
     s_back[a.batch] = R;
   }
   __syncthreads();
-  // every block has read the lengths and the stack height: they may be overwritten after this barrier's second half
-  asm volatile("barrier.cluster.arrive;" ::: "memory");
 
   const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
   auto handed_back = [&](int i) {  // i-th page of the finished requests
@@ -123,11 +126,58 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     const int e = F - 1 - i;
     return e >= fc ? handed_back(e - fc) : a.free_pages[e];
   };
-  for (int i = first; i < A; i += stride) {
-    const int s = find_segment(s_want, a.batch, i);
-    a.block_table[static_cast<size_t>(s) * a.max_pages + (s_old[s] + kPage - 1) / kPage + (i - s_want[s])] = page_of(i);
+  // Every page number that the step moves or goes on in is looked at before anything is written: one that cannot be, found by
+  // any block, stops all of them.
+  bool odd_page = false;
+  auto look = [&](int page) {
+    odd_page |= page < 0 || page > kMaxPage;
+    return page;
+  };
+  int out[kKept] = {}, back[kKept] = {};  // this thread's first pages, for the second time
+  if (ok) {
+    if (tid < a.batch && add > 0 && old % kPage) look(a.block_table[static_cast<size_t>(tid) * a.max_pages + old / kPage]);
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int i = first + k * stride;
+      if (i < A) out[k] = look(page_of(i));
+      if (i < R - A) back[k] = look(handed_back(i));
+    }
+    for (int i = first + kKept * stride; i < A; i += stride) look(page_of(i));
+    for (int i = first + kKept * stride; i < R - A; i += stride) look(handed_back(i));
   }
-  for (int i = first; i < R - A; i += stride) a.free_pages[fc + i] = handed_back(i);
+  if (!alone) asm volatile("barrier.cluster.wait;" ::: "memory");
+  odd_page = __syncthreads_or(odd_page);
+  if (!alone) {
+    if (odd_page && tid < gridDim.x)
+      asm volatile(
+          "{\n\t.reg .b32 there;\n\tmapa.shared::cluster.u32 there, %0, %1;\n\tst.shared::cluster.u32 [there], %2;\n\t}" ::"r"(
+              static_cast<uint32_t>(__cvta_generic_to_shared(&s_odd_page))),
+          "r"(tid), "r"(1)
+          : "memory");
+    asm volatile("barrier.cluster.arrive;" ::: "memory");
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+    odd_page = s_odd_page;
+  }
+  // from here on every block has read the lengths and the stack height, which may be overwritten, and knows of odd pages
+  if (odd_page) {
+    status = KVQ_ERR_DEVICE_BOUNDS;
+    ok = false;
+    n_rows = A = 0;
+  }
+  if (ok) {
+    auto hand_out = [&](int i, int page) {
+      const int s = find_segment(s_want, a.batch, i);
+      a.block_table[static_cast<size_t>(s) * a.max_pages + (s_old[s] + kPage - 1) / kPage + (i - s_want[s])] = page;
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int i = first + k * stride;
+      if (i < A) hand_out(i, out[k]);
+      if (i < R - A) a.free_pages[fc + i] = back[k];
+    }
+    for (int i = first + kKept * stride; i < A; i += stride) hand_out(i, page_of(i));
+    for (int i = first + kKept * stride; i < R - A; i += stride) a.free_pages[fc + i] = handed_back(i);
+  }
   if (a.slots || a.positions) {
     // four rows in a row to a thread: one search, and mostly one page, for them
     for (int r0 = 4 * first; r0 < a.max_rows; r0 += 4 * stride) {
@@ -148,15 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
             j = pos / kPage;
             page = j < h ? a.block_table[static_cast<size_t>(s) * a.max_pages + j] : page_of(s_want[s] + j - h);
           }
-          if (page < 0 || page > 0x7FFFFFF) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
-          else slot = page * kPage + pos % kPage;
+          slot = page * kPage + pos % kPage;
         }
         if (a.slots) a.slots[r] = slot;
         if (a.positions) a.positions[r] = pos;
       }
     }
   }
-  asm volatile("barrier.cluster.wait;" ::: "memory");
   if (blockIdx.x == 0) {
     if (tid < a.batch) {
       a.run_starts[tid] = ok ? s_start[tid] : 0;
@@ -164,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     }
     if (tid == 0) {
       a.run_starts[a.batch] = n_rows;
-      *a.free_count_out = F - A;
+      *a.free_count_out = ok ? F - A : fc;
       if (!ok) report(a.err, status);
     }
   }
