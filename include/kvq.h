@@ -435,15 +435,16 @@ kvq_status kvq_meter(const float* meter_state_dev, int32_t n_layers, int32_t bat
  * last run are left as they are, so num_rows can be the fixed size of a captured step.  A run that cannot be (outside
  * [0, num_rows], longer than max_run, a length outside [0, 16 max_pages_per_seq]) is reported as
  * KVQ_ERR_DEVICE_BOUNDS and skipped.  batch <= KVQ_MAX_BATCH, contexts <= KVQ_MAX_CONTEXT tokens.  Two runs of one call
- * must not overlap or share a page that either of them writes; requests may share pages that are only read.
+ * must not overlap or share a page that either of them writes; requests may share pages that are only read (a common
+ * prefix; what kvq_map_runs does with the pages of a finished request is said there).
  */
 
 /*
  * kvq_map_runs -- a step's page bookkeeping on the device: finished requests hand their pages back, the others get the
  * pages that their new tokens need, and every row its slot and position.
  *
- * new_lens_dev: [batch] int32, tokens that request s adds (0 allowed); negative: the request is finished, its pages go
- *   back and its length becomes 0.  seq_lens_dev: [batch] lengths before the step.
+ * new_lens_dev: [batch] int32, tokens that request s adds (0 allowed); negative: the request is finished, all its pages go
+ *   back, whoever else's table holds them (shared pages: kvq_map_runs_ex), and its length becomes 0.  seq_lens_dev: [batch] lengths before the step.
  * free_pages_dev: [free_capacity] int32 stack of free pages, entries 0 .. *free_count_dev - 1 in use.  Pages handed back
  *   are pushed in order of request and page, then the pages needed are popped one by one in order of request and page.
  * block_table_dev: [batch][max_pages_per_seq]; the entries of new pages are written, the others kept (those of a
@@ -465,6 +466,20 @@ kvq_status kvq_map_runs(const int32_t* new_lens_dev, const int32_t* seq_lens_dev
                         int32_t max_pages_per_seq, int32_t* run_starts_dev, int32_t* seq_lens_out_dev,
                         int32_t* free_count_out_dev, int32_t* slot_mapping_dev, int32_t* positions_dev, int32_t max_rows,
                         int32_t* err_word_dev, kvq_stream_t stream);
+
+/*
+ * kvq_map_runs_ex -- kvq_map_runs where requests share pages.
+ * kept_pages_dev (nullable: 0 for all): [batch] int32; the first kept_pages[s] pages of a finished request do not go back,
+ *   since another request's table or the caller's store of prefixes holds them too.  Whoever gives a shared page up last
+ *   lets it go back, the others keep it.  A count outside [0, pages of the request] is KVQ_ERR_DEVICE_BOUNDS (nothing
+ *   changes); not read for requests that are not finished.
+ * Everything else is that of kvq_map_runs.
+ */
+kvq_status kvq_map_runs_ex(const int32_t* new_lens_dev, const int32_t* seq_lens_dev, int32_t batch, int32_t* free_pages_dev,
+                           int32_t free_capacity, const int32_t* free_count_dev, int32_t* block_table_dev,
+                           int32_t max_pages_per_seq, int32_t* run_starts_dev, int32_t* seq_lens_out_dev,
+                           int32_t* free_count_out_dev, int32_t* slot_mapping_dev, int32_t* positions_dev, int32_t max_rows,
+                           const int32_t* kept_pages_dev, int32_t* err_word_dev, kvq_stream_t stream);
 
 /*
  * kvq_append_runs -- quantize the runs' keys and values into a page-scaled cache (KVQ_FMT_E4M3_PAGE, KVQ_FMT_INT8_PAGE).

@@ -19,21 +19,24 @@ E_MIN, E_MAX = -24, 15
 QMAX = {"e4m3p": 448.0, "int8p": 127.0}
 
 
-def map_runs(new_lens, seq_lens, stack, count, table, max_rows):
-    """-> dict(ok, run_starts, seq_lens, count, stack, table, slots, positions); inputs are not changed."""
+def map_runs(new_lens, seq_lens, stack, count, table, max_rows, kept=None):
+    """-> dict(ok, run_starts, seq_lens, count, stack, table, slots, positions); inputs are not changed.  kept: per request the
+    first pages that do not go back when it is finished."""
     B, width = table.shape
     stack, table = list(stack), table.copy()
     out = dict(run_starts=np.zeros(B + 1, int), seq_lens=np.array(seq_lens), count=count, stack=np.array(stack), table=table,
                slots=np.full(max_rows, -1), positions=np.zeros(max_rows, int))
     cap = len(stack)
     cur = stack[:count]
+    kept = [0] * B if kept is None else kept
     for s in range(B):
         if new_lens[s] < 0:
-            cur += [int(p) for p in table[s, :-(-seq_lens[s] // PAGE)]]
+            cur += [int(p) for p in table[s, kept[s]:-(-seq_lens[s] // PAGE)]]
     lens = [0 if n < 0 else l + n for n, l in zip(new_lens, seq_lens)]
     want = [0 if n < 0 else -(-e // PAGE) - -(-l // PAGE) for n, l, e in zip(new_lens, seq_lens, lens)]
     rows = sum(max(n, 0) for n in new_lens)
     bad = any(e > width * PAGE or l < 0 or l > width * PAGE for l, e in zip(seq_lens, lens)) or rows > max_rows
+    bad = bad or any(n < 0 and not 0 <= k <= -(-l // PAGE) for n, l, k in zip(new_lens, seq_lens, kept))
     bad = bad or count < 0 or count > cap or len(cur) - sum(want) > cap
     if bad or sum(want) > len(cur):
         return dict(out, ok=False)

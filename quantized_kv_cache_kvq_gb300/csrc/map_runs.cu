@@ -34,6 +34,7 @@ struct MapArgs {
   int32_t* slots;
   int32_t* positions;
   int max_rows;
+  const int32_t* kept;  // pages that a finished request leaves to others, or nullptr
   int32_t* err;
 };
 
@@ -49,7 +50,7 @@ __device__ __forceinline__ int find_segment(const int* a, int n, int x) {
 
 __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) {
   __shared__ int s_start[kMaxBatch + 1], s_want[kMaxBatch + 1], s_back[kMaxBatch + 1];
-  __shared__ int s_old[kMaxBatch];
+  __shared__ int s_old[kMaxBatch], s_kept[kMaxBatch];
   __shared__ long long s_tot[3][kThreads / 32];
   __shared__ int s_bad, s_odd_page;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -66,9 +67,17 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     bad = old < 0 || old > cap || static_cast<long long>(old) + add > cap;
   }
   const int held = bad ? 0 : (old + kPage - 1) / kPage;
+  int kept = 0;
+  if (gone && a.kept) {
+    kept = a.kept[tid];
+    if (kept < 0 || kept > held) {
+      bad = true;
+      kept = 0;
+    }
+  }
   // (tokens, pages wanted, pages handed back), summed in 64 bits: the totals are checked before anything is written
   long long v[3] = {bad ? 0 : add, bad || gone ? 0 : (static_cast<long long>(old) + add + kPage - 1) / kPage - held,
-                    gone ? held : 0};
+                    gone ? held - kept : 0};
   long long inc[3] = {v[0], v[1], v[2]};
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1)
@@ -106,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     s_want[tid] = static_cast<int>(inc[1] - v[1]);
     s_back[tid] = static_cast<int>(inc[2] - v[2]);
     s_old[tid] = old;
+    s_kept[tid] = kept;
   }
   bool ok = status == KVQ_OK;
   const int R = ok ? static_cast<int>(total[2]) : 0, F = fc + R;
@@ -120,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
   const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
   auto handed_back = [&](int i) {  // i-th page of the finished requests
     const int s = find_segment(s_back, a.batch, i);
-    return a.block_table[static_cast<size_t>(s) * a.max_pages + (i - s_back[s])];
+    return a.block_table[static_cast<size_t>(s) * a.max_pages + s_kept[s] + (i - s_back[s])];
   };
   auto page_of = [&](int i) {  // i-th page handed out
     const int e = F - 1 - i;
@@ -227,6 +237,15 @@ extern "C" kvq_status kvq_map_runs(const int32_t* new_lens, const int32_t* seq_l
                                    int32_t max_pages_per_seq, int32_t* run_starts, int32_t* seq_lens_out,
                                    int32_t* free_count_out, int32_t* slot_mapping, int32_t* positions, int32_t max_rows,
                                    int32_t* err_word, kvq_stream_t stream) {
+  return kvq_map_runs_ex(new_lens, seq_lens, batch, free_pages, free_capacity, free_count, block_table, max_pages_per_seq, run_starts,
+                         seq_lens_out, free_count_out, slot_mapping, positions, max_rows, nullptr, err_word, stream);
+}
+
+extern "C" kvq_status kvq_map_runs_ex(const int32_t* new_lens, const int32_t* seq_lens, int32_t batch, int32_t* free_pages,
+                                      int32_t free_capacity, const int32_t* free_count, int32_t* block_table,
+                                      int32_t max_pages_per_seq, int32_t* run_starts, int32_t* seq_lens_out,
+                                      int32_t* free_count_out, int32_t* slot_mapping, int32_t* positions, int32_t max_rows,
+                                      const int32_t* kept_pages, int32_t* err_word, kvq_stream_t stream) {
   using namespace kvq::runs;
   if (batch < 0 || batch > kMaxBatch || free_capacity < 0 || max_pages_per_seq < 0 || max_rows < 0) return KVQ_ERR_INVALID_ARG;
   if ((slot_mapping || positions) && max_rows > 1 << 30) return KVQ_ERR_INVALID_ARG;  // rows are indexed with 32-bit integers
@@ -234,7 +253,7 @@ extern "C" kvq_status kvq_map_runs(const int32_t* new_lens, const int32_t* seq_l
   if (batch > 0 && (!new_lens || !seq_lens || !seq_lens_out || (max_pages_per_seq > 0 && !block_table)))
     return KVQ_ERR_INVALID_ARG;
   MapArgs a{new_lens,   seq_lens,     batch,          free_pages,   free_capacity, free_count, block_table, max_pages_per_seq,
-            run_starts, seq_lens_out, free_count_out, slot_mapping, positions,     max_rows,   err_word};
+            run_starts, seq_lens_out, free_count_out, slot_mapping, positions,     max_rows,   kept_pages, err_word};
   cudaLaunchConfig_t cfg = {};
   // one block while its threads have a few rows each: a cluster of eight starts later (64 requests: 8.1 instead of 11 us a call)
   const long long work = batch + (slot_mapping || positions ? max_rows : 0ll);

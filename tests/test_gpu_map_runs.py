@@ -64,3 +64,78 @@ def test_a_page_that_cannot_be_stops_the_whole_step(kvq, where, batch, in_place)
         got, err = run_map(kvq, *step, in_place)
         assert err == (0 if ref["ok"] else 5)
         check_map(got, ref)
+
+
+# ------------------------------------------------------------------------------------------------ shared pages
+SHARED = dict(new=[-1, 0, 20], lens=[20, 25, 0], stack=[3, -9, -9, -9], count=1, rows=20,
+              table=[[5, 1, -1], [5, 2, -1], [-1, -1, -1]])  # requests 0 and 1 have page 5, a common prefix; 0 is finished
+
+
+def test_oracle_keeps_a_shared_page():
+    s = SHARED
+    args = (s["new"], s["lens"], s["stack"], s["count"], np.array(s["table"], dtype=np.int32), s["rows"])
+    m = R.map_runs(*args, kept=[1, 0, 0])
+    assert m["ok"] and m["table"][2].tolist() == [1, 3, -1] and m["count"] == 0  # not page 5
+    assert not R.map_runs(*args, kept=[3, 0, 0])["ok"] and not R.map_runs(*args, kept=[-1, 0, 0])["ok"]
+    m = R.map_runs([-1, -1, 0], *args[1:], kept=[1, 0, 7])  # then the last that has it
+    assert m["stack"].tolist() == [3, 1, 5, 2]
+
+
+def dev(x, dtype=torch.int32):
+    return torch.as_tensor(np.ascontiguousarray(x)).to("cuda", dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["e4m3p", "int8p"])
+def test_a_prefix_outlives_the_first_request_that_had_it(kvq, fmt):  # noqa: F811
+    """Requests 0 and 1 share their first page; 0 ends, 2 starts and writes its pages: request 1 still reads its prefix."""
+    H, Hq, pages = 2, 4, 6
+    cache = kvq.PagedCache(fmt, fmt, H, pages)
+    table = dev(np.array(SHARED["table"]))
+    x = torch.randn(45, 2 * H, 128, device="cuda").bfloat16()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    # the prefix with request 0's own tokens, then request 1's own tokens behind the same prefix
+    kvq.append_runs(cache, x[:20, :H], x[:20, H:], dev([20, 0, 0]), table, run_starts=dev([0, 20, 20, 20]), err=err)
+    kvq.append_runs(cache, x[20:29, :H], x[20:29, H:], dev([0, 25, 0]), table, run_starts=dev([0, 0, 9, 9]), err=err)
+    q = torch.randn(3, Hq, 128, device="cuda").bfloat16()
+    ws = torch.empty(kvq.attn_runs_workspace_size(3, 3, 1, H, Hq, q.dtype), dtype=torch.uint8, device="cuda")
+
+    def attend(lens):
+        out = torch.empty_like(q)
+        kvq.attn_runs(cache, q, dev(lens), table, out, ws, err=err)
+        return out[1].clone()
+
+    before = attend([20, 25, 0])
+    new, lens, stack, count = dev(SHARED["new"]), dev(SHARED["lens"]), dev(SHARED["stack"]), dev([SHARED["count"]])
+    starts = dev([0] * 4)
+    kvq.map_runs(new, lens, stack, count, table, starts, lens, count, kept_pages=dev([1, 0, 0]), err=err)
+    assert table[2, :2].tolist() == [1, 3] and count.item() == 0 and lens.tolist() == [0, 25, 20]
+    kvq.append_runs(cache, x[25:, :H], x[25:, H:], lens, table, run_starts=starts, err=err)
+    assert torch.equal(attend([0, 25, 20]), before)
+    assert err.item() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch", [7, 400])
+def test_kept_pages_equal_the_oracle(kvq, batch):  # noqa: F811
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 200, batch)
+    new = np.where(rng.random(batch) < 0.4, -1, rng.integers(0, 40, batch))
+    kept = np.array([rng.integers(0, -(-n // 16) + 1) for n in lens])
+    table, total = tables(rng, lens, width=16)
+    stack = np.full(2 * total, -9)
+    stack[:total] = total + np.arange(total)
+    for bad in (None, -1, 1):
+        k = kept.copy()
+        k[new >= 0] = 99  # not looked at
+        if bad is not None:
+            s = np.flatnonzero(new < 0)[-1]
+            k[s] = -1 if bad < 0 else -(-lens[s] // 16) + 1
+        ref = R.map_runs(new, lens, stack, total, table, int(np.maximum(new, 0).sum()), kept=k)
+        assert ref["ok"] == (bad is None)
+        t = dict(new=dev(new), lens=dev(lens), stack=dev(stack), count=dev([total]), table=dev(table))
+        starts, err = dev(np.full(batch + 1, -7)), torch.zeros(1, dtype=torch.int32, device="cuda")
+        kvq.map_runs(t["new"], t["lens"], t["stack"], t["count"], t["table"], starts, t["lens"], t["count"], kept_pages=dev(k), err=err)
+        assert err.item() == (0 if ref["ok"] else 5)
+        assert np.array_equal(t["stack"].cpu().numpy(), ref["stack"]) and np.array_equal(t["table"].cpu().numpy(), ref["table"])
+        assert t["lens"].tolist() == list(ref["seq_lens"]) and t["count"].item() == ref["count"] and starts.tolist() == ref["run_starts"].tolist()
