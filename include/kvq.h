@@ -454,8 +454,9 @@ kvq_status kvq_meter(const float* meter_state_dev, int32_t n_layers, int32_t bat
  *   needs it) or other buffers.  No other two buffers may overlap.
  * slot_mapping_dev, positions_dev (both nullable): [max_rows] int32; row r's slot (page 16 + offset, as kvq_append
  *   takes it) and position; rows behind the last run get slot -1 (which kvq_append skips) and position 0.
- * A request that gives up its last tokens (a rejected draft) has its length set back by the caller; pages that lie wholly
- *   behind the new length are the caller's to push back, or they are lost when the request grows again.
+ * A request that gives up its last tokens (a rejected draft) has its length set back by the caller.  This call takes a
+ *   request's pages from its length alone: pages that lie wholly behind the new length are the caller's to push back, or
+ *   they are lost when the request grows again.  kvq_map_runs_ex can count them instead.
  * All or nothing: with too few pages (KVQ_ERR_NO_PAGES), more than max_rows tokens, a length outside
  *   [0, 16 max_pages_per_seq] before or after, a stack height outside [0, free_capacity], or a page number outside [0, 2^27)
  *   among those handed back, handed out or gone on in (KVQ_ERR_DEVICE_BOUNDS) nothing is handed out or back: the state is
@@ -468,18 +469,22 @@ kvq_status kvq_map_runs(const int32_t* new_lens_dev, const int32_t* seq_lens_dev
                         int32_t* err_word_dev, kvq_stream_t stream);
 
 /*
- * kvq_map_runs_ex -- kvq_map_runs where requests share pages.
+ * kvq_map_runs_ex -- kvq_map_runs where requests share pages or give up tokens.
  * kept_pages_dev (nullable: 0 for all): [batch] int32; the first kept_pages[s] pages of a finished request do not go back,
  *   since another request's table or the caller's store of prefixes holds them too.  Whoever gives a shared page up last
  *   lets it go back, the others keep it.  A count outside [0, pages of the request] is KVQ_ERR_DEVICE_BOUNDS (nothing
  *   changes); not read for requests that are not finished.
+ * held_pages_dev (nullable): [batch] int32, in and out: the pages that request s has, entries 0 .. held_pages[s] - 1 of its
+ *   row.  A request whose length was set back still has the pages behind it: its next tokens go there before it gets new
+ *   ones, and all of them go back when it is finished.  Fewer than its length needs, or more than max_pages_per_seq, is
+ *   KVQ_ERR_DEVICE_BOUNDS (nothing changes).  Afterwards: 0 for a finished request, else at least what its length needs.
  * Everything else is that of kvq_map_runs.
  */
 kvq_status kvq_map_runs_ex(const int32_t* new_lens_dev, const int32_t* seq_lens_dev, int32_t batch, int32_t* free_pages_dev,
                            int32_t free_capacity, const int32_t* free_count_dev, int32_t* block_table_dev,
                            int32_t max_pages_per_seq, int32_t* run_starts_dev, int32_t* seq_lens_out_dev,
                            int32_t* free_count_out_dev, int32_t* slot_mapping_dev, int32_t* positions_dev, int32_t max_rows,
-                           const int32_t* kept_pages_dev, int32_t* err_word_dev, kvq_stream_t stream);
+                           const int32_t* kept_pages_dev, int32_t* held_pages_dev, int32_t* err_word_dev, kvq_stream_t stream);
 
 /*
  * kvq_append_runs -- quantize the runs' keys and values into a page-scaled cache (KVQ_FMT_E4M3_PAGE, KVQ_FMT_INT8_PAGE).

@@ -19,29 +19,32 @@ E_MIN, E_MAX = -24, 15
 QMAX = {"e4m3p": 448.0, "int8p": 127.0}
 
 
-def map_runs(new_lens, seq_lens, stack, count, table, max_rows, kept=None):
-    """-> dict(ok, run_starts, seq_lens, count, stack, table, slots, positions); inputs are not changed.  kept: per request the
-    first pages that do not go back when it is finished."""
+def map_runs(new_lens, seq_lens, stack, count, table, max_rows, kept=None, held=None):
+    """-> dict(ok, run_starts, seq_lens, count, stack, table, slots, positions, held); inputs are not changed.  kept: per request
+    the first pages that do not go back when it is finished; held: the pages that it has (None: those of its length)."""
     B, width = table.shape
     stack, table = list(stack), table.copy()
-    out = dict(run_starts=np.zeros(B + 1, int), seq_lens=np.array(seq_lens), count=count, stack=np.array(stack), table=table,
+    pages = [-(-n // PAGE) for n in seq_lens]
+    held = pages if held is None else [int(h) for h in held]
+    out = dict(held=np.array(held, dtype=int), run_starts=np.zeros(B + 1, int), seq_lens=np.array(seq_lens), count=count, stack=np.array(stack), table=table,
                slots=np.full(max_rows, -1), positions=np.zeros(max_rows, int))
     cap = len(stack)
     cur = stack[:count]
     kept = [0] * B if kept is None else kept
     for s in range(B):
         if new_lens[s] < 0:
-            cur += [int(p) for p in table[s, kept[s]:-(-seq_lens[s] // PAGE)]]
+            cur += [int(p) for p in table[s, kept[s]:held[s]]]
     lens = [0 if n < 0 else l + n for n, l in zip(new_lens, seq_lens)]
-    want = [0 if n < 0 else -(-e // PAGE) - -(-l // PAGE) for n, l, e in zip(new_lens, seq_lens, lens)]
+    want = [0 if n < 0 else max(0, -(-e // PAGE) - h) for n, h, e in zip(new_lens, held, lens)]
     rows = sum(max(n, 0) for n in new_lens)
     bad = any(e > width * PAGE or l < 0 or l > width * PAGE for l, e in zip(seq_lens, lens)) or rows > max_rows
-    bad = bad or any(n < 0 and not 0 <= k <= -(-l // PAGE) for n, l, k in zip(new_lens, seq_lens, kept))
+    bad = bad or any(h < p or h > width for h, p in zip(held, pages))
+    bad = bad or any(n < 0 and not 0 <= k <= h for n, h, k in zip(new_lens, held, kept))
     bad = bad or count < 0 or count > cap or len(cur) - sum(want) > cap
     if bad or sum(want) > len(cur):
         return dict(out, ok=False)
     moved = cur[min(count, len(cur) - sum(want)):]  # handed back or out
-    going_on = [int(table[s, l // PAGE]) for s, (n, l) in enumerate(zip(new_lens, seq_lens)) if n > 0 and l % PAGE]
+    going_on = [int(p) for s in range(B) if new_lens[s] > 0 for p in table[s, seq_lens[s] // PAGE:min(held[s], -(-lens[s] // PAGE))]]
     if not all(0 <= p <= MAX_PAGE for p in moved + going_on):
         return dict(out, ok=False)
     r = 0
@@ -50,9 +53,8 @@ def map_runs(new_lens, seq_lens, stack, count, table, max_rows, kept=None):
         if n < 0:
             out["run_starts"][s + 1] = r
             continue
-        first = -(-seq_lens[s] // PAGE)
         for j in range(want[s]):
-            table[s, first + j] = cur.pop()
+            table[s, held[s] + j] = cur.pop()
         for p in range(seq_lens[s], lens[s]):
             out["slots"][r] = table[s, p // PAGE] * PAGE + p % PAGE
             out["positions"][r] = p
@@ -61,6 +63,7 @@ def map_runs(new_lens, seq_lens, stack, count, table, max_rows, kept=None):
     left = np.array(stack)
     if len(cur) > count:
         left[count:len(cur)] = cur[count:]
+    out["held"] = np.array([0 if n < 0 else h + w for n, h, w in zip(new_lens, held, want)], dtype=int)
     return dict(out, ok=True, seq_lens=np.array(lens), count=len(cur), stack=left)
 
 

@@ -170,7 +170,7 @@ def load(path: str = LIB_PATH):
     L.kvq_map_runs.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
                                c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p]
     L.kvq_map_runs_ex.restype = c_int32
-    L.kvq_map_runs_ex.argtypes = L.kvq_map_runs.argtypes[:14] + [c_void_p, c_void_p, c_void_p]
+    L.kvq_map_runs_ex.argtypes = L.kvq_map_runs.argtypes[:14] + [c_void_p, c_void_p, c_void_p, c_void_p]
     L.kvq_append_runs.restype = c_int32
     L.kvq_append_runs.argtypes = [POINTER(_Cache), c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_int32,
                                   c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_void_p]
@@ -488,19 +488,22 @@ def _launch(name: str, fn, device: int, stream, *args):
 def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
              block_table: torch.Tensor, run_starts: torch.Tensor, seq_lens_out: torch.Tensor, free_count_out: torch.Tensor,
              *, slot_mapping: torch.Tensor | None = None, positions: torch.Tensor | None = None,
-             kept_pages: torch.Tensor | None = None, err: torch.Tensor | None = None, stream=None):
+             kept_pages: torch.Tensor | None = None, held_pages: torch.Tensor | None = None, err: torch.Tensor | None = None,
+             stream=None):
     """kvq_map_runs_ex: pages, slots and positions of a step from new_lens [B] (negative: finished) and seq_lens [B].
 
     free_pages [capacity] is the stack of free pages with free_count [1] in use, block_table [B, max_pages]; run_starts
     [B + 1], seq_lens_out [B] and free_count_out [1] are written (the latter two may be the inputs), and slot_mapping and
     positions [max_rows] where given.  kept_pages [B]: the first pages of a finished request that do not go back, others hold
-    them too.  All int32 and contiguous."""
+    them too; held_pages [B], in and out: the pages that a request has, those behind a length that was set back among them.
+    All int32 and contiguous."""
     device = run_starts.get_device()
     _i32(device, new_lens, seq_lens, free_pages, free_count, block_table, run_starts, seq_lens_out, free_count_out,
-         slot_mapping, positions, kept_pages, err)
+         slot_mapping, positions, kept_pages, held_pages, err)
     B, width = block_table.shape
     assert new_lens.numel() == B and seq_lens.numel() == B and seq_lens_out.numel() == B and run_starts.numel() == B + 1
     assert free_count.numel() == 1 and free_count_out.numel() == 1 and (kept_pages is None or kept_pages.numel() == B)
+    assert held_pages is None or held_pages.numel() == B
     rows = 0x7FFFFFFF
     if slot_mapping is not None:
         rows = slot_mapping.numel()
@@ -510,7 +513,7 @@ def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.T
     _launch("kvq_map_runs_ex", lib().kvq_map_runs_ex, device, stream, new_lens.data_ptr(), seq_lens.data_ptr(), B,
             free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), block_table.data_ptr(), width,
             run_starts.data_ptr(), seq_lens_out.data_ptr(), free_count_out.data_ptr(), _ptr(slot_mapping), _ptr(positions),
-            rows, _ptr(kept_pages), _ptr(err))
+            rows, _ptr(kept_pages), _ptr(held_pages), _ptr(err))
 
 
 def append_runs(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,

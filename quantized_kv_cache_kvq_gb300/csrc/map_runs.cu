@@ -7,6 +7,8 @@
 // output follows from the inputs alone, and the blocks share nothing but the inputs and whether one of them met a page number that
 // cannot be.  Everything is written behind a cluster barrier that all blocks reach after their reads of the states that may be
 // updated in place (lengths, stack height) and their look at the page numbers: a step is taken whole or not at all.
+// A request's pages are those of its length, or the caller keeps their number beside it: a draft's rejected tokens then leave
+// their pages with the request, which uses them before it takes new ones.
 // Bound by latency: one launch, two dependent rounds of loads.  64 requests of one token 5.5 us in a graph (8.0 a call from Python),
 // 256 requests with prompts and finished ones among them 10.2 (12.3), 1024 prompts of 83,360 tokens 13.3 (14.6).
 #include "runs.cuh"
@@ -35,6 +37,7 @@ struct MapArgs {
   int32_t* positions;
   int max_rows;
   const int32_t* kept;  // pages that a finished request leaves to others, or nullptr
+  int32_t* held;        // pages that a request has, in and out, or nullptr: those of its length
   int32_t* err;
 };
 
@@ -50,7 +53,7 @@ __device__ __forceinline__ int find_segment(const int* a, int n, int x) {
 
 __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) {
   __shared__ int s_start[kMaxBatch + 1], s_want[kMaxBatch + 1], s_back[kMaxBatch + 1];
-  __shared__ int s_old[kMaxBatch], s_kept[kMaxBatch];
+  __shared__ int s_old[kMaxBatch], s_held[kMaxBatch], s_kept[kMaxBatch];
   __shared__ long long s_tot[3][kThreads / 32];
   __shared__ int s_bad, s_odd_page;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -66,17 +69,19 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     const long long cap = min(static_cast<long long>(a.max_pages) * kPage, static_cast<long long>(kMaxContext));
     bad = old < 0 || old > cap || static_cast<long long>(old) + add > cap;
   }
-  const int held = bad ? 0 : (old + kPage - 1) / kPage;
-  int kept = 0;
+  const int needed = bad ? 0 : (old + kPage - 1) / kPage;
+  const int had = a.held && tid < a.batch ? a.held[tid] : needed;
+  bad |= had < needed || had > a.max_pages;
+  int held = bad ? 0 : had, kept = 0;
   if (gone && a.kept) {
     kept = a.kept[tid];
     if (kept < 0 || kept > held) {
       bad = true;
-      kept = 0;
+      kept = held = 0;
     }
   }
   // (tokens, pages wanted, pages handed back), summed in 64 bits: the totals are checked before anything is written
-  long long v[3] = {bad ? 0 : add, bad || gone ? 0 : (static_cast<long long>(old) + add + kPage - 1) / kPage - held,
+  long long v[3] = {bad ? 0 : add, bad || gone ? 0 : max(0ll, (static_cast<long long>(old) + add + kPage - 1) / kPage - held),
                     gone ? held - kept : 0};
   long long inc[3] = {v[0], v[1], v[2]};
 #pragma unroll
@@ -115,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     s_want[tid] = static_cast<int>(inc[1] - v[1]);
     s_back[tid] = static_cast<int>(inc[2] - v[2]);
     s_old[tid] = old;
+    s_held[tid] = held;
     s_kept[tid] = kept;
   }
   bool ok = status == KVQ_OK;
@@ -145,7 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
   };
   int out[kKept] = {}, back[kKept] = {};  // this thread's first pages, for the second time
   if (ok) {
-    if (tid < a.batch && add > 0 && old % kPage) look(a.block_table[static_cast<size_t>(tid) * a.max_pages + old / kPage]);
+    if (tid < a.batch && add > 0)
+      for (int j = old / kPage, end = min(held, (old + add + kPage - 1) / kPage); j < end; ++j)
+        look(a.block_table[static_cast<size_t>(tid) * a.max_pages + j]);
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
       const int i = first + k * stride;
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
   if (ok) {
     auto hand_out = [&](int i, int page) {
       const int s = find_segment(s_want, a.batch, i);
-      a.block_table[static_cast<size_t>(s) * a.max_pages + (s_old[s] + kPage - 1) / kPage + (i - s_want[s])] = page;
+      a.block_table[static_cast<size_t>(s) * a.max_pages + s_held[s] + (i - s_want[s])] = page;
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
@@ -202,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
             ++s;
             j = -1;
           }
-          const int o = s_old[s], h = (o + kPage - 1) / kPage;
+          const int o = s_old[s], h = s_held[s];
           pos = o + (r - s_start[s]);
           if (pos / kPage != j) {
             j = pos / kPage;
@@ -219,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     if (tid < a.batch) {
       a.run_starts[tid] = ok ? s_start[tid] : 0;
       a.seq_lens_out[tid] = !ok ? old : gone ? 0 : old + add;
+      if (a.held && ok) a.held[tid] = gone ? 0 : held + static_cast<int>(v[1]);
     }
     if (tid == 0) {
       a.run_starts[a.batch] = n_rows;
@@ -238,14 +247,14 @@ extern "C" kvq_status kvq_map_runs(const int32_t* new_lens, const int32_t* seq_l
                                    int32_t* free_count_out, int32_t* slot_mapping, int32_t* positions, int32_t max_rows,
                                    int32_t* err_word, kvq_stream_t stream) {
   return kvq_map_runs_ex(new_lens, seq_lens, batch, free_pages, free_capacity, free_count, block_table, max_pages_per_seq, run_starts,
-                         seq_lens_out, free_count_out, slot_mapping, positions, max_rows, nullptr, err_word, stream);
+                         seq_lens_out, free_count_out, slot_mapping, positions, max_rows, nullptr, nullptr, err_word, stream);
 }
 
 extern "C" kvq_status kvq_map_runs_ex(const int32_t* new_lens, const int32_t* seq_lens, int32_t batch, int32_t* free_pages,
                                       int32_t free_capacity, const int32_t* free_count, int32_t* block_table,
                                       int32_t max_pages_per_seq, int32_t* run_starts, int32_t* seq_lens_out,
                                       int32_t* free_count_out, int32_t* slot_mapping, int32_t* positions, int32_t max_rows,
-                                      const int32_t* kept_pages, int32_t* err_word, kvq_stream_t stream) {
+                                      const int32_t* kept_pages, int32_t* held_pages, int32_t* err_word, kvq_stream_t stream) {
   using namespace kvq::runs;
   if (batch < 0 || batch > kMaxBatch || free_capacity < 0 || max_pages_per_seq < 0 || max_rows < 0) return KVQ_ERR_INVALID_ARG;
   if ((slot_mapping || positions) && max_rows > 1 << 30) return KVQ_ERR_INVALID_ARG;  // rows are indexed with 32-bit integers
@@ -253,7 +262,8 @@ extern "C" kvq_status kvq_map_runs_ex(const int32_t* new_lens, const int32_t* se
   if (batch > 0 && (!new_lens || !seq_lens || !seq_lens_out || (max_pages_per_seq > 0 && !block_table)))
     return KVQ_ERR_INVALID_ARG;
   MapArgs a{new_lens,   seq_lens,     batch,          free_pages,   free_capacity, free_count, block_table, max_pages_per_seq,
-            run_starts, seq_lens_out, free_count_out, slot_mapping, positions,     max_rows,   kept_pages, err_word};
+            run_starts, seq_lens_out, free_count_out, slot_mapping, positions,     max_rows,   kept_pages,
+            held_pages, err_word};
   cudaLaunchConfig_t cfg = {};
   // one block while its threads have a few rows each: a cluster of eight starts later (64 requests: 8.1 instead of 11 us a call)
   const long long work = batch + (slot_mapping || positions ? max_rows : 0ll);

@@ -139,3 +139,83 @@ def test_kept_pages_equal_the_oracle(kvq, batch):  # noqa: F811
         assert err.item() == (0 if ref["ok"] else 5)
         assert np.array_equal(t["stack"].cpu().numpy(), ref["stack"]) and np.array_equal(t["table"].cpu().numpy(), ref["table"])
         assert t["lens"].tolist() == list(ref["seq_lens"]) and t["count"].item() == ref["count"] and starts.tolist() == ref["run_starts"].tolist()
+
+
+# ------------------------------------------------------------------------------------------------ pages behind a length set back
+def drafts(step, batch=5):
+    """Steps of drafts: each request adds some tokens, then all but a few of them are rejected; sometimes one is finished."""
+    rng = np.random.default_rng(100 * batch + step)
+    new = rng.integers(0, 40, batch)
+    if step % 4 == 3:
+        new[rng.integers(batch)] = -1
+    return new, rng.random(batch)
+
+
+def test_oracle_loses_no_page_to_rejected_drafts():
+    B, width, pages = 5, 12, 80
+    lens, table, stack, count, held = np.zeros(B, int), np.full((B, width), -1), np.arange(pages), pages, np.zeros(B, int)
+    for step in range(60):
+        new, share = drafts(step)
+        new = np.where(lens + new > width * 16, -1, new)
+        m = R.map_runs(new, lens, stack, count, table, 200, held=held)
+        assert m["ok"]
+        lens, table, stack, count, held = m["seq_lens"], m["table"], m["stack"], m["count"], m["held"]
+        owned = [int(p) for s in range(B) for p in table[s, :held[s]]] + stack[:count].tolist()
+        assert sorted(owned) == list(range(pages))  # every page has one owner
+        lens = np.where(new > 0, lens - (share * np.maximum(new, 0)).astype(int), lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,in_graph", [(5, True), (300, False)])
+def test_rejected_drafts_keep_their_pages(kvq, batch, in_graph):  # noqa: F811
+    """Captured once and replayed in place, the lengths set back between the steps; every step against the oracle."""
+    width, pages, rows = 12, 16 * batch, 40 * batch
+    lens, table, stack, count, held = np.zeros(batch, int), np.full((batch, width), -1), np.arange(pages), pages, np.zeros(batch, int)
+    t = dict(new=dev(np.zeros(batch)), lens=dev(lens), stack=dev(stack), count=dev([count]), table=dev(table), held=dev(held),
+             starts=dev(np.zeros(batch + 1)), slots=dev(np.zeros(rows)), pos=dev(np.zeros(rows)))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        kvq.map_runs(t["new"], t["lens"], t["stack"], t["count"], t["table"], t["starts"], t["lens"], t["count"], slot_mapping=t["slots"],
+                     positions=t["pos"], held_pages=t["held"], err=err)
+
+    call()  # no tokens: nothing changes
+    torch.cuda.synchronize()
+    run = call
+    if in_graph:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        run = graph.replay
+    for step in range(12):
+        new, share = drafts(step, batch)
+        new = np.where(lens + new > width * 16, -1, new)
+        t["new"].copy_(dev(new))
+        run()
+        m = R.map_runs(new, lens, stack, count, table, rows, held=held)
+        assert m["ok"] and err.item() == 0
+        lens, table, stack, count, held = m["seq_lens"], m["table"], m["stack"], m["count"], m["held"]
+        got = {k: v.cpu().numpy() for k, v in t.items()}
+        for a, b in (("lens", lens), ("table", table), ("stack", stack), ("held", held), ("starts", m["run_starts"]), ("slots", m["slots"]),
+                     ("pos", m["positions"])):
+            assert np.array_equal(got[a], b), (step, a)
+        assert got["count"][0] == count
+        lens = np.where(new > 0, lens - (share * np.maximum(new, 0)).astype(int), lens)
+        t["lens"].copy_(dev(lens))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("held", [[1, 2, 0], [2, 2, -1], [2, 4, 0]])
+def test_a_wrong_number_of_held_pages_is_refused(kvq, held):  # noqa: F811
+    table = np.array(SHARED["table"], dtype=np.int32)
+    lens, stack = SHARED["lens"], SHARED["stack"]
+    assert not R.map_runs([0, 1, 0], lens, stack, 1, table, 9, held=held)["ok"]
+    t = [dev([0, 1, 0]), dev(lens), dev(stack), dev([1]), dev(table), dev([7] * 4)]
+    h, err = dev(held), torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvq.map_runs(*t, t[1], t[3], held_pages=h, err=err)
+    assert err.item() == 5 and h.tolist() == held and t[1].tolist() == lens and t[2].tolist() == stack and t[3].tolist() == [1]
+    assert t[4].tolist() == table.tolist() and t[5].tolist() == [0] * 4
+    # kept and held together: all that a finished request has, but the shared page
+    h, err, pages = dev([3, 2, 0]), torch.zeros_like(err), dev([[5, 1, 0], [5, 2, -1], [-1, -1, -1]])
+    kvq.map_runs(dev([-1, 1, 0]), *t[1:4], pages, t[5], t[1], t[3], kept_pages=dev([1, 0, 0]), held_pages=h, err=err)
+    assert err.item() == 0 and t[2].tolist() == [3, 1, 0, -9] and t[3].tolist() == [3] and h.tolist() == [0, 2, 0]
