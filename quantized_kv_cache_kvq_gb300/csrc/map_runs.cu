@@ -9,8 +9,9 @@
 // updated in place (lengths, stack height) and their look at the page numbers: a step is taken whole or not at all.
 // A request's pages are those of its length, or the caller keeps their number beside it: a draft's rejected tokens then leave
 // their pages with the request, which uses them before it takes new ones.
-// Bound by latency: one launch, two dependent rounds of loads.  64 requests of one token 5.5 us in a graph (8.0 a call from Python),
-// 256 requests with prompts and finished ones among them 10.2 (12.3), 1024 prompts of 83,360 tokens 13.3 (14.6).
+// Bound by latency: one launch, two dependent rounds of loads.  64 requests of one token 5.9 us in a graph (8.4 a call from Python),
+// 256 requests with prompts and finished ones among them 10.9 (12.3), 1024 prompts of 83,360 tokens 13.5 (15.0).  Rows written between
+// the halves of the cluster barrier, which hides it: 13.5 as well.
 #include "runs.cuh"
 
 namespace kvq {
