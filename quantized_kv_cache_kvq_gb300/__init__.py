@@ -488,13 +488,14 @@ def _launch(name: str, fn, device: int, stream, *args):
 def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
              block_table: torch.Tensor, run_starts: torch.Tensor, seq_lens_out: torch.Tensor, free_count_out: torch.Tensor,
              *, slot_mapping: torch.Tensor | None = None, positions: torch.Tensor | None = None,
-             kept_pages: torch.Tensor | None = None, held_pages: torch.Tensor | None = None, err: torch.Tensor | None = None,
-             stream=None):
+             kept_pages: torch.Tensor | None = None, held_pages: torch.Tensor | None = None, max_rows: int | None = None,
+             err: torch.Tensor | None = None, stream=None):
     """kvq_map_runs_ex: pages, slots and positions of a step from new_lens [B] (negative: finished) and seq_lens [B].
 
     free_pages [capacity] is the stack of free pages with free_count [1] in use, block_table [B, max_pages]; run_starts
     [B + 1], seq_lens_out [B] and free_count_out [1] are written (the latter two may be the inputs), and slot_mapping and
-    positions [max_rows] where given.  kept_pages [B]: the first pages of a finished request that do not go back, others hold
+    positions [max_rows] where given.  A step of more than max_rows tokens is not taken: give the rows of the step's tensors
+    where there is no slot_mapping to tell them, or the lengths of a larger step move on and its tokens are missed.  kept_pages [B]: the first pages of a finished request that do not go back, others hold
     them too; held_pages [B], in and out: the pages that a request has, those behind a length that was set back among them.
     All int32 and contiguous."""
     device = run_starts.get_device()
@@ -504,12 +505,11 @@ def map_runs(new_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.T
     assert new_lens.numel() == B and seq_lens.numel() == B and seq_lens_out.numel() == B and run_starts.numel() == B + 1
     assert free_count.numel() == 1 and free_count_out.numel() == 1 and (kept_pages is None or kept_pages.numel() == B)
     assert held_pages is None or held_pages.numel() == B
-    rows = 0x7FFFFFFF
-    if slot_mapping is not None:
-        rows = slot_mapping.numel()
-        assert positions is None or positions.numel() == rows
-    elif positions is not None:
-        rows = positions.numel()
+    rows = 0x7FFFFFFF if max_rows is None else max_rows
+    for t in (slot_mapping, positions):
+        if t is not None:
+            assert max_rows is None or t.numel() == max_rows
+            max_rows = rows = t.numel()
     _launch("kvq_map_runs_ex", lib().kvq_map_runs_ex, device, stream, new_lens.data_ptr(), seq_lens.data_ptr(), B,
             free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), block_table.data_ptr(), width,
             run_starts.data_ptr(), seq_lens_out.data_ptr(), free_count_out.data_ptr(), _ptr(slot_mapping), _ptr(positions),
