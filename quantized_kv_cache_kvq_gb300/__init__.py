@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from ctypes import POINTER, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
@@ -225,10 +226,27 @@ def status_string(status: int) -> str:
     return lib().kvq_status_string(status).decode()
 
 
+def _plane(name: str):
+    """A plane of PagedCache.  Those of a page-scaled cache may be exchanged (the kernels take their sizes from the cache's heads and
+    pages, so each is looked at when it is put in)."""
+    slot = "_" + name
+
+    def put(self, t):
+        if self.k_fmt in PAGE_SCALED:
+            n = self.num_pages * self.num_kv_heads
+            dtype, n = (torch.float16, n) if name.endswith("scale") else (torch.uint8, 2048 * n)
+            assert t.dtype is dtype and t.numel() == n and t.is_contiguous(), f"{name}: {n} elements of {dtype}, contiguous"
+        setattr(self, slot, t)
+
+    return property(operator.attrgetter(slot), put)
+
+
 class PagedCache:
     """One layer's paged planes (device memory owned by torch tensors).
 
     The page-scaled formats ("e4m3p", "int8p") have fp16 scale planes [num_kv_heads, num_pages] and no witness."""
+
+    k, v, k_scale, v_scale = _plane("k"), _plane("v"), _plane("k_scale"), _plane("v_scale")
 
     def __init__(self, k_fmt: str, v_fmt: str, num_kv_heads: int, num_pages: int, layer: int = 0,
                  seed: int = 0, device="cuda", witness: bool = True, value_witness: bool = False,
@@ -283,11 +301,14 @@ class PagedCache:
         c._page_scaled(k, v, k_scale, v_scale)
         return c
 
+    def _check_device(self, device: int):
+        _on(device, self._k, self._v, self._k_scale, self._v_scale)
+
     def desc(self) -> _Cache:
         if self.k_fmt in PAGE_SCALED:
             f = FMT[self.k_fmt]
-            return _Cache(f, f, self.num_kv_heads, self.num_pages, self.layer, 0, 0, self.k.data_ptr(), self.v.data_ptr(),
-                          self.k_scale.data_ptr(), self.v_scale.data_ptr())
+            return _Cache(f, f, self.num_kv_heads, self.num_pages, self.layer, 0, 0, self._k.data_ptr(), self._v.data_ptr(),
+                          self._k_scale.data_ptr(), self._v_scale.data_ptr())
         return _Cache(FMT[self.k_fmt], FMT[self.v_fmt], self.num_kv_heads, self.num_pages, self.layer, 0,
                       self.seed & 0xFFFFFFFFFFFFFFFF, _ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
                       _ptr(self.v_scale), _ptr(self.witness), _ptr(self.v_witness), _ptr(self.outlier_pairs),
@@ -523,7 +544,8 @@ def append_runs(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, seq_lens: t
     rows, heads, d = k.shape
     assert k.dtype == v.dtype and k.shape == v.shape and heads == cache.num_kv_heads and d == HEAD_DIM
     device = k.get_device()
-    _on(device, v, cache.k)
+    _on(device, v)
+    cache._check_device(device)
     _i32(device, seq_lens, block_table, run_starts, err)
     B, width = block_table.shape
     assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)
@@ -546,7 +568,8 @@ def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_
     rows, Hq, d = q.shape
     assert d == HEAD_DIM and out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
     device = q.get_device()
-    _on(device, out, workspace, lse, cache.k)
+    _on(device, out, workspace, lse)
+    cache._check_device(device)
     _i32(device, seq_lens, block_table, run_starts, err)
     B, width = block_table.shape
     assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)

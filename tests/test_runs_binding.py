@@ -21,3 +21,60 @@ def test_bytes_of_a_cache_are_those_of_its_tiles(kvq, k_fmt, v_fmt):
     c = kvq.PagedCache(k_fmt, v_fmt, heads, pages, device="cpu")
     per_tile = sum(kvq.tile_bytes(f, p) for f, p in ((k_fmt, 0), (v_fmt, 1), (k_fmt, 2), (v_fmt, 3), (k_fmt, 4)))
     assert c.nbytes() == heads * pages * per_tile
+
+
+class _Launched(Exception):
+    pass
+
+
+class Elsewhere:
+    """A tensor that says it is on device 1."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return (lambda: 1) if name == "get_device" else getattr(self.t, name)
+
+
+def calls(kvq, monkeypatch, cache):
+    """The two calls over ``cache`` on the host; one that gets as far as the launch raises _Launched."""
+    def launch(*a):
+        raise _Launched
+
+    monkeypatch.setattr(kvq, "_launch", launch)
+    # host tensors stand in for the device's: -1 is their device
+    x, lens, table = torch.zeros((2, 2, 128)), torch.zeros(2, dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32)
+    return (lambda: kvq.append_runs(cache, x, x, lens, table),
+            lambda: kvq.attn_runs(cache, x, lens, table, x.clone(), torch.zeros(64, dtype=torch.uint8)))
+
+
+PLANES = [("k", lambda t: t[:-1]), ("v", lambda t: t[:-1].clone()), ("v", lambda t: torch.cat([t, t])), ("k", lambda t: t.t()),
+          ("k", lambda t: t.float()), ("k", lambda t: torch.cat([t, t], 1)[:, :2048]), ("k_scale", lambda t: t[:, :-1].contiguous()),
+          ("v_scale", lambda t: t.t()), ("k_scale", lambda t: t.float()), ("v_scale", lambda t: t[:1])]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3p", "int8p"])
+def test_planes_put_into_a_cache_are_looked_at(kvq, monkeypatch, fmt):
+    for name, change in [(None, None), *PLANES]:
+        cache = kvq.PagedCache(fmt, fmt, 2, 4, device="cpu")
+        for i in range(2):
+            with pytest.raises(AssertionError if name else _Launched):
+                if name:
+                    setattr(cache, name, change(getattr(cache, name)))
+                calls(kvq, monkeypatch, cache)[i]()
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale"])
+def test_planes_of_another_device_than_the_calls(kvq, monkeypatch, name):
+    cache = kvq.PagedCache("int8p", "int8p", 2, 4, device="cpu")
+    setattr(cache, name, Elsewhere(getattr(cache, name)))
+    for call in calls(kvq, monkeypatch, cache):
+        with pytest.raises(AssertionError):
+            call()
+
+
+def test_a_cache_of_another_format_is_the_librarys_to_refuse(kvq, monkeypatch):
+    for call in calls(kvq, monkeypatch, kvq.PagedCache("int8", "int8", 2, 4, device="cpu")):
+        with pytest.raises(_Launched):
+            call()
