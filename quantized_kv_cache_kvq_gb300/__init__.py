@@ -560,11 +560,12 @@ def attn_runs_workspace_size(batch: int, num_rows: int, max_run: int, num_kv_hea
 
 
 def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, out: torch.Tensor,
-              workspace: torch.Tensor, *, run_starts: torch.Tensor | None = None, max_run: int = 1,
+              workspace: torch.Tensor, *, run_starts: torch.Tensor | None = None, max_run: int | None = None,
               lse: torch.Tensor | None = None, sm_scale: float | None = None, err: torch.Tensor | None = None, stream=None):
     """kvq_attn_runs: causal attention of the runs' queries q [rows, Hq, 128] (fp32 or bf16; rows may be strided) over a
-    page-scaled cache -> out [rows, Hq, 128] in q's type (+ lse [rows, Hq] fp32).  No run is longer than max_run;
-    run_starts None: one query token for each request."""
+    page-scaled cache -> out [rows, Hq, 128] in q's type (+ lse [rows, Hq] fp32).  No run is longer than max_run
+    (None: one token without run_starts, else as many as there are rows; the workspace goes by the same number); run_starts
+    None: one query token for each request."""
     rows, Hq, d = q.shape
     assert d == HEAD_DIM and out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
     device = q.get_device()
@@ -573,6 +574,8 @@ def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_
     _i32(device, seq_lens, block_table, run_starts, err)
     B, width = block_table.shape
     assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1)
+    if max_run is None:
+        max_run = 1 if run_starts is None else rows
     assert lse is None or (lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() == rows * Hq)
     _launch("kvq_attn_runs", lib().kvq_attn_runs, device, stream, ctypes.byref(cache.desc()), q.data_ptr(), _rows(q, rows, Hq),
             DTYPE[q.dtype], Hq, _ptr(run_starts), B, rows, max_run, block_table.data_ptr(), width, seq_lens.data_ptr(),

@@ -78,3 +78,19 @@ def test_a_cache_of_another_format_is_the_librarys_to_refuse(kvq, monkeypatch):
     for call in calls(kvq, monkeypatch, kvq.PagedCache("int8", "int8", 2, 4, device="cpu")):
         with pytest.raises(_Launched):
             call()
+
+
+@pytest.mark.parametrize("given,starts,passed", [(None, False, 1), (None, True, 6), (3, True, 3), (1, True, 1)])
+def test_max_run_is_never_less_than_the_runs_may_be(kvq, monkeypatch, given, starts, passed):
+    """Left out, it allows every run that the rows allow: none is skipped unseen."""
+    got = []
+    monkeypatch.setattr(kvq, "_launch", lambda name, fn, device, stream, *a: got.append(a))
+    cache = kvq.PagedCache("int8p", "int8p", 2, 4, device="cpu")
+    B = 2 if starts else 6
+    lens, table = torch.zeros(B, dtype=torch.int32), torch.zeros((B, 2), dtype=torch.int32)
+    q = torch.zeros((6, 4, 128))
+    kw = dict(run_starts=torch.zeros(B + 1, dtype=torch.int32)) if starts else {}
+    if given is not None:
+        kw["max_run"] = given
+    kvq.attn_runs(cache, q, lens, table, q.clone(), torch.zeros(64, dtype=torch.uint8), **kw)
+    assert got[0][5:8] == (kw["run_starts"].data_ptr() if starts else None, B, 6) and got[0][8] == passed
