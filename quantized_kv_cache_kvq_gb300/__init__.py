@@ -569,6 +569,7 @@ def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_
     rows, Hq, d = q.shape
     assert d == HEAD_DIM and out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
     device = q.get_device()
+    assert workspace.is_contiguous(), "workspace: one piece of memory"
     _on(device, out, workspace, lse)
     cache._check_device(device)
     _i32(device, seq_lens, block_table, run_starts, err)

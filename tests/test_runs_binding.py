@@ -94,3 +94,14 @@ def test_max_run_is_never_less_than_the_runs_may_be(kvq, monkeypatch, given, sta
         kw["max_run"] = given
     kvq.attn_runs(cache, q, lens, table, q.clone(), torch.zeros(64, dtype=torch.uint8), **kw)
     assert got[0][5:8] == (kw["run_starts"].data_ptr() if starts else None, B, 6) and got[0][8] == passed
+
+
+def test_a_workspace_in_pieces_is_refused(kvq, monkeypatch):
+    """Its bytes would be taken in a row from its address, those between the pieces among them."""
+    cache = kvq.PagedCache("int8p", "int8p", 2, 4, device="cpu")
+    monkeypatch.setattr(kvq, "_launch", lambda *a: None)
+    lens, table, q = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32), torch.zeros((2, 2, 128))
+    ws = torch.zeros((64, 2), dtype=torch.uint8)
+    kvq.attn_runs(cache, q, lens, table, q.clone(), ws)
+    with pytest.raises(AssertionError):
+        kvq.attn_runs(cache, q, lens, table, q.clone(), ws[:, 0])
