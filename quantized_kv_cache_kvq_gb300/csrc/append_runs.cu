@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 2048;
+constexpr int kSmemStatic = 2 * kTile + 128;  // of the kernel, at most
 
 struct AppendArgs {
   uint8_t* k;
@@ -154,7 +155,7 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 constexpr int kStages = 2;  // an item on its way while one is quantized
-// Blocks on an SM.  11996 tokens of 8 heads, bf16, inputs not in the L2: 20.6 us with 6 blocks and 2 stages, 22.4 with 7 and
+// Blocks on an SM, where its shared memory holds as many.  11996 tokens of 8 heads, bf16, inputs not in the L2: 20.6 us with 6 blocks and 2 stages, 22.4 with 7 and
 // 2, 22.3 with 6 and 3, 21.5 with 5 and 3, 28.6 with 8 and 3 (64 registers do not hold the loop).
 constexpr int kBlocksBf16 = 6, kBlocksF32 = 4;
 template <bool BF16>
@@ -444,8 +445,14 @@ cudaError_t launch(const AppendArgs& a, long long items, cudaStream_t s) {
   static SmemLimit limit;
   const cudaError_t e = limit.raise(kern, smem_of(kMaxBatch));
   if (e != cudaSuccess) return e;
-  // as many blocks as the SMs hold (152 SMs), each going through its share of the items
-  kern<<<static_cast<unsigned>(std::min<long long>(items, 152 * (BF16 ? kBlocksBf16 : kBlocksF32))), kThreads, smem, s>>>(a);
+  // As many blocks as the SMs hold at once, each going through its share of the items: a large batch's tables leave room for
+  // fewer (bf16, 1024 requests: five; of 64 tokens and 8 heads each 265 us with six, the sixth a second wave, 175 with five).
+  const int sms = device_sm_count(), sm_smem = device_attr<cudaDevAttrMaxSharedMemoryPerMultiprocessor>();
+  const int reserved = device_attr<cudaDevAttrReservedSharedMemoryPerBlock>();
+  if (sms <= 0 || sm_smem <= 0) return cudaErrorInvalidDevice;
+  const int fit = std::max(1, sm_smem / static_cast<int>(smem + kSmemStatic + reserved));
+  const long long blocks = static_cast<long long>(sms) * std::min(BF16 ? kBlocksBf16 : kBlocksF32, fit);
+  kern<<<static_cast<unsigned>(std::min(items, blocks)), kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 

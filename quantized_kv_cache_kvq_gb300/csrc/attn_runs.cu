@@ -621,18 +621,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const AttnArgs 
 }
 
 // ------------------------------------------------------------------------------------------------ host
-int sm_count() {
-  static int cache[kMaxDevices] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  if (!cache[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -724,7 +712,7 @@ extern "C" size_t kvq_attn_runs_workspace_size(int32_t batch, int32_t num_rows, 
   if (batch < 0 || batch > kMaxBatch || num_rows < 0 || max_run < 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
       num_q_heads % num_kv_heads || (q_dtype != KVQ_DTYPE_F32 && q_dtype != KVQ_DTYPE_BF16))
     return 0;
-  const int sms = sm_count();
+  const int sms = device_sm_count();
   if (sms <= 0) return 0;
   return workspace(batch, num_rows, max_run, num_kv_heads, num_q_heads, q_dtype, sms).total;
 }
@@ -750,7 +738,7 @@ extern "C" kvq_status kvq_attn_runs(const kvq_cache* cache, const void* q, int64
   if (q_row_stride < static_cast<int64_t>(num_q_heads) * kHeadDim || q_row_stride % unit) return KVQ_ERR_INVALID_ARG;
   if (!q || !seq_lens || !out || !workspace_dev || (max_pages_per_seq > 0 && !block_table)) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace_dev)) return KVQ_ERR_INVALID_ARG;
-  const int sms = sm_count(), smem_max = device_smem_optin();
+  const int sms = device_sm_count(), smem_max = device_smem_optin();
   if (sms <= 0 || smem_max <= 0) return KVQ_ERR_CUDA;
   const int mr = std::min(max_run, num_rows);
   const Workspace w = workspace(batch, num_rows, mr, hkv, num_q_heads, q_dtype, sms);

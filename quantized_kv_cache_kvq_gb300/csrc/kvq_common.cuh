@@ -93,17 +93,21 @@ __host__ __device__ __forceinline__ int vw_offset(int t, int k) { return 8 * (t 
 // Devices a process can drive (per-device caches of attributes and of kernel settings).
 constexpr int kMaxDevices = 64;
 
-// Most shared memory that a block of the current device can have (static and dynamic); 0 when it cannot be told.
-inline int device_smem_optin() {
+// An attribute of the current device; 0 when it cannot be told.
+template <cudaDeviceAttr kAttr>
+inline int device_attr() {
   static std::atomic<int> cache[kMaxDevices] = {};
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   if ((n = cache[dev].load(std::memory_order_relaxed)) == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&n, kAttr, dev) != cudaSuccess) return 0;
     cache[dev].store(n, std::memory_order_relaxed);
   }
   return n;
 }
+inline int device_sm_count() { return device_attr<cudaDevAttrMultiProcessorCount>(); }
+// Most shared memory that a block can have, static and dynamic.
+inline int device_smem_optin() { return device_attr<cudaDevAttrMaxSharedMemoryPerBlockOptin>(); }
 
 // A kernel's dynamic shared memory limit: a setting of the device's context that all host threads share.  So it is always set to
 // the same value, the most that any call of the kernel needs, and threads whose first calls meet write the same thing.

@@ -32,3 +32,16 @@ def test_shared_memory_limits_do_not_depend_on_the_call(fake):
 def test_first_calls_of_two_threads_leave_every_batch_possible(fake):
     r = fake("threads")
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("sms", [152, 100, 1])
+def test_the_appends_grid_is_what_the_device_holds_at_once(fake, sms):
+    """A persistent grid of more blocks than are resident would run as two waves, each block of the second with a full share."""
+    r = fake("grid", str(sms))
+    assert r.returncode == 0, r.stdout + r.stderr
+    rows = [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
+    assert len(rows) == 4
+    for dtype, batch, blocks, smem in rows:
+        fits = 228 * 1024 // (smem + 4096 + 1024)  # two staged tiles, what the device keeps for itself
+        assert blocks % sms == 0 and 1 <= blocks // sms <= fits, (dtype, batch, blocks, fits)
+        assert blocks // sms >= min(fits, 4)
