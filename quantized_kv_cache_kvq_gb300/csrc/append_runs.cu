@@ -230,14 +230,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? kBlocksBf16 : kBlocksF32) app
     }
     while (w.run + 1 < a.batch && s_cum[w.run + 1] <= w.pi) ++w.run;
   };
-  struct Page {
-    int first, p0, from, to, page;  // the run's first position, the page's, its new tokens [from, to), its index
-  };
-  auto page_at = [&](const Walk& w) {
-    const int first = s_first[w.run], len = s_len[w.run], nth = w.pi - s_cum[w.run], page = first / kPage + nth;
-    if (nth < 0 || len <= 0 || nth > (len - 1) / kPage - first / kPage) return Page{0, 0, 0, 0, 0};  // wrapped sums of overlapping runs
-    return Page{first, page * kPage, max(first - page * kPage, 0), min(len - page * kPage, kPage), page};
-  };
+  auto page_at = [&](const Walk& w) { return page_of_run(s_first[w.run], s_len[w.run], w.pi - s_cum[w.run]); };
   Walk ahead{static_cast<int>(blockIdx.x / a.H), static_cast<int>(blockIdx.x % a.H), 0};
   {
     int hi = a.batch - 1;  // last run with cum <= pi
@@ -252,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? kBlocksBf16 : kBlocksF32) app
   auto entry_of = [&](int stage) { return reinterpret_cast<int*>(stages + stage * stage_bytes<BF16>() + kThreads * 4 * kWords * 16) + tid; };
   auto fetch = [&](long long item, int stage) {
     if (item < items) {
-      const Page p = page_at(ahead);
+      const RunPage p = page_at(ahead);
       uint4* dst = words_of(stage);
       copy4(entry_of(stage), a.block_table + static_cast<size_t>(ahead.run) * a.max_pages + p.page);
 #pragma unroll
@@ -279,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? kBlocksBf16 : kBlocksF32) app
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     fetch(item + static_cast<long long>(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);
     copies_wait<kStages - 1>();
-    const Page page = page_at(here);
+    const RunPage page = page_at(here);
     const int h = here.h, from = page.from, phys = *entry_of(stage);
     advance(here);
     float x[2][2][8];  // [plane][token t8, t8 + 8][channel]

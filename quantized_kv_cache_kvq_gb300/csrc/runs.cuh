@@ -27,6 +27,19 @@ __device__ __forceinline__ Run load_run(const int32_t* run_starts, const int32_t
   return Run{a, b - a, len};
 }
 
+// Page nth of those that a run of positions first .. len - 1 touches: the run's first position, the page's, its new tokens [from, to),
+// its index.  Nothing (to = from) for one that the run does not have, whatever the numbers: where runs overlap, against the
+// rules, the sums over them may wrap, and a page may be looked up in a run that has none.
+struct RunPage {
+  int first, p0, from, to, page;
+};
+__host__ __device__ __forceinline__ RunPage page_of_run(int first, int len, int nth) {
+  const int page = first / kPage + nth;
+  if (nth < 0 || first < 0 || len <= 0 || nth > (len - 1) / kPage - first / kPage) return RunPage{0, 0, 0, 0, 0};
+  const int p0 = page * kPage;
+  return RunPage{first, p0, first > p0 ? first - p0 : 0, len - p0 < kPage ? len - p0 : kPage, page};
+}
+
 // 2^e as fp16 bits, kMinExp <= e <= kMaxExp: subnormal below 2^-14.
 __device__ __forceinline__ uint16_t exp_to_f16(int e) {
   return static_cast<uint16_t>(e >= -14 ? (e + 15) << 10 : 1 << (e + 24));
