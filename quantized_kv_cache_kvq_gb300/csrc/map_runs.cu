@@ -9,9 +9,10 @@
 // updated in place (lengths, stack height) and their look at the page numbers: a step is taken whole or not at all.
 // A request's pages are those of its length, or the caller keeps their number beside it: a draft's rejected tokens then leave
 // their pages with the request, which uses them before it takes new ones.
-// Bound by latency: one launch, two dependent rounds of loads.  64 requests of one token 5.9 us in a graph (8.4 a call from Python),
-// 256 requests with prompts and finished ones among them 10.9 (12.3), 1024 prompts of 83,360 tokens 13.5 (15.0).  Rows written between
-// the halves of the cluster barrier, which hides it: 13.5 as well.
+// Bound by latency: one launch, two dependent rounds of loads.  64 requests of one token 5.8 us in a graph (8.4 a call from Python),
+// 256 requests with prompts and finished ones among them 10.8 (12.3), 1024 prompts of 83,360 tokens 13.4 (15.0), 1.2 of which the
+// look at the page numbers and the barrier behind it cost.  Rows written ahead of the look, or between the halves of the barrier,
+// come to the same or more (13.9, 13.5).
 #include "runs.cuh"
 
 namespace kvq {
@@ -19,7 +20,6 @@ namespace runs {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kKept = 2;  // pages that a thread keeps from its look at them until it writes them
 constexpr int kMaxPage = 0x7FFFFFFF / kPage;  // the last page whose slots fit 31 bits
 
 struct MapArgs {
@@ -150,19 +150,23 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     odd_page |= page < 0 || page > kMaxPage;
     return page;
   };
-  int out[kKept] = {}, back[kKept] = {};  // this thread's first pages, for the second time
+  int out0 = 0, out1 = 0, back0 = 0, back1 = 0;  // this thread's first pages, kept until they are written
   if (ok) {
     if (tid < a.batch && add > 0)
       for (int j = old / kPage, end = min(held, (old + add + kPage - 1) / kPage); j < end; ++j)
         look(a.block_table[static_cast<size_t>(tid) * a.max_pages + j]);
-#pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-      const int i = first + k * stride;
-      if (i < A) out[k] = look(page_of(i));
-      if (i < R - A) back[k] = look(handed_back(i));
+#pragma unroll 1
+    for (int i = first; i < A; i += stride) {
+      const int page = look(page_of(i));
+      if (i == first) out0 = page;
+      if (i == first + stride) out1 = page;
     }
-    for (int i = first + kKept * stride; i < A; i += stride) look(page_of(i));
-    for (int i = first + kKept * stride; i < R - A; i += stride) look(handed_back(i));
+#pragma unroll 1
+    for (int i = first; i < R - A; i += stride) {
+      const int page = look(handed_back(i));
+      if (i == first) back0 = page;
+      if (i == first + stride) back1 = page;
+    }
   }
   if (!alone) asm volatile("barrier.cluster.wait;" ::: "memory");
   odd_page = __syncthreads_or(odd_page);
@@ -184,18 +188,15 @@ __global__ void __launch_bounds__(kThreads, 1) map_runs_kernel(const MapArgs a) 
     n_rows = A = 0;
   }
   if (ok) {
-    auto hand_out = [&](int i, int page) {
+#pragma unroll 1
+    for (int i = first; i < A; i += stride) {
       const int s = find_segment(s_want, a.batch, i);
-      a.block_table[static_cast<size_t>(s) * a.max_pages + s_held[s] + (i - s_want[s])] = page;
-    };
-#pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-      const int i = first + k * stride;
-      if (i < A) hand_out(i, out[k]);
-      if (i < R - A) a.free_pages[fc + i] = back[k];
+      a.block_table[static_cast<size_t>(s) * a.max_pages + s_held[s] + (i - s_want[s])] =
+          i == first ? out0 : i == first + stride ? out1 : page_of(i);
     }
-    for (int i = first + kKept * stride; i < A; i += stride) hand_out(i, page_of(i));
-    for (int i = first + kKept * stride; i < R - A; i += stride) a.free_pages[fc + i] = handed_back(i);
+#pragma unroll 1
+    for (int i = first; i < R - A; i += stride)
+      a.free_pages[fc + i] = i == first ? back0 : i == first + stride ? back1 : handed_back(i);
   }
   if (a.slots || a.positions) {
     // four rows in a row to a thread: one search, and mostly one page, for them
