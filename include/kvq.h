@@ -444,7 +444,8 @@ kvq_status kvq_meter(const float* meter_state_dev, int32_t n_layers, int32_t bat
  * pages that their new tokens need, and every row its slot and position.
  *
  * new_lens_dev: [batch] int32, tokens that request s adds (0 allowed); negative: the request is finished, all its pages go
- *   back, whoever else's table holds them (shared pages: kvq_map_runs_ex), and its length becomes 0.  seq_lens_dev: [batch] lengths before the step.
+ *   back, whoever else's table holds them (shared pages: kvq_map_runs_ex), and its length becomes 0.
+ * seq_lens_dev: [batch] lengths before the step.
  * free_pages_dev: [free_capacity] int32 stack of free pages, entries 0 .. *free_count_dev - 1 in use.  Pages handed back
  *   are pushed in order of request and page, then the pages needed are popped one by one in order of request and page.
  * block_table_dev: [batch][max_pages_per_seq]; the entries of new pages are written, the others kept (those of a
@@ -518,7 +519,8 @@ size_t kvq_attn_runs_workspace_size(int32_t batch, int32_t num_rows, int32_t max
  *
  * q_dev: [num_rows] rows of [num_q_heads][128] post-RoPE queries (q_dtype), 16-byte aligned, q_row_stride elements apart
  *   (>= num_q_heads * 128, a multiple of 16 bytes); query head h reads kv head h / (num_q_heads / num_kv_heads).
- * max_run: no run of the call is longer; it chooses the kernels and sizes the workspace.
+ * max_run: no run of the call is longer (a longer one is reported and skipped); it chooses the kernels, for all requests of
+ *   the call, and sizes the workspace.
  * out_dev: [num_rows][num_q_heads][128] in the queries' type.  lse_dev (nullable): [num_rows][num_q_heads] fp32,
  *   ln sum_t e^{x_t}.  A row that sees no token (an empty context) gives 0 and -inf.
  * BF16 queries: the softmax weights are rounded to fp16 (11 bits; weights below 2^-21 of the largest, page scale included,

@@ -7,7 +7,7 @@
 // ring of bulk copies per warp, the page's 16 tokens are the M dimension of every tensor-core product (mma.sync: a page gives
 // each row 2 x 2048 multiply-adds for 4096 bytes, far below where the tensor rate matters), and the pieces are merged
 // with log-sum-exp weights.  Bound by HBM: 4,100 bytes a page and kv head.  64 requests of 32768 tokens, 4 kv and 28 query heads,
-// INT8: 349 us, 6,160 GB/s (91 % of the copy rate); 128 of 1024..16384, 8 and 32 heads, E4M3: 265 us, 5,940 GB/s; 16 drafts of
+// INT8: 345 us, 6,240 GB/s (92 % of the copy rate); 128 of 1024..16384, 8 and 32 heads, E4M3: 262 us, 6,010 GB/s; 16 drafts of
 // 2..4 tokens over 11000..11996, two row blocks a page: 79 us, 4,790 GB/s (dependent products that 12 warps do not hide).
 #include <algorithm>
 #include <cmath>
@@ -637,7 +637,9 @@ struct Workspace {
   long long tiles;
 };
 
-// BF16 runs of more than 16 (token, head) rows are the tile kernel's; fp32 queries have the split kernel for every length.
+// BF16 runs of more than 16 (token, head) rows, where a unit's two row blocks end, are the tile kernel's; fp32 queries have the split
+// kernel for every length.  16 drafts over 11500 tokens, 8 and 32 heads, E4M3 (INT8): the split kernel, one pass over the context for
+// every 16 rows, 96 us (95) at 16 rows, 141-143 (152) at 20 to 32, 213 (217) at 48; the tile kernel 200 (208) at 20 to 48.
 constexpr int kFewRows = 16;
 
 Workspace workspace(int batch, int num_rows, int max_run, int hkv, int hq, int q_dtype, int sms) {
