@@ -526,6 +526,8 @@ size_t kvq_attn_runs_workspace_size(int32_t batch, int32_t num_rows, int32_t max
  * BF16 queries: the softmax weights are rounded to fp16 (11 bits; weights below 2^-21 of the largest, page scale included,
  *   to a step of 2^-31 of it) before the value product, everything else is exact or binary32.  F32 queries: queries and
  *   weights are carried in two fp16 parts (22 bits).  Products are summed in binary32; the same call gives the same bits.
+ *   The value scales are carried in the exponents, in binary32: lse is off by up to 2^-17 (absolute) beside the rounding of
+ *   the logits where they are near 2^-24 or far apart.
  * Device errors: KVQ_ERR_DEVICE_BOUNDS (a run that cannot be; a page outside the cache, which is left out of its request's
  *   sums), KVQ_ERR_TIMEOUT.
  * workspace_dev: at least kvq_attn_runs_workspace_size() bytes, 16-byte aligned; calls that can run at the same time
