@@ -278,13 +278,12 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
   const int cum_bytes = ((a.batch + 1) * 12 + 127) & ~127;
   int* cumt = reinterpret_cast<int*>(smem + (a.batch + 1) * 8);  // row tiles of the requests before
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long all_tiles = 0;  // runs that overlap, against the rules, may have more than 32 bits count
   {
-    __shared__ long long w_pages[NW];
-    __shared__ int w_tiles[NW];
+    __shared__ long long w_pages[NW], w_tiles[NW];
     const int per = (a.batch + blockDim.x - 1) / blockDim.x;
     const int s0 = threadIdx.x * per;
-    long long lp = 0;
-    int lt = 0;
+    long long lp = 0, lt = 0;
     for (int i = 0; i < per; ++i) {
       const int s = s0 + i;
       if (s < a.batch) {
@@ -298,24 +297,24 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
         lt += t;
       }
     }
-    long long ip = lp;
-    int it = lt;
+    long long ip = lp, it = lt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long tp = __shfl_up_sync(kFull, ip, o);
-      const int tt = __shfl_up_sync(kFull, it, o);
+      const long long tt = __shfl_up_sync(kFull, it, o);
       if (lane >= o) { ip += tp; it += tt; }
     }
     if (lane == 31) { w_pages[warp] = ip; w_tiles[warp] = it; }
     __syncthreads();
-    long long rp = ip - lp;
-    int rt = it - lt;
+    long long rp = ip - lp, rt = it - lt;
     for (int w = 0; w < warp; ++w) { rp += w_pages[w]; rt += w_tiles[w]; }
+    for (int w = 0; w < NW; ++w) all_tiles += w_tiles[w];
     for (int i = 0; i < per; ++i) {
       const int s = s0 + i;
       if (s < a.batch) {
         cum[s + 1] = rp += cum[s + 1];
-        cumt[s + 1] = rt += cumt[s + 1];
+        rt += cumt[s + 1];
+        cumt[s + 1] = static_cast<int>(rt);
       }
     }
     if (threadIdx.x == 0) {
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(NW * 32, 1) split_kernel(const AttnArgs a) {
     }
     __syncthreads();
   }
-  if (cumt[a.batch] > a.max_tiles || cumt[a.batch] < 0) {  // runs that overlap: more tiles than the rows can make
+  if (all_tiles > a.max_tiles) {  // runs that overlap: more tiles than the rows can make
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       report(a.err, KVQ_ERR_DEVICE_BOUNDS);
       *a.ws_units = 0;  // nothing for the merge
