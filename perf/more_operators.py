@@ -1,0 +1,700 @@
+"""A speculative step over a page-scaled 8-bit KV cache, whose drafts are trees of tokens.
+
+A request's run (the new tokens that it brings to a step) is a tree: row 0 is the token chosen last, every other row is a
+drafted token below its parent, an earlier row of the run.  Row i sees the request's context, its ancestors and itself.
+
+* ``tree``: parents -> masks of ancestors and positions (``tree_runs``);
+* ``rope``: queries and keys normed per head and rotated to those positions (``rope_runs``);
+* ``attn``: attention of the tree's queries over the cache (``attn_tree``);
+* ``verify``: which path of the tree the target's probabilities accept, from given random numbers (``verify_runs``);
+* ``keep``: the accepted path's keys and values moved to the front of the run, in all layers (``keep_runs``).
+"""
+import math
+
+import torch
+
+own = False
+
+PAGE, D = 16, 128
+E_MIN, E_MAX = -24, 15  # page scales are powers of two that fp16 holds
+ONE = 2.0 ** 44  # probabilities are summed as whole numbers of 2^-44
+DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ------------------------------------------------------------------------------------------------ cases
+def listed():
+    return [
+        # the usual step: 16 requests with trees of up to 64 tokens
+        dict(name="tree_step", op="tree", batch=16, run_lo=25, run_hi=64, spread=8, lo=2000, hi=12000),
+        # a full batch of the largest trees, chains of hundreds of tokens among their branches
+        dict(name="tree_full", op="tree", batch=1024, run_lo=200, run_hi=1000, spread=2, lo=1, hi=2000),
+        # the trees' queries and keys, as slices of a fused projection with norms of each head
+        dict(name="rope_step", op="rope", batch=16, run_lo=25, run_hi=64, spread=8, lo=2000, hi=12000, kv_heads=8, q_heads=32, dtype="bf16",
+             norm=True, inside=True),
+        # a whole prompt of the cartridge workload's length (a chain), fp32, without norms, to tensors of their own
+        dict(name="rope_prompt_f32", op="rope", batch=1, run_lo=11996, run_hi=11996, spread=1, lo=11996, hi=11996, kv_heads=4, q_heads=28,
+             dtype="f32", norm=False, inside=False),
+        # the smallest call: one tree of 7 tokens over 512, fp32 queries
+        dict(name="attn_tiny_f32", op="attn", batch=1, run_lo=7, run_hi=7, spread=3, lo=512, hi=512, kv_heads=8, q_heads=32, fmt="int8p",
+             dtype="f32"),
+        # little trees of up to 4 tokens beside single ones, in a ragged batch
+        dict(name="attn_little", op="attn", batch=96, run_lo=1, run_hi=4, spread=2, lo=1024, hi=16384, kv_heads=8, q_heads=32, fmt="e4m3p",
+             dtype="bf16"),
+        # trees of up to 16 tokens over the cartridge workload's length
+        dict(name="attn_trees", op="attn", batch=16, run_lo=9, run_hi=16, spread=4, lo=11000, hi=11996, kv_heads=8, q_heads=32, fmt="e4m3p",
+             dtype="bf16"),
+        # the widest: trees of up to 64 tokens, 7 query heads for each kv head, a large batch of the 7B shape
+        dict(name="attn_wide", op="attn", batch=64, run_lo=25, run_hi=64, spread=8, lo=2000, hi=8192, kv_heads=4, q_heads=28, fmt="int8p",
+             dtype="bf16"),
+        # greedy decoding: the largest logit decides
+        dict(name="verify_greedy", op="verify", batch=16, run_lo=9, run_hi=16, spread=4, vocab=32000, dtype="bf16", how="greedy"),
+        # sampling from probabilities, drafts from a smaller model's distribution
+        dict(name="verify_drafts", op="verify", batch=32, run_lo=25, run_hi=64, spread=6, vocab=131072, dtype="f32", how="draft"),
+        # one layer of a few requests
+        dict(name="keep_layer", op="keep", batch=4, run_lo=9, run_hi=16, spread=4, lo=200, hi=400, kv_heads=4, layers=1, fmt="int8p"),
+        # the accepted paths of a step in all layers of the Qwen3-8B shape
+        dict(name="keep_model", op="keep", batch=32, run_lo=25, run_hi=64, spread=6, lo=40, hi=300, kv_heads=8, layers=36, fmt="e4m3p"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.49)))))))
+
+
+def draw(rng):
+    op = rng.choice(["tree", "rope", "attn", "attn", "verify", "keep"])
+    fmt = rng.choice(["e4m3p", "int8p"])
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    spread = rng.choice([1, 2, 4, 8, 30])
+    if op == "tree":
+        hi = _log(rng, 1, 1000)
+        return dict(op=op, batch=_log(rng, 1, 1024), run_lo=max(1, hi // rng.choice([1, 2, 5])), run_hi=hi, spread=spread, lo=0, hi=_log(rng, 1, 30000))
+    if op == "rope":
+        batch, hi = _log(rng, 1, 64), _log(rng, 1, 180)
+        kv = rng.choice([1, 2, 4, 8])
+        return dict(op=op, batch=batch, run_lo=max(1, hi // 2), run_hi=hi, spread=spread, lo=0, hi=_log(rng, 1, 12000), kv_heads=kv,
+                    q_heads=kv * rng.choice([1, 2, 4]), dtype=dtype, norm=rng.random() < 0.6, inside=rng.random() < 0.5)
+    if op == "attn":
+        kv = rng.choice([1, 2, 4, 8])
+        group = min(rng.choice([1, 2, 3, 4, 7, 8]), 32 // kv)
+        batch = _log(rng, 1, 64)
+        hi = _log(rng, 16, min(16384, 400000 // batch))
+        run = _log(rng, 1, 200 if batch < 8 else 64)
+        if dtype == "f32":
+            run = min(run, 16)
+        return dict(op=op, batch=batch, run_lo=max(1, run // 3), run_hi=run, spread=spread, lo=hi // 8, hi=hi, kv_heads=kv, q_heads=kv * group,
+                    fmt=fmt, dtype=dtype)
+    if op == "verify":
+        batch = _log(rng, 1, 32)
+        hi = _log(rng, 1, 60)
+        return dict(op=op, batch=batch, run_lo=max(1, hi // 2), run_hi=hi, spread=rng.choice([1, 2, 4, 8]), vocab=_log(rng, 1000, 131072),
+                    dtype=dtype, how=rng.choice(["greedy", "draft", "draft", "target"]))
+    hi = _log(rng, 2, 100)
+    return dict(op=op, batch=_log(rng, 1, 32), run_lo=max(1, hi // 2), run_hi=hi, spread=spread, lo=0, hi=_log(rng, 1, 300),
+                kv_heads=rng.choice([1, 2, 3, 4, 8]), layers=_log(rng, 1, 36), fmt=fmt)
+
+
+# ------------------------------------------------------------------------------------------------ inputs
+def _lens(case, what):
+    """Lengths of a case: log-uniform between its bounds, the last one at the upper bound; part of the case, not of the seed's data."""
+    lo, hi = case[what[0]], case[what[1]]
+    u = torch.rand(case["batch"], generator=torch.Generator().manual_seed(11 if what[0] == "lo" else 29), dtype=torch.float64)
+    a, b = math.log(max(lo, 0.5)), math.log(max(hi, 0.5) + 0.49)
+    x = torch.exp(a + u * (b - a)).round().long().clamp(lo, hi)
+    x[-1] = hi
+    return x
+
+
+def _shape(case):
+    """Runs of the requests, and the lengths of their contexts before them."""
+    n = _lens(case, ("run_lo", "run_hi"))
+    before = _lens(case, ("lo", "hi")) if "lo" in case else torch.zeros_like(n)
+    if case["op"] in ("attn", "rope"):  # lengths that count the run
+        before = (before - n).clamp(min=0)
+    return n, before
+
+
+def _trees(n, spread, seed):
+    """Parents of all rows: row 0 of a run is its root, row i hangs below one of the `spread` rows before it."""
+    g = torch.Generator().manual_seed(seed * 31 + 7)
+    starts = torch.cat([torch.zeros(1, dtype=torch.int64), n.cumsum(0)])
+    i = torch.arange(int(starts[-1])) - torch.repeat_interleave(starts[:-1], n)
+    back = (torch.rand(i.shape, generator=g) * i.clamp(min=1, max=spread)).long()
+    return torch.where(i == 0, -1, i - 1 - back), starts
+
+
+def _depths(parents, starts, n):
+    """Depth of every row below its run's root (on the host)."""
+    root = torch.repeat_interleave(starts[:-1], n)
+    up = torch.where(parents < 0, torch.arange(len(parents)), root + parents)
+    depth = (parents >= 0).long()
+    while True:
+        more = depth + depth[up]
+        if torch.equal(more, depth):
+            return depth
+        depth, up = more, up[up]
+
+
+def _pages(n):
+    return (n + PAGE - 1) // PAGE
+
+
+def _tables(lens, g, dev):
+    """A block table over pages in random order, and how many pages there are."""
+    counts = _pages(lens)
+    width, total = int(counts.max()) + 1, int(counts.sum()) + 3
+    perm = torch.randperm(total, generator=g, device=dev).to(torch.int32)
+    first = counts.cumsum(0) - counts
+    at = (first[:, None] + torch.arange(width)[None, :]).clamp(max=total - 1).to(dev)
+    mine = (torch.arange(width)[None, :] < counts[:, None]).to(dev)
+    return torch.where(mine, perm[at], torch.full((1, 1), -1, dtype=torch.int32, device=dev)).contiguous(), total
+
+
+def _codes_random(n, fmt, g, dev):
+    """[n, 2048] bytes of codes as a normal distribution fills them."""
+    out = torch.empty((n, PAGE * D), dtype=torch.uint8, device=dev)
+    step = 1 << 16
+    for i in range(0, n, step):
+        x = torch.randn((min(step, n - i), PAGE * D), generator=g, device=dev)
+        if fmt == "int8p":
+            out[i:i + step] = (x * 36).round_().clamp_(-127, 127).add_(128).to(torch.uint8)
+        else:
+            out[i:i + step] = (x * 120).clamp_(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return out
+
+
+def _scales_random(shape, fmt, g, dev):
+    """Powers of two, fp16: about unit variance for the values that the codes stand for."""
+    e = torch.randint(0, 2, shape, generator=g, device=dev) - (6 if fmt == "int8p" else 7)
+    return torch.exp2(e.float()).to(torch.float16)
+
+
+def _masks(parents, starts, n, words):
+    """Bit j of row i: row j of the run is row i or an ancestor of it.  [rows, words] int32."""
+    rows = int(starts[-1])
+    root = torch.repeat_interleave(starts[:-1], n)
+    up = torch.where(parents < 0, torch.arange(rows, device=parents.device), root + parents)
+    sees = torch.zeros((rows, 32 * words), dtype=torch.bool, device=parents.device)
+    sees[torch.arange(rows, device=parents.device), torch.arange(rows, device=parents.device) - root] = True
+    for _ in range(max(1, (int(n.max()) - 1).bit_length())):  # ancestors 1, 2, 4, .. further up
+        sees = sees | sees[up]
+        up = up[up]
+    return _bits(sees)
+
+
+def _bits(sees):
+    w = sees.view(sees.shape[0], -1, 32).long() << torch.arange(32, device=sees.device)
+    w = w.sum(-1)
+    return torch.where(w >= 1 << 31, w - (1 << 32), w).to(torch.int32)
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(int(seed))
+    i32 = dict(dtype=torch.int32, device=dev)
+    n, before = _shape(case)
+    B, after = case["batch"], before + n
+    # a step's trees go by its drafts: other ones with every seed where they are the input, the same work where they are not
+    parents, starts = _trees(n, case["spread"], int(seed) if case["op"] in ("tree", "keep") else 1)
+    rows, top = int(starts[-1]), int(n.max())
+    words = (top + 31) // 32
+    st = dict(case=case, op=case["op"], rows=rows, top=top, err=torch.zeros(1, **i32), run_starts=starts.to(**i32),
+              n=n.to(dev), starts=starts.to(dev))
+    if case["op"] == "tree":
+        st.update(parents=parents.to(**i32), seq_lens=after.to(**i32), mask=torch.zeros((rows, words), **i32),
+                  positions=torch.zeros(rows, **i32))
+        return st
+    if case["op"] == "rope":
+        Hq, H, dt = case["q_heads"], case["kv_heads"], DTYPE[case["dtype"]]
+        theta = 1e6 ** (-torch.arange(64, dtype=torch.float64, device=dev) / 64)
+        angle = torch.arange(int(after.max()) + 1, dtype=torch.float64, device=dev)[:, None] * theta
+        fused = torch.randn((rows, Hq + 2 * H, D), generator=g, device=dev)
+        fused[..., ::37] *= 6  # a few large channels, as trained models have them
+        depth = _depths(parents, starts, n)
+        weight = lambda: (1 + 0.2 * torch.randn(D, generator=g, device=dev)) if case["norm"] else None  # noqa: E731
+        fused = fused.to(dt)
+        st.update(q=fused[:, :Hq], k=fused[:, Hq:Hq + H], positions=(torch.repeat_interleave(before, n) + depth).to(**i32),
+                  cos_sin=torch.cat([angle.cos(), angle.sin()], 1).float().contiguous(), q_weight=weight(), k_weight=weight())
+        # in place a second pass would norm and rotate what the first one left: the inputs of every pass are copied in by it
+        st.update(q_out=torch.zeros((rows, Hq, D), dtype=dt, device=dev), k_out=torch.zeros((rows, H, D), dtype=dt, device=dev))
+        if case["inside"]:  # the keys' heads between other ones, as an append takes them
+            st["k_out"] = torch.zeros((rows, 2 * H, D), dtype=dt, device=dev)[:, :H]
+        return st
+    if case["op"] == "verify":
+        return _prepare_verify(case, st, parents, g, dev)
+    H, fmt, L = case["kv_heads"], case["fmt"], case.get("layers", 1)
+    bt, total = _tables(after, g, dev)
+    st.update(k=_codes_random(L * total * H, fmt, g, dev).view(L, total * H, -1), v=_codes_random(L * total * H, fmt, g, dev).view(L, total * H, -1),
+              k_scale=_scales_random((L, H, total), fmt, g, dev), v_scale=_scales_random((L, H, total), fmt, g, dev), bt=bt, total=total)
+    if case["op"] == "attn":
+        dt = DTYPE[case["dtype"]]
+        st.update(seq_lens=after.to(**i32), mask=_masks(parents, starts, n, words).to(dev),
+                  q=(torch.randn((rows, case["q_heads"], D), generator=g, device=dev) * 1.5).to(dt),
+                  out=torch.zeros((rows, case["q_heads"], D), dtype=dt, device=dev), lse=torch.zeros((rows, case["q_heads"]), device=dev))
+        return st
+    # the path to a row that is no deeper than accepted drafts are
+    depth = _depths(parents, starts, n)
+    lists = torch.full((rows,), -1, dtype=torch.int64)
+    kept = torch.zeros(B, dtype=torch.int64)
+    pick = torch.rand(rows, generator=torch.Generator().manual_seed(int(seed) + 3))
+    pick = torch.where(depth <= 6, pick, -1.0)
+    for s in range(B):
+        a, b = int(starts[s]), int(starts[s + 1])
+        i = int(pick[a:b].argmax())
+        path = []
+        while i >= 0:
+            path.append(i)
+            i = int(parents[a + i])
+        kept[s] = len(path)
+        lists[a:a + len(path)] = torch.tensor(path[::-1])
+    st.update(keep=lists.to(**i32), kept=kept.to(**i32), seq_lens=(before + kept).to(**i32), kept_top=int(kept.max()))
+    return st
+
+
+def _prepare_verify(case, st, parents, g, dev):
+    rows, V, dt = st["rows"], case["vocab"], DTYPE[case["dtype"]]
+    n, starts = st["n"], st["starts"]
+    i32 = dict(dtype=torch.int32, device=dev)
+    own_row = torch.arange(rows, device=dev)
+    root = torch.repeat_interleave(starts[:-1], n)
+    parents = parents.to(dev)
+    above = torch.where(parents < 0, own_row, root + parents)
+    target = torch.empty((rows, V), dtype=dt, device=dev)
+    draft = torch.empty((rows, V), dtype=dt, device=dev) if case["how"] == "draft" else None
+    tokens = torch.zeros(rows, dtype=torch.int64, device=dev)
+    step = max(1, (1 << 26) // V)
+    best = torch.zeros((rows, 4), dtype=torch.int64, device=dev)
+    for a in range(0, rows, step):
+        b = min(rows, a + step)
+        # language models' distributions: a few likely tokens and a long tail, the draft's near the target's
+        x = torch.randn((b - a, V), generator=g, device=dev) * 3.5
+        y = x + torch.randn((b - a, V), generator=g, device=dev) * 0.7
+        target[a:b] = x.to(dt) if case["how"] == "greedy" else torch.softmax(x, -1).to(dt)
+        y = torch.softmax(y, -1).to(dt)
+        if draft is not None:
+            draft[a:b] = y
+        best[a:b] = torch.multinomial(y.float(), 4, generator=g) if draft is not None else y.float().topk(4, -1).indices
+    # children of a row in turn take what was drawn, or its most likely tokens
+    turn = torch.zeros(rows, dtype=torch.int64)
+    seen = {}
+    for r, p in enumerate(above.tolist()):
+        turn[r] = seen.get(p, 0) % 4
+        seen[p] = seen.get(p, 0) + 1
+    tokens = best[above, turn.to(dev)]
+    if draft is not None:  # independent draws: the same token may be drawn twice
+        tokens = best[above, torch.randint(0, 4, (rows,), generator=g, device=dev)]
+    st.update(parents=parents.to(**i32), tokens=tokens.to(**i32), target=target, draft=draft,
+              uniform=None if case["how"] == "greedy" else torch.rand((rows, 2), generator=g, device=dev),
+              seq_lens=(500 + n).to(**i32), seq_lens_out=torch.zeros(case["batch"], **i32),
+              keep=torch.zeros(rows, **i32), kept=torch.zeros(case["batch"], **i32), next=torch.zeros(case["batch"], **i32))
+    host = parents.cpu()
+    first = st["starts"].cpu()
+    # what the walk is bounded by: the deepest row, the most children of one
+    depth = int(_depths(host, first, n.cpu()).max())
+    up = above.cpu()[host >= 0]
+    st.update(depth=depth, kids=int(torch.bincount(up, minlength=1).max()) if len(up) else 0)
+    return st
+
+
+# ------------------------------------------------------------------------------------------------ plain forms
+def _plain_tree(st):
+    parents, starts, n = st["parents"].long(), st["starts"], st["n"]
+    rows, dev = st["rows"], st["parents"].device
+    i = torch.arange(rows, device=dev)
+    seq = torch.searchsorted(starts[1:].contiguous(), i, right=True)
+    root = starts[seq]
+    up = torch.where(parents < 0, i, root + parents)
+    top = parents < 0
+    sees = torch.zeros((rows, st["mask"].shape[1] * 32), dtype=torch.bool, device=dev)
+    sees[i, i - root] = True
+    depth = (~top).long()
+    for _ in range(max(1, (st["top"] - 1).bit_length())):  # ancestors 1, 2, 4, .. further up
+        sees = sees | sees[up]
+        depth = depth + depth[up]
+        up = up[up]
+    w = (sees.view(rows, -1, 32).int() << torch.arange(32, device=dev, dtype=torch.int32)).sum(-1, dtype=torch.int64)
+    st["mask"].copy_(w.to(torch.int32))
+    st["positions"].copy_((st["seq_lens"].long() - n)[seq] + depth)
+    return dict(mask=st["mask"], positions=st["positions"])
+
+
+def _plain_rope(st):
+    cs = st["cos_sin"][st["positions"].long()]
+    c, s = cs[:, None, :64], cs[:, None, 64:]
+    out = {}
+    for name in ("q", "k"):
+        x, w = st[name].float(), st[name + "_weight"]
+        if w is not None:
+            x = x * torch.rsqrt((x * x).mean(-1, keepdim=True) + 1e-6) * w
+        a, b = x[..., :64], x[..., 64:]
+        st[name + "_out"].copy_(torch.cat([a * c - b * s, b * c + a * s], -1))
+        out[name] = st[name + "_out"]
+    return out
+
+
+def _unpack_k(b):
+    """[..., 2048] key tiles -> [..., 16 tokens, 128 channels]."""
+    s = b.shape[:-1]
+    n = len(s)
+    return b.view(*s, 2, 2, 8, 4, 16).permute(*range(n), n, n + 2, n + 1, n + 3, n + 4).reshape(*s, PAGE, D)
+
+
+def _pack_k(x):
+    s = x.shape[:-2]
+    n = len(s)
+    return x.reshape(*s, 2, 8, 2, 4, 16).permute(*range(n), n, n + 2, n + 1, n + 3, n + 4).reshape(*s, PAGE * D)
+
+
+_V = (4, 2, 6, 0, 3, 5, 1)  # the tile's axes (c>>5, c&7, (t>>1)&3, (c>>4)&1, t>>3, (c>>3)&1, t&1) in token, channel order
+
+
+def _unpack_v(b):
+    s = b.shape[:-1]
+    n = len(s)
+    return b.view(*s, 4, 8, 4, 2, 2, 2, 2).permute(*range(n), *(n + i for i in _V)).reshape(*s, PAGE, D)
+
+
+def _pack_v(x):
+    s = x.shape[:-2]
+    n = len(s)
+    back = sorted(range(7), key=lambda i: _V[i])
+    return x.reshape(*s, 2, 4, 2, 4, 2, 2, 8).permute(*range(n), *(n + i for i in back)).reshape(*s, PAGE * D)
+
+
+def _values(b, fmt):
+    return b.float() - 128.0 if fmt == "int8p" else b.view(torch.float8_e4m3fn).float()
+
+
+def _encode(x, fmt):
+    if fmt == "int8p":
+        return (x.round().clamp(-127, 127) + 128.0).to(torch.uint8)
+    return x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _plain_attn(st):
+    case, fmt = st["case"], st["case"]["fmt"]
+    B, H, Hq = case["batch"], case["kv_heads"], case["q_heads"]
+    G, dev = Hq // H, st["bt"].device
+    starts, lens, n = st["starts"], st["seq_lens"].long(), st["n"]
+    N, width = st["top"], st["bt"].shape[1] - 1
+    L = width * PAGE
+    pages = st["bt"][:, :width].clamp(min=0).long()
+
+    def plane(p, scale, unpack):
+        x = _values(unpack(p.view(-1, H, PAGE * D)[pages]), fmt)
+        x *= scale.t()[pages].float()[..., None, None]
+        return x.permute(0, 2, 1, 3, 4).reshape(B, H, L, D)
+
+    i = torch.arange(N, device=dev)
+    row = (starts[:-1, None] + i).clamp(max=st["rows"] - 1)
+    q = st["q"][row].float().view(B, N, H, G, D).permute(0, 2, 3, 1, 4).reshape(B, H, G * N, D)
+    x = torch.matmul(q, plane(st["k"], st["k_scale"][0], _unpack_k).transpose(-1, -2)).view(B, H, G, N, L)
+    x *= 1.0 / math.sqrt(D)
+    # a token of the run is seen by its bit, one before it by all
+    t = torch.arange(L, device=dev) - (lens - n)[:, None]
+    bits = st["mask"][row].long()
+    inside = (torch.gather(bits, 2, (t.clamp(0, 32 * bits.shape[-1] - 1) // 32)[:, None].expand(B, N, L)) >> (t.clamp(min=0) % 32)[:, None]) & 1
+    seen = torch.where((t < 0)[:, None], True, (inside != 0) & (t < n[:, None])[:, None])
+    x.masked_fill_(~seen[:, None, None], float("-inf"))
+    m = x.amax(-1, keepdim=True)
+    x -= m
+    x.exp_()
+    s = x.sum(-1, keepdim=True)
+    o = torch.matmul(x.view(B, H, G * N, L), plane(st["v"], st["v_scale"][0], _unpack_v)).view(B, H, G, N, D) / s
+    lse = (m + s.log())[..., 0]
+    r = torch.arange(st["rows"], device=dev)
+    seq = torch.searchsorted(starts[1:].contiguous(), r, right=True)
+    off = r - starts[seq]
+    st["out"].copy_(o.permute(0, 3, 1, 2, 4)[seq, off].reshape(-1, Hq, D))
+    st["lse"].copy_(lse.permute(0, 3, 1, 2)[seq, off].reshape(-1, Hq))
+    return dict(out=st["out"], lse=st["lse"])
+
+
+def _whole(r):
+    return (r.double() * ONE).long()
+
+
+def _plain_verify(st):
+    dev = st["parents"].device
+    starts, n, N = st["starts"], st["n"], st["top"]
+    B = n.shape[0]
+    i = torch.arange(N, device=dev)
+    there = i < n[:, None]
+    row = (starts[:-1, None] + i).clamp(max=st["rows"] - 1)
+    parent = torch.where(there, st["parents"][row].long(), -2)
+    parent[:, 0] = -2  # the root is nobody's child
+    token = torch.where(there, st["tokens"][row].long(), -1)
+    who = torch.arange(B, device=dev)
+    cur = torch.zeros(B, dtype=torch.int64, device=dev)
+    live = n > 0
+    path = torch.full((B, N), -1, dtype=torch.int64, device=dev)
+    path[:, 0] = torch.where(live, 0, -1)
+    kept = live.long()
+    last = torch.full((B,), -1, dtype=torch.int64, device=dev)
+    target, draft = st["target"], st["draft"]
+    greedy = st["uniform"] is None
+    none = torch.full((B,), N, dtype=torch.int64, device=dev)
+    for _ in range(st["depth"] + 1):
+        at = (starts[:-1] + cur).clamp(max=st["rows"] - 1)
+        mine = parent == cur[:, None]
+        go = none
+        p = target[at].float()
+        if greedy:
+            drawn = p.argmax(-1)
+        else:
+            w = _whole(p)
+            if draft is not None:
+                q = draft[at].float()
+                c = torch.zeros(B, device=dev)
+                z = w.sum(-1)
+                order = torch.where(mine, i, N).sort(-1).values  # children in turn
+                for k in range(st["kids"]):
+                    child = order[:, k]
+                    open_ = (child < N) & (go == N)
+                    j = child.clamp(max=N - 1)
+                    x = token[who, j].clamp(min=0)
+                    u = st["uniform"][(starts[:-1] + j).clamp(max=st["rows"] - 1), 0].double()
+                    px, qx = p[who, x].double(), q[who, x].double()
+                    yes = (u * qx) * (z.double() / ONE) < px - c.double() * qx
+                    go = torch.where(open_ & yes, child, go)
+                    c = torch.where(open_ & ~yes, (c.double() + z.double() / ONE).float(), c)
+                    rest = _whole((p - c[:, None] * q).clamp(min=0))
+                    w = torch.where((c > 0)[:, None], rest, w)
+                    z = w.sum(-1)
+                w = torch.where((z == 0)[:, None], _whole(p), w)
+            cum = w.cumsum(-1)
+            z = cum[:, -1]
+            t = (st["uniform"][at, 1].double() * z.double()).floor().long().clamp(min=0)
+            drawn = (cum <= torch.minimum(t, z - 1)[:, None]).sum(-1)
+        if draft is None:  # the child that holds the drawn token, the first of them
+            go = torch.where(mine & (token == drawn[:, None]), i, N).amin(-1)
+        moves = live & (go < N)
+        last = torch.where(live & ~moves, drawn, last)
+        path[who, kept.clamp(max=N - 1)] = torch.where(moves, go, path[who, kept.clamp(max=N - 1)])
+        kept = kept + moves
+        cur = torch.where(moves, go, cur)
+        live = moves
+    st["keep"].copy_(path[there])
+    st["kept"].copy_(kept)
+    st["next"].copy_(last)
+    st["seq_lens_out"].copy_(st["seq_lens"] - n + kept)
+    return _verify_out(st)
+
+
+def _verify_out(st):
+    return dict(keep=st["keep"], kept=st["kept"], next=st["next"], seq_lens=st["seq_lens_out"])
+
+
+def _plain_keep(st):
+    case, fmt = st["case"], st["case"]["fmt"]
+    H, total, dev = case["kv_heads"], st["total"], st["bt"].device
+    starts, n, kept = st["starts"], st["n"], st["kept"].long()
+    before = st["seq_lens"].long() - kept
+    B, width = st["bt"].shape
+    first = before // PAGE
+    reach = lambda m: (m + 2 * PAGE - 2) // PAGE  # noqa: E731  pages that m tokens can touch
+    src = (first[:, None] + torch.arange(reach(st["top"]), device=dev)).clamp(max=width - 1)
+    src = st["bt"].gather(1, src).clamp(min=0).long()
+    page = first[:, None] + torch.arange(reach(st["kept_top"]), device=dev)
+    phys = st["bt"].gather(1, page.clamp(max=width - 1)).long()
+    pos = page[..., None] * PAGE + torch.arange(PAGE, device=dev)
+    j = pos - before[:, None, None]
+    valid = j < kept[:, None, None]  # what the page holds afterwards
+    idx = st["keep"][(starts[:-1, None, None] + j.clamp(min=0)).clamp(max=st["rows"] - 1)].long()
+    was = torch.where(j < 0, pos, before[:, None, None] + idx).clamp(min=0)  # where its token is
+    moves = (valid & (was != pos)).any(-1)
+    was = (was - first[:, None, None] * PAGE).clamp(0, src.shape[1] * PAGE - 1)
+    who = torch.arange(B, device=dev)[:, None, None]
+    for name, unpack, pack in (("k", _unpack_k, _pack_k), ("v", _unpack_v, _pack_v)):
+        tiles = st[name].view(-1, total, H, PAGE * D)
+        L = tiles.shape[0]
+        old = unpack(tiles[:, src]).permute(1, 2, 4, 0, 3, 5).reshape(B, -1, L, H, D)  # [request, token, layer, head, channel]
+        scale = st[name + "_scale"]  # [layer, head, page]
+        exps = torch.log2(scale.float()).round().permute(2, 0, 1)[src]  # [request, page, layer, head]
+        e_tok = exps[who, was // PAGE]  # [request, page, 16, layer, head]
+        ok = valid[..., None, None]
+        e1 = torch.where(ok, e_tok, float(E_MIN)).amax(2)
+        x = _values(old, fmt)[who, was] * torch.exp2(e_tok - e1[:, :, None])[..., None]
+        x = torch.where(ok[..., None], x, 0.0).permute(0, 1, 3, 4, 2, 5)  # [request, page, layer, head, 16, channel]
+        done = phys[moves]
+        tiles[:, done] = pack(_encode(x[moves], fmt)).transpose(0, 1)
+        scale[:, :, done] = torch.exp2(e1[moves]).to(torch.float16).permute(1, 2, 0)
+    return _keep_out(st)
+
+
+def _keep_out(st):
+    # codes beside their scales, both exact by definition, are compared bit for bit
+    kind = torch.float8_e4m3fn if st["case"]["fmt"] == "e4m3p" else torch.uint8
+    return dict(k=st["k"].view(kind), v=st["v"].view(kind), k_scale=st["k_scale"], v_scale=st["v_scale"])
+
+
+# ------------------------------------------------------------------------------------------------ the framework's operators
+def _own(st):
+    import quantized_kv_cache_kvq_gb300 as kvq
+
+    case, starts, err = st["case"], st["run_starts"], st["err"]
+    if st["op"] == "tree":
+        kvq.tree_runs(st["parents"], st["seq_lens"], st["mask"], positions=st["positions"], run_starts=starts, err=err)
+        return dict(mask=st["mask"], positions=st["positions"])
+    if st["op"] == "rope":
+        kvq.rope_runs(st["q"], st["k"], st["positions"], st["cos_sin"], q_weight=st["q_weight"], k_weight=st["k_weight"],
+                      q_out=st["q_out"], k_out=st["k_out"], run_starts=starts, err=err)
+        return dict(q=st["q_out"], k=st["k_out"])
+    if st["op"] == "verify":
+        kvq.verify_runs(st["target"], st["tokens"], st["parents"], st["uniform"], st["keep"], st["kept"], st["next"], draft=st["draft"],
+                        seq_lens=st["seq_lens"], seq_lens_out=st["seq_lens_out"], run_starts=starts, err=err)
+        return _verify_out(st)
+    if "caches" not in st:
+        st["caches"] = [kvq.PagedCache.over(case["fmt"], case["fmt"], case["kv_heads"], st["total"], k=k, v=v, k_scale=ks, v_scale=vs, layer=i)
+                        for i, (k, v, ks, vs) in enumerate(zip(st["k"], st["v"], st["k_scale"], st["v_scale"]))]
+    if st["op"] == "keep":
+        kvq.keep_runs(st["caches"], st["seq_lens"], st["bt"], st["keep"], st["kept"], run_starts=starts, err=err)
+        return _keep_out(st)
+    if "workspace" not in st:
+        size = kvq.attn_tree_workspace_size(case["batch"], st["rows"], st["top"], case["kv_heads"], case["q_heads"], st["q"].dtype)
+        st["workspace"] = torch.empty(size, dtype=torch.uint8, device=st["q"].device)
+    kvq.attn_tree(st["caches"][0], st["q"], st["seq_lens"], st["bt"], st["mask"], st["out"], st["workspace"], run_starts=starts,
+                  max_run=st["top"], lse=st["lse"], err=err)
+    return dict(out=st["out"], lse=st["lse"])
+
+
+def run(state):
+    if own:
+        return _own(state)
+    if state["op"] == "tree":
+        return _plain_tree(state)
+    if state["op"] == "rope":
+        return _plain_rope(state)
+    if state["op"] == "attn":
+        return _plain_attn(state)
+    if state["op"] == "verify":
+        return _plain_verify(state)
+    return _plain_keep(state)
+
+
+# ------------------------------------------------------------------------------------------------ work
+def work(case):
+    n, before = _shape(case)
+    B, rows = case["batch"], int(n.sum())
+    if case["op"] == "tree":
+        return {"bytes": 4 * rows * (2 + (int(n.max()) + 31) // 32) + 8 * B, "flops": 0}
+    if case["op"] == "rope":
+        size = 2 if case["dtype"] == "bf16" else 4
+        heads = case["q_heads"] + case["kv_heads"]
+        return {"bytes": rows * (2 * heads * D * size + 4 + 4 * D), "flops": rows * heads * D * (8 if case["norm"] else 3)}
+    if case["op"] == "verify":
+        # the rows of the accepted path, which goes by the data: with these inputs 2.8 rows on average with drafts, else 1.4
+        size = 2 if case["dtype"] == "bf16" else 4
+        read = B * min(2.8, rows / B) * 2 if case["how"] == "draft" else B * min(1.4, rows / B)
+        return {"bytes": read * case["vocab"] * size + 12 * rows + 16 * B, "flops": read * case["vocab"]}
+    if case["op"] == "keep":
+        # a path of about four tokens, read and written once in each plane
+        moved = int(n.clamp(max=4).sum())
+        return {"bytes": 4 * moved * case["layers"] * case["kv_heads"] * D, "flops": 0}
+    size = 2 if case["dtype"] == "bf16" else 4
+    H, Hq = case["kv_heads"], case["q_heads"]
+    after = before + n
+    seen = float((n * before).sum()) + rows * 2.0  # (row, key) pairs
+    keys = int(after.sum())
+    return {"bytes": 2 * keys * H * D + 4 * H * keys / PAGE + rows * Hq * (2 * D * size + 4), "flops": 4.0 * D * Hq * seen}
+
+
+# ------------------------------------------------------------------------------------------------ in 64 bits
+def _tile_order():
+    """Byte of (token, channel) in a key tile and in a value tile."""
+    t, c = torch.arange(PAGE)[:, None], torch.arange(D)[None, :]
+    k = 16 * (((t >> 3) * 2 + (c >> 6)) * 32 + (t & 7) * 4 + ((c >> 4) & 3)) + (c & 15)
+    v = 16 * (32 * (c >> 5) + 4 * (c & 7) + ((t & 7) >> 1)) + 8 * ((c >> 4) & 1) + 2 * (2 * (t >> 3) + ((c >> 3) & 1)) + (t & 1)
+    return k.reshape(-1), v.reshape(-1)
+
+
+def _float_of_e4m3(b):
+    b = b.to(torch.int64)
+    e, m = (b >> 3) & 15, (b & 7).double()
+    x = torch.where(e == 0, m * 2.0 ** -9, (8 + m) * torch.exp2((e - 10).double()))
+    return torch.where(b >= 128, -x, x)
+
+
+def exact(case, seed):
+    if case["op"] in ("tree", "verify"):
+        return None  # whole numbers
+    st = prepare(case, seed)
+    dev = st["run_starts"].device
+    if case["op"] == "rope":
+        out = {}
+        at = st["positions"].long()
+        cos, sin = st["cos_sin"].double()[at, :64], st["cos_sin"].double()[at, 64:]
+        turn = torch.complex(cos, sin)[:, None, :]
+        for name in ("q", "k"):
+            x = st[name].double()
+            if st[name + "_weight"] is not None:
+                x = x / (x.square().sum(-1, keepdim=True) / D + 1e-6).sqrt() * st[name + "_weight"].double()
+            z = torch.complex(x[..., :64].contiguous(), x[..., 64:].contiguous()) * turn
+            out[name] = torch.cat([z.real, z.imag], -1)
+        return out
+    fmt, H = case["fmt"], case["kv_heads"]
+    ko, vo = (o.to(dev) for o in _tile_order())
+    value = (lambda b: b.double() - 128) if fmt == "int8p" else _float_of_e4m3
+    starts, lens, bt = st["run_starts"].tolist(), st["seq_lens"].tolist(), st["bt"].tolist()
+    if case["op"] == "keep":
+        grid = _float_of_e4m3(torch.arange(127, device=dev)) if fmt == "e4m3p" else torch.arange(128, device=dev, dtype=torch.float64)
+
+        def nearest(x):  # the nearest value of the grid, ties to the even code
+            a = x.abs().clamp(max=float(grid[-1])).contiguous()
+            hi = torch.searchsorted(grid, a).clamp(max=len(grid) - 1)
+            lo = (hi - 1).clamp(min=0)
+            up, down = grid[hi] - a, a - grid[lo]
+            pick = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+            return torch.copysign(grid[pick], x)
+
+        L, total, kept, lists = case["layers"], st["total"], st["kept"].tolist(), st["keep"].tolist()
+        outs = {}
+        for name, order in (("k", ko), ("v", vo)):
+            back = torch.argsort(order)
+            codes = value(st[name].view(L, total, H, PAGE * D))
+            scale = st[name + "_scale"]  # [layer, head, page]
+            for s in range(case["batch"]):
+                first = lens[s] - kept[s]
+                path = lists[starts[s]:starts[s] + kept[s]]
+                at = lambda pos: (bt[s][pos // PAGE], pos % PAGE)  # noqa: E731
+                new = []
+                for page in range(first // PAGE, _pages(lens[s])):
+                    home = [p if p < first else first + path[p - first] for p in range(page * PAGE, min(lens[s], page * PAGE + PAGE))]
+                    if all(p == page * PAGE + t for t, p in enumerate(home)):
+                        continue
+                    where = [at(p) for p in home]
+                    e = torch.stack([torch.log2(scale[:, :, p].double()).round() for p, _ in where], -1)  # [layer, head, token]
+                    top = e.amax(-1)
+                    x = torch.stack([codes[:, p][..., order[t * D:(t + 1) * D]] for p, t in where], -2)
+                    full = torch.zeros((L, H, PAGE, D), dtype=torch.float64, device=dev)
+                    full[:, :, :len(home)] = nearest(x * torch.exp2(e - top[..., None])[..., None])
+                    new.append((bt[s][page], full, top))
+                for phys, full, top in new:
+                    codes[:, phys] = full.view(L, H, -1)[..., back]
+                    scale[:, :, phys] = torch.exp2(top).to(torch.float16)
+            outs[name] = codes.view(st[name].shape) if fmt == "e4m3p" else None  # INT8 comes back as its bytes
+            outs[name + "_scale"] = scale.double()
+        return outs
+    Hq = case["q_heads"]
+    G = Hq // H
+    if 4.0 * D * Hq * sum((starts[s + 1] - starts[s]) * lens[s] for s in range(case["batch"])) > 2e12:
+        return None
+    out = torch.zeros((st["rows"], Hq, D), dtype=torch.float64, device=dev)
+    lse = torch.zeros((st["rows"], Hq), dtype=torch.float64, device=dev)
+    for s in range(case["batch"]):
+        a, b, end = starts[s], starts[s + 1], lens[s]
+        pages = st["bt"][s, :_pages(end)].long()
+        words = st["mask"][a:b].long()
+        j = torch.arange(b - a, device=dev)
+        tree = ((words[:, j // 32] >> (j % 32)) & 1) == 1
+        seen = torch.cat([torch.ones((b - a, end - (b - a)), dtype=torch.bool, device=dev), tree], 1)
+        for h in range(H):
+            k, v = ((value(st[p].view(-1, H, PAGE * D)[pages, h][:, o]) * st[p + "_scale"][0, h, pages].double()[:, None])
+                    .view(-1, D)[:end] for p, o in (("k", ko), ("v", vo)))
+            q = st["q"][a:b, h * G:(h + 1) * G].double()
+            x = torch.einsum("igd,td->igt", q, k) / math.sqrt(D)
+            x = torch.where(seen[:, None, :], x, -math.inf)
+            z = torch.logsumexp(x, -1)
+            out[a:b, h * G:(h + 1) * G] = torch.einsum("igt,td->igd", torch.exp(x - z[..., None]), v)
+            lse[a:b, h * G:(h + 1) * G] = z
+    return dict(out=out, lse=lse)
