@@ -46,6 +46,8 @@ extern "C" {
 #define KVQ_MAX_BATCH 1024
 /* Longest context (tokens) of the runs' calls: kvq_map_runs, kvq_append_runs, kvq_attn_runs. */
 #define KVQ_MAX_CONTEXT (1 << 30)
+/* Most tokens of a run that is a tree: kvq_tree_runs, kvq_attn_tree, kvq_verify_runs, kvq_keep_runs. */
+#define KVQ_MAX_TREE 1024
 #define KVQ_VERSION 1
 
 /* A cudaStream_t, declared without the CUDA headers. */
@@ -538,6 +540,120 @@ kvq_status kvq_attn_runs(const kvq_cache* cache, const void* q_dev, int64_t q_ro
                          int32_t max_run, const int32_t* block_table_dev, int32_t max_pages_per_seq,
                          const int32_t* seq_lens_dev, float sm_scale, void* out_dev, float* lse_dev, void* workspace_dev,
                          size_t ws_bytes, int32_t* err_word_dev, kvq_stream_t stream);
+
+/*
+ * Trees.  The run of a request may be a tree of drafted tokens: row 0 is the token chosen last, every other row is drafted below its
+ * parent, an earlier row of the run.  One speculative step is
+ *   kvq_map_runs -> kvq_tree_runs -> kvq_rope_runs -> kvq_append_runs -> kvq_attn_tree (each layer) -> kvq_verify_runs -> kvq_keep_runs
+ * where tokens are cached in the order of the run's rows, whatever their positions, until kvq_keep_runs moves the accepted path to the
+ * front.  A run has at most KVQ_MAX_TREE tokens; a longer one is reported as KVQ_ERR_DEVICE_BOUNDS and skipped.  Rows behind the last run
+ * are left as they are.
+ */
+
+/*
+ * kvq_tree_runs -- what the rows of a tree see, and where they are.
+ *
+ * parents_dev: [num_rows] int32; row i of a run is below row parents[i] of it, 0 <= parents[i] < i, or begins a path (-1).
+ * seq_lens_dev: lengths that count the runs' tokens already (as kvq_map_runs leaves them).
+ * mask_dev: [num_rows][mask_words] int32, written: bit j & 31 of word j >> 5 of row i is set for j = i and for the ancestors j of i.
+ *   32 mask_words must not be less than any run's tokens (a longer run is reported and skipped).
+ * positions_dev (nullable): [num_rows] int32, written: seq_len - n + depth, the depth of a row that begins a path being 0.
+ * Device errors: KVQ_ERR_DEVICE_BOUNDS (a run that cannot be or is longer than its context: skipped; a parent outside -1 .. i - 1: taken as -1).
+ */
+kvq_status kvq_tree_runs(const int32_t* parents_dev, const int32_t* run_starts_dev, int32_t batch, int32_t num_rows,
+                         const int32_t* seq_lens_dev, int32_t* mask_dev, int32_t mask_words, int32_t* positions_dev,
+                         int32_t* err_word_dev, kvq_stream_t stream);
+
+/*
+ * kvq_rope_runs -- queries and keys of a step normed per head and rotated to their positions, in one pass.
+ *
+ * q_dev, k_dev: [num_rows] rows of [num_q_heads][128] and [num_kv_heads][128] elements of type dtype, 16-byte aligned, rows
+ *   q_row_stride / k_row_stride elements apart (a multiple of 16 bytes), so that slices of a fused projection are taken as they are.  Either
+ *   of the two may be absent (NULL, and no heads).
+ * q_weight_dev, k_weight_dev (each nullable: no norm): [128] fp32, 16-byte aligned; x becomes x rsqrt(mean x^2 + eps) weight.
+ * positions_dev: [num_rows] int32; cos_sin_dev, max_position: the table of kvq_append_rope.  Half-split pairs (channel j with j + 64):
+ *   x' = x c - y s, y' = y c + x s.  All in binary32, rounded once to the outputs' type.
+ * q_out_dev, k_out_dev: outputs of the same type, rows q_out_row_stride / k_out_row_stride apart; an output may be its input (same address
+ *   and stride), apart from that nothing may overlap.
+ * run_starts_dev, batch: rows behind run_starts[batch] are left as they are; NULL: all rows are taken.
+ * Device errors: KVQ_ERR_DEVICE_BOUNDS (a position outside [0, max_position): the row is left as it is; run_starts[batch] outside
+ *   [0, num_rows]: no row is taken).
+ */
+kvq_status kvq_rope_runs(const void* q_dev, int64_t q_row_stride, int32_t num_q_heads, const void* k_dev, int64_t k_row_stride,
+                         int32_t num_kv_heads, int32_t dtype, const float* q_weight_dev, const float* k_weight_dev, float eps,
+                         const int32_t* positions_dev, const float* cos_sin_dev, int32_t max_position, void* q_out_dev,
+                         int64_t q_out_row_stride, void* k_out_dev, int64_t k_out_row_stride, const int32_t* run_starts_dev,
+                         int32_t batch, int32_t num_rows, int32_t* err_word_dev, kvq_stream_t stream);
+
+/* Workspace bytes kvq_attn_tree needs on the current device; max_run is the call's. */
+size_t kvq_attn_tree_workspace_size(int32_t batch, int32_t num_rows, int32_t max_run, int32_t num_kv_heads, int32_t num_q_heads,
+                                    int32_t q_dtype);
+
+/*
+ * kvq_attn_tree -- kvq_attn_runs where a mask says what a row sees of its own run: every row attends to all tokens before the run
+ * and to token j of the run where bit j & 31 of word j >> 5 of its mask is set (its own bit too, or it does not see itself).
+ *
+ * mask_dev: [num_rows][mask_words] int32, 32 mask_words >= max_run; bits behind the run's tokens are not looked at.  Any mask will do, not
+ *   only a tree's.  A row that sees nothing (no token before the run, no bit) gives 0 and -inf.
+ * max_run: as for kvq_attn_runs, at most KVQ_MAX_TREE.
+ * Everything else (rounding, errors, workspace, rows behind the last run) is that of kvq_attn_runs.
+ */
+kvq_status kvq_attn_tree(const kvq_cache* cache, const void* q_dev, int64_t q_row_stride, int32_t q_dtype, int32_t num_q_heads,
+                         const int32_t* run_starts_dev, int32_t batch, int32_t num_rows, int32_t max_run,
+                         const int32_t* block_table_dev, int32_t max_pages_per_seq, const int32_t* seq_lens_dev,
+                         const int32_t* mask_dev, int32_t mask_words, float sm_scale, void* out_dev, float* lse_dev,
+                         void* workspace_dev, size_t ws_bytes, int32_t* err_word_dev, kvq_stream_t stream);
+
+/*
+ * kvq_verify_runs -- which path of every tree the target accepts, and the token after it.
+ *
+ * Row i of target stands for the token after row i.  From row 0 (kept always) the walk goes on to at most one child of the row it
+ * is at; where it goes to none, it ends with a token of its own.  At a row with probabilities p:
+ *   greedy (uniform_dev == NULL): target may hold any scores; the token is the largest one's (the lowest index of equal ones; a NaN counts
+ *     as -inf and is reported), and the walk goes to the first child that holds it.
+ *   no draft probabilities: the token is drawn from p with uniform[i][1]; the walk goes to the first child that holds it.
+ *   draft probabilities q (row i of draft_dev; children are independent draws from it, the same token may be drawn twice): the
+ *     children are tried in order.  With c = 0 and Z = sum p at first, child x (its own uniform[x][0] = u) is accepted where
+ *     u q(x) Z < p(x) - c q(x); else c becomes c + Z and Z = sum max(p - c q, 0): the k-th residual distribution of recursive rejection
+ *     sampling is max(p - c q, 0) / Z.  With no child left the token is drawn from that, with uniform[i][1] (from p where Z = 0).
+ *   Drawing: with W(t) = floor(2^44 w(t)), the lowest token whose sum W(0) + .. + W(t) exceeds floor(u sum W).  Z is 2^-44 sum W too.  Sums
+ *     of whole numbers have no order, so the same inputs give the same tokens whatever the batch; products with Z and u are binary64, c is
+ *     rounded to binary32, p - c q in a sum is binary32 (product and difference rounded).
+ * target_dev, draft_dev (nullable): [num_rows] rows of vocab elements of type dtype (F32 or BF16), target_row_stride / draft_row_stride
+ *   elements apart (>= vocab), any alignment of the type.  Probabilities lie in [0, 1] and need not sum to 1.  vocab <= 2^19.
+ * tokens_dev, parents_dev: [num_rows] int32 (tokens of row 0 are not looked at); uniform_dev (nullable): [num_rows][2] fp32 in [0, 1).
+ * keep_dev: [num_rows] int32, written: the path's rows (indices in the run, rising, the first of them 0), -1 behind them; kept_lens_dev:
+ *   [batch] int32, their number (0 for an empty run); next_tokens_dev: [batch] int32, the token after the path (-1 for an empty run).
+ * seq_lens_dev, seq_lens_out_dev (both nullable, together; may be the same): lengths that count the run's tokens, and lengths that count
+ *   the kept ones.
+ * Device errors: KVQ_ERR_DEVICE_BOUNDS (a run that cannot be, or longer than its context: nothing is kept, its rows of keep are left, its
+ *   length is copied; a drafted token outside the vocabulary: not accepted; a parent outside -1 .. i - 1: not reached),
+ *   KVQ_ERR_NONFINITE_INPUT (a NaN or an infinity that the walk read, a NaN of scores: a probability of 0),
+ *   KVQ_ERR_RANGE (a probability outside [0, 1]: taken as 0; a row that sums to 0: token -1; a random number outside [0, 1)).
+ */
+kvq_status kvq_verify_runs(const void* target_dev, int64_t target_row_stride, const void* draft_dev, int64_t draft_row_stride,
+                           int32_t dtype, int32_t vocab, const int32_t* tokens_dev, const int32_t* parents_dev,
+                           const float* uniform_dev, const int32_t* run_starts_dev, int32_t batch, int32_t num_rows,
+                           int32_t* keep_dev, int32_t* kept_lens_dev, int32_t* next_tokens_dev, const int32_t* seq_lens_dev,
+                           int32_t* seq_lens_out_dev, int32_t* err_word_dev, kvq_stream_t stream);
+
+/*
+ * kvq_keep_runs -- after a verification, the kept tokens' keys and values moved to the front of their run, in the caches of all layers.
+ *
+ * caches: [n_caches] descriptors (host memory) of page-scaled caches, all of the same format, heads and pages, that share the block table
+ *   (one for each layer); no two share memory.
+ * run_starts_dev, num_rows: the step's runs; keep_dev, kept_lens_dev: as kvq_verify_runs leaves them; seq_lens_dev: lengths that count the
+ *   kept tokens already, so that run s began at position seq_lens[s] - kept_lens[s], and token keep[run_starts[s] + j] of the run goes to
+ *   the j-th position from there.
+ * A page into which a token moves is written whole: its scale is the largest of those that its tokens had, codes under smaller ones
+ *   become rne(code 2^-d) (as kvq_append_runs rescales them), slots behind the last kept token get code 0.  Other pages are left as they are;
+ *   those behind the new length belong to their request still (held_pages of kvq_map_runs_ex).
+ * Device errors: KVQ_ERR_DEVICE_BOUNDS (a run that cannot be, a list that does not rise or names a row outside its run, a page outside the
+ *   cache: the request's cache is left as it is).
+ */
+kvq_status kvq_keep_runs(const kvq_cache* caches, int32_t n_caches, const int32_t* run_starts_dev, int32_t batch, int32_t num_rows,
+                         const int32_t* block_table_dev, int32_t max_pages_per_seq, const int32_t* seq_lens_dev,
+                         const int32_t* keep_dev, const int32_t* kept_lens_dev, int32_t* err_word_dev, kvq_stream_t stream);
 
 /* Test hook: the dither xi of (seed, layer, kv_head, slots[i], channel c) into xi_dev[i * 128 + c]. */
 kvq_status kvq_debug_dither(uint64_t seed, int32_t layer, int32_t kv_head, const int32_t* slots_dev, int32_t n,

@@ -30,6 +30,8 @@ bytes      byte account per layout and per workload (test_oracle_meter_bytes, te
 rope       binary32 RoPE-on-append and its cos/sin table (test_oracle_rope)
 runs       page maps, quantized append and causal attention of runs over a page-scaled cache
            (test_oracle_runs)
+trees      masks of trees of drafted tokens, norms and rotation, attention under masks, verification
+           and the kept path (test_oracle_trees)
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test in
 ``tests/test_oracle_*.py``; the Philox generator is additionally pinned word for

@@ -9,8 +9,9 @@ needs the built ``libkvq.so`` and a CUDA device, and raises otherwise.
 Entry points mirror the C names: ``append``, ``decode_attn``, ``meter``,
 ``decode_workspace_size``, ``debug_dither``, ``debug_encode``, those of the
 runs (``map_runs``, ``append_runs``, ``attn_runs`` and
-``attn_runs_workspace_size``), plus the ``PagedCache`` helper that owns one
-layer's planes.
+``attn_runs_workspace_size``) and of trees of drafted tokens (``tree_runs``,
+``rope_runs``, ``attn_tree``, ``attn_tree_workspace_size``, ``verify_runs``,
+``keep_runs``), plus the ``PagedCache`` helper that owns one layer's planes.
 """
 from __future__ import annotations
 
@@ -44,6 +45,12 @@ __all__ = [
     "append_runs",
     "attn_runs",
     "attn_runs_workspace_size",
+    "tree_runs",
+    "rope_runs",
+    "attn_tree",
+    "attn_tree_workspace_size",
+    "verify_runs",
+    "keep_runs",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -56,6 +63,7 @@ DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 TIER_A, TIER_B, TIER_V, TIER_S = 1, 2, 4, 8
 METER_STATE_FLOATS = 8  # floats per (sequence, query head) cell of meter_state
 HEAD_DIM, PAGE, N_BANDS = 128, 16, 16
+MAX_TREE = 1024  # tokens of a run that is a tree
 _SM_SCALE = 1.0 / math.sqrt(HEAD_DIM)
 _INT32 = torch.int32
 
@@ -181,6 +189,24 @@ def load(path: str = LIB_PATH):
     L.kvq_attn_runs.argtypes = [POINTER(_Cache), c_void_p, c_int64, c_int32, c_int32, c_void_p, c_int32, c_int32, c_int32,
                                 c_void_p, c_int32, c_void_p, c_float, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
                                 c_void_p]
+    L.kvq_tree_runs.restype = c_int32
+    L.kvq_tree_runs.argtypes = [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p]
+    L.kvq_rope_runs.restype = c_int32
+    L.kvq_rope_runs.argtypes = [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p, c_float,
+                                c_void_p, c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32, c_int32,
+                                c_void_p, c_void_p]
+    L.kvq_attn_tree_workspace_size.restype = c_size_t
+    L.kvq_attn_tree_workspace_size.argtypes = [c_int32] * 6
+    L.kvq_attn_tree.restype = c_int32
+    L.kvq_attn_tree.argtypes = [POINTER(_Cache), c_void_p, c_int64, c_int32, c_int32, c_void_p, c_int32, c_int32, c_int32,
+                                c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_float, c_void_p, c_void_p, c_void_p, c_size_t,
+                                c_void_p, c_void_p]
+    L.kvq_verify_runs.restype = c_int32
+    L.kvq_verify_runs.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]
+    L.kvq_keep_runs.restype = c_int32
+    L.kvq_keep_runs.argtypes = [POINTER(_Cache), c_int32, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
+                                c_void_p, c_void_p, c_void_p]
     L.kvq_sizeof.restype = c_size_t
     L.kvq_sizeof.argtypes = [c_int32]
     L.kvq_debug_dither.restype = c_int32
@@ -582,6 +608,145 @@ def attn_runs(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_
             DTYPE[q.dtype], Hq, _ptr(run_starts), B, rows, max_run, block_table.data_ptr(), width, seq_lens.data_ptr(),
             _SM_SCALE if sm_scale is None else sm_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
             _ptr(err))
+
+
+def _tree(batch: int, rows: int, run_starts, *per_row):
+    assert run_starts is None and rows == batch or run_starts is not None and run_starts.numel() == batch + 1
+    for t in per_row:
+        assert t is None or t.numel() == rows, "one for each row"
+
+
+def tree_runs(parents: torch.Tensor, seq_lens: torch.Tensor, mask: torch.Tensor, *, positions: torch.Tensor | None = None,
+              run_starts: torch.Tensor | None = None, err: torch.Tensor | None = None, stream=None):
+    """kvq_tree_runs: parents [rows] (of a run's row i: an earlier row of the run, or -1) -> mask [rows, words], bit j of row i for
+    j = i and i's ancestors, and positions [rows].  seq_lens [B] count the runs' tokens; words: for 32 tokens of a run each.  All int32
+    and contiguous.  run_starts None: one token for each request."""
+    device = parents.get_device()
+    _i32(device, parents, seq_lens, mask, positions, run_starts, err)
+    rows, words = mask.shape
+    _tree(seq_lens.numel(), rows, run_starts, parents, positions)
+    _launch("kvq_tree_runs", lib().kvq_tree_runs, device, stream, parents.data_ptr(), _ptr(run_starts), seq_lens.numel(), rows,
+            seq_lens.data_ptr(), mask.data_ptr(), words, _ptr(positions), _ptr(err))
+
+
+def _dense_rows(x: torch.Tensor, heads_of: str) -> int:
+    """Row stride of [rows, heads, 128] whose rows are dense."""
+    assert x.dim() == 3 and x.shape[2] == HEAD_DIM, f"{heads_of}: [rows, heads, 128]"
+    return _rows(x, x.shape[0], x.shape[1])
+
+
+def _f32(device: int, n: int, t):
+    assert t is None or (t.dtype is torch.float32 and t.is_contiguous() and t.numel() == n and t.get_device() == device), \
+        f"{n} fp32, contiguous and on one CUDA device"
+
+
+def rope_runs(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor, cos_sin: torch.Tensor, *,
+              q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, run_starts: torch.Tensor | None = None,
+              err: torch.Tensor | None = None, stream=None):
+    """kvq_rope_runs: q [rows, Hq, 128] and k [rows, Hkv, 128] (fp32 or bf16; rows may be strided; either may be None) normed per head
+    where q_weight / k_weight [128] (fp32) are given, and rotated to positions [rows] with the table ``cos_sin`` of append_rope.  In place
+    unless q_out / k_out are given.  run_starts [B + 1]: rows behind the last run are left as they are."""
+    one = q if q is not None else k
+    device, rows = one.get_device(), one.shape[0]
+    assert q is None or k is None or (q.dtype == k.dtype and k.shape[0] == rows)
+    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    args = []
+    for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            assert y is None
+            args.append((None, 0, 0, None, 0))
+            continue
+        assert y.shape == x.shape and y.dtype == x.dtype
+        _on(device, x, y)
+        args.append((x.data_ptr(), _dense_rows(x, what), x.shape[1], y.data_ptr(), _dense_rows(y, what)))
+    (qp, qs, hq, qo, qos), (kp, ks, hk, ko, kos) = args
+    _i32(device, positions, run_starts, err)
+    assert positions.numel() == rows and cos_sin.dim() == 2 and cos_sin.shape[1] == HEAD_DIM
+    _f32(device, cos_sin.numel(), cos_sin)
+    _f32(device, HEAD_DIM, q_weight)
+    _f32(device, HEAD_DIM, k_weight)
+    _launch("kvq_rope_runs", lib().kvq_rope_runs, device, stream, qp, qs, hq, kp, ks, hk, DTYPE[one.dtype], _ptr(q_weight),
+            _ptr(k_weight), eps, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], qo, qos, ko, kos, _ptr(run_starts),
+            0 if run_starts is None else run_starts.numel() - 1, rows, _ptr(err))
+
+
+def attn_tree_workspace_size(batch: int, num_rows: int, max_run: int, num_kv_heads: int, num_q_heads: int, q_dtype: torch.dtype) -> int:
+    return int(lib().kvq_attn_tree_workspace_size(batch, num_rows, max_run, num_kv_heads, num_q_heads, DTYPE[q_dtype]))
+
+
+def attn_tree(cache: PagedCache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, mask: torch.Tensor,
+              out: torch.Tensor, workspace: torch.Tensor, *, run_starts: torch.Tensor | None = None, max_run: int | None = None,
+              lse: torch.Tensor | None = None, sm_scale: float | None = None, err: torch.Tensor | None = None, stream=None):
+    """kvq_attn_tree: attn_runs where a row sees all tokens before its run, and of its run those whose bits its mask [rows, words] has (int32,
+    as tree_runs writes them).  max_run None: one token without run_starts, else as many as the mask has bits for or as there are rows."""
+    rows, Hq, d = q.shape
+    assert d == HEAD_DIM and out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
+    device = q.get_device()
+    assert workspace.is_contiguous(), "workspace: one piece of memory"
+    _on(device, out, workspace, lse)
+    cache._check_device(device)
+    _i32(device, seq_lens, block_table, mask, run_starts, err)
+    B, width = block_table.shape
+    assert seq_lens.numel() == B and (run_starts is None or run_starts.numel() == B + 1) and mask.shape[0] == rows
+    words = mask.shape[1]
+    if max_run is None:
+        max_run = 1 if run_starts is None else min(rows, 32 * words, MAX_TREE)
+    assert lse is None or (lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() == rows * Hq)
+    _launch("kvq_attn_tree", lib().kvq_attn_tree, device, stream, ctypes.byref(cache.desc()), q.data_ptr(), _rows(q, rows, Hq),
+            DTYPE[q.dtype], Hq, _ptr(run_starts), B, rows, max_run, block_table.data_ptr(), width, seq_lens.data_ptr(),
+            mask.data_ptr(), words, _SM_SCALE if sm_scale is None else sm_scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+            workspace.nbytes, _ptr(err))
+
+
+def _vocab_rows(x: torch.Tensor) -> int:
+    rows, vocab = x.shape
+    assert vocab == 1 or x.stride(1) == 1, "a row's elements side by side"
+    return x.stride(0) if rows > 1 else vocab
+
+
+def verify_runs(target: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor, uniform: torch.Tensor | None, keep: torch.Tensor,
+                kept_lens: torch.Tensor, next_tokens: torch.Tensor, *, draft: torch.Tensor | None = None,
+                seq_lens: torch.Tensor | None = None, seq_lens_out: torch.Tensor | None = None,
+                run_starts: torch.Tensor | None = None, err: torch.Tensor | None = None, stream=None):
+    """kvq_verify_runs: the path of every tree that the target accepts -> keep [rows] (the path's rows, -1 behind them), kept_lens [B]
+    and next_tokens [B].
+
+    target [rows, vocab] (fp32 or bf16; rows may be strided): probabilities of the token after each row, or any scores where
+    uniform is None (greedy).  uniform [rows, 2] fp32 in [0, 1): for accepting the row's token, for drawing after it.  draft: probabilities
+    that the rows' children were drawn from independently; None: children are no draws.  tokens, parents [rows] int32.  seq_lens [B] (with
+    the runs' tokens) -> seq_lens_out [B] (with the kept ones), which may be the same tensor."""
+    device = target.get_device()
+    rows, vocab = target.shape
+    assert draft is None or (draft.shape == target.shape and draft.dtype == target.dtype)
+    _on(device, draft)
+    _i32(device, tokens, parents, keep, kept_lens, next_tokens, seq_lens, seq_lens_out, run_starts, err)
+    _f32(device, 2 * rows, uniform)
+    B = kept_lens.numel()
+    _tree(B, rows, run_starts, tokens, parents, keep)
+    for t in (next_tokens, seq_lens, seq_lens_out):
+        assert t is None or t.numel() == B
+    _launch("kvq_verify_runs", lib().kvq_verify_runs, device, stream, target.data_ptr(), _vocab_rows(target), _ptr(draft),
+            0 if draft is None else _vocab_rows(draft), DTYPE[target.dtype], vocab, tokens.data_ptr(), parents.data_ptr(), _ptr(uniform),
+            _ptr(run_starts), B, rows, keep.data_ptr(), kept_lens.data_ptr(), next_tokens.data_ptr(), _ptr(seq_lens),
+            _ptr(seq_lens_out), _ptr(err))
+
+
+def keep_runs(caches, seq_lens: torch.Tensor, block_table: torch.Tensor, keep: torch.Tensor, kept_lens: torch.Tensor, *,
+              run_starts: torch.Tensor | None = None, err: torch.Tensor | None = None, stream=None):
+    """kvq_keep_runs: after verify_runs, the kept tokens' keys and values to the front of their runs, in ``caches`` (a page-scaled PagedCache, or a
+    list of them, one for each layer, all alike).  seq_lens [B] count the kept tokens already (verify_runs's seq_lens_out)."""
+    caches = [caches] if isinstance(caches, PagedCache) else list(caches)
+    device = seq_lens.get_device()
+    for c in caches:
+        c._check_device(device)
+    _i32(device, seq_lens, block_table, keep, kept_lens, run_starts, err)
+    B, width = block_table.shape
+    assert seq_lens.numel() == B and kept_lens.numel() == B
+    _tree(B, keep.numel(), run_starts)
+    descs = (_Cache * len(caches))(*[c.desc() for c in caches])
+    _launch("kvq_keep_runs", lib().kvq_keep_runs, device, stream, descs, len(caches), _ptr(run_starts), B, keep.numel(),
+            block_table.data_ptr(), width, seq_lens.data_ptr(), keep.data_ptr(), kept_lens.data_ptr(), _ptr(err))
 
 
 def debug_dither(seed: int, layer: int, kv_head: int, slots: torch.Tensor, out: torch.Tensor, stream=None):

@@ -17,6 +17,7 @@
 // are issue slots (2,200 instructions of a warp for an item).
 #include <algorithm>
 
+#include "codes.cuh"
 #include "runs.cuh"
 
 namespace kvq {
@@ -51,35 +52,6 @@ __device__ __forceinline__ int exponent_for(float amax) {
   const uint32_t b = __float_as_uint(amax);
   const int e = static_cast<int>(b >> 23) - 127 - k0 + ((b & 0x7FFFFFu) > lead ? 1 : 0);
   return min(max(e, kMinExp), kMaxExp);
-}
-
-// Four codes of x f, f = 2^-e.  INT8: the sum with 1.5 2^23 + 128 is rounded once, to an integer, and its low byte is
-// code + 128; the values are in range (the caller has clamped them where they need not be).
-template <bool INT8>
-__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float f) {
-  if (INT8) {
-    constexpr float kMagic = 12582912.f + 128.f;
-    const uint32_t a = __float_as_uint(__fmaf_rn(x0, f, kMagic)), b = __float_as_uint(__fmaf_rn(x1, f, kMagic));
-    const uint32_t c = __float_as_uint(__fmaf_rn(x2, f, kMagic)), d = __float_as_uint(__fmaf_rn(x3, f, kMagic));
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
-  }
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 * f, x1 * f), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2 * f, x3 * f), __NV_SATFINITE, __NV_E4M3);
-  return lo | hi << 16;
-}
-template <bool INT8>
-__device__ __forceinline__ float decode(uint8_t b) {
-  return INT8 ? static_cast<float>(static_cast<int>(b) - 128) : e4m3_bits_to_f32(b);
-}
-
-template <bool INT8>
-__device__ __forceinline__ uint4 rescale(uint4 w, float f) {  // 16 codes times f = 2^-d
-  uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = encode4<INT8>(decode<INT8>(x[i]), decode<INT8>(x[i] >> 8), decode<INT8>(x[i] >> 16), decode<INT8>(x[i] >> 24), f);
-  }
-  return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 // eight channels of one row, as loaded and as values

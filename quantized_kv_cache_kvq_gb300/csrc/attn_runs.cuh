@@ -48,6 +48,8 @@ struct AttnArgs {
   const int32_t* seq_lens;
   const int32_t* block_table;
   int max_pages, batch, num_rows, max_run;
+  const int32_t* mask;  // trees only: [num_rows][mask_words]
+  int mask_words;
   float sm_scale;
   void* out;   // [num_rows][Hq][128], the queries' type
   float* lse;  // [num_rows][Hq] or nullptr
@@ -67,6 +69,12 @@ struct AttnArgs {
   int unit_cost;            // what a unit costs beside its tiles, in tiles
   int32_t* err;
 };
+
+// Checks the arguments and fills `args`, all but the workspace's; batch 0: there is nothing to do (attn_runs.cu).
+kvq_status attn_args(AttnArgs* args, const kvq_cache* cache, const void* q, int64_t q_row_stride, int32_t q_dtype, int32_t num_q_heads,
+                     const int32_t* run_starts, int32_t batch, int32_t num_rows, int32_t max_run, const int32_t* block_table,
+                     int32_t max_pages_per_seq, const int32_t* seq_lens, float sm_scale, void* out, float* lse, void* workspace_dev,
+                     int32_t* err_word);
 
 // Tile kernel and its merge (attn_runs_tile.cu); its part of the workspace, with the offsets of the three arrays.
 cudaError_t launch_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s);

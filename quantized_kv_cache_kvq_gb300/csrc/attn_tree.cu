@@ -1,0 +1,69 @@
+// attn_tree.cu -- kvq_attn_tree: attention of trees of drafted tokens over a page-scaled cache; the host side.
+//
+// Every row sees the tokens before its run, and of its run what its mask says.  The split kernel (attn_runs_split.cuh) looks at the masks
+// in the pages that the run touches, as it looks at the causal limit in the last pages of a draft.
+#include <algorithm>
+
+#include "attn_runs_split.cuh"
+
+namespace kvq {
+namespace runs {
+namespace {
+
+struct Workspace {
+  SplitWorkspace split;
+  size_t total;
+  int nt;
+};
+Workspace workspace(int batch, int num_rows, int max_run, int hkv, int hq, int sms) {
+  const int G = hq / hkv;
+  Workspace w{};
+  w.nt = row_blocks(static_cast<long long>(max_run) * G);
+  w.split = split_workspace((static_cast<size_t>(num_rows) * G) / (8 * w.nt) + batch, w.nt, hkv, sms);
+  w.total = w.split.total;
+  return w;
+}
+
+}  // namespace
+}  // namespace runs
+}  // namespace kvq
+
+using namespace kvq;
+using namespace kvq::runs;
+
+extern "C" size_t kvq_attn_tree_workspace_size(int32_t batch, int32_t num_rows, int32_t max_run, int32_t num_kv_heads,
+                                               int32_t num_q_heads, int32_t q_dtype) {
+  if (batch < 0 || batch > kMaxBatch || num_rows < 0 || max_run < 0 || max_run > KVQ_MAX_TREE || num_kv_heads <= 0 || num_q_heads <= 0 ||
+      num_q_heads % num_kv_heads || (q_dtype != KVQ_DTYPE_F32 && q_dtype != KVQ_DTYPE_BF16))
+    return 0;
+  const int sms = device_sm_count();
+  if (sms <= 0) return 0;
+  return workspace(batch, num_rows, std::min(max_run, num_rows), num_kv_heads, num_q_heads, sms).total;
+}
+
+extern "C" kvq_status kvq_attn_tree(const kvq_cache* cache, const void* q, int64_t q_row_stride, int32_t q_dtype, int32_t num_q_heads,
+                                    const int32_t* run_starts, int32_t batch, int32_t num_rows, int32_t max_run,
+                                    const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* mask,
+                                    int32_t mask_words, float sm_scale, void* out, float* lse, void* workspace_dev, size_t ws_bytes,
+                                    int32_t* err_word, kvq_stream_t stream) {
+  AttnArgs a{};
+  const kvq_status st = attn_args(&a, cache, q, q_row_stride, q_dtype, num_q_heads, run_starts, batch, num_rows, max_run, block_table,
+                                  max_pages_per_seq, seq_lens, sm_scale, out, lse, workspace_dev, err_word);
+  if (st != KVQ_OK) return st;
+  if (max_run > KVQ_MAX_TREE || mask_words < (max_run + 31) / 32) return KVQ_ERR_INVALID_ARG;
+  if (a.batch == 0) return KVQ_OK;
+  if (!mask) return KVQ_ERR_INVALID_ARG;
+  a.mask = mask;
+  a.mask_words = mask_words;
+  const int sms = device_sm_count(), smem_max = device_smem_optin();
+  if (sms <= 0 || smem_max <= 0) return KVQ_ERR_CUDA;
+  const Workspace w = workspace(batch, num_rows, a.max_run, a.Hkv, a.Hq, sms);
+  if (ws_bytes < w.total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  a.few_rows = 0x7FFFFFFF;
+  w.split.put(a, static_cast<uint8_t*>(workspace_dev));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool f32 = q_dtype == KVQ_DTYPE_F32;
+  const cudaError_t e = cache->k_fmt == KVQ_FMT_INT8_PAGE ? launch<true, true>(a, f32, w.nt, sms, smem_max, s)
+                                                          : launch<false, true>(a, f32, w.nt, sms, smem_max, s);
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}

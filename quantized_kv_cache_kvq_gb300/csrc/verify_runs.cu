@@ -1,0 +1,442 @@
+// verify_runs.cu -- kvq_verify_runs: which path of a tree of drafted tokens the target's probabilities accept, from given random numbers.
+//
+// Recursive rejection at a row with probabilities p and draft probabilities q: child x is accepted with probability
+// min(1, p_k(x) / q(x)), p_0 = p / sum p, and a refusal goes on with p_{k+1} = max(p_k - q, 0) / sum of it.  All of these are one family:
+//     p_k = max(p - c_k q, 0) / Z_k,   Z_k = sum max(p - c_k q, 0),   c_0 = 0,  c_{k+1} = c_k + Z_k
+// (p_k - q = (max(p - c_k q, 0) - Z_k q) / Z_k, positive where p > (c_k + Z_k) q), so a refusal costs one sum over the vocabulary and no
+// vector is kept.  Without draft probabilities the token is drawn from p and followed to the child that holds it; greedy, it is the largest score's.
+//
+// Sums are whole numbers, floor(2^44 w) in 64 bits: they do not depend on the order, the split or the batch, and the cumulative
+// distribution that a token is drawn from is exact (with binary32 sums of a flat distribution of 10^5 tokens, a random number in a
+// hundred would find another token).
+//
+// A cluster of eight blocks has a request and walks its tree: only the rows of the path are read.  A row is cut into one piece for each warp;
+// after every pass the warps write their sums to all blocks, one cluster barrier, and all blocks take the same decision.  What decides is
+// read by the first block alone and handed to the others (the tree at the start, a child's numbers beside the sums), so that blocks take
+// the same number of barriers whatever another stream does to the inputs.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "runs.cuh"
+
+namespace kvq {
+namespace runs {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kCluster = 8;
+constexpr int kWarps = 16;  // of a block
+constexpr int kThreads = 32 * kWarps;
+constexpr int kPieces = kCluster * kWarps;
+constexpr int kMaxVocab = 1 << 19;  // sums of 2^19 times 2^44 fit 64 bits
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct VerifyArgs {
+  const void* target;
+  const void* draft;
+  long long target_stride, draft_stride;
+  int vocab;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const float* uniform;
+  const int32_t* run_starts;
+  int batch, num_rows;
+  int32_t* keep;
+  int32_t* kept;
+  int32_t* next;
+  const int32_t* seq_lens;
+  int32_t* seq_lens_out;
+  int32_t* err;
+};
+
+// What the first block reads for the decision after a pass.
+struct Ask {
+  float u, p, q;  // of the child that is tried next
+  float draw;     // the row's own random number
+};
+struct Shared {
+  int32_t parent[KVQ_MAX_TREE], token[KVQ_MAX_TREE];
+  unsigned long long part[2][kPieces];  // sums of a pass (two in turn), or its largest keys
+  unsigned long long first[kPieces];    // those of p itself
+  Ask ask[2];
+  int run[4];   // row0, n, len, whether there is a run
+  int found[2];  // drawn token
+};
+
+template <bool BF16>
+__device__ __forceinline__ float value_at(const void* p, long long i) {
+  return BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16) : static_cast<const float*>(p)[i];
+}
+template <bool BF16>
+constexpr int kVecOf = BF16 ? 8 : 4;  // elements of 16 bytes
+
+// Elements i .. of a row of n elements; `fill` outside.  One load where the 16 bytes are aligned and all inside.
+template <bool BF16>
+__device__ __forceinline__ void load_vec(const uint8_t* row, int i, int n, float (&x)[kVecOf<BF16>], float fill) {
+  constexpr int kSize = BF16 ? 2 : 4, kVec = kVecOf<BF16>;
+  const uint8_t* p = row + static_cast<long long>(i) * kSize;
+  if (i >= 0 && i + kVec <= n && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (BF16) {
+        x[(2 * e) % kVec] = __uint_as_float(u[e] << 16);
+        x[(2 * e + 1) % kVec] = __uint_as_float(u[e] & 0xFFFF0000u);
+      } else {
+        x[e] = __uint_as_float(u[e]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) x[e] = i + e >= 0 && i + e < n ? value_at<BF16>(row, i + e) : fill;
+  }
+}
+// Elements by which a row begins behind a 16-byte boundary.
+template <bool BF16>
+__device__ __forceinline__ int phase_of(const uint8_t* row) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / (BF16 ? 2 : 4);
+}
+
+// A probability as it is taken: 0 for what is none.  bad: 1 outside [0, 1], 2 not finite.
+__device__ __forceinline__ float probability(float x, int& bad) {
+  if (x >= 0.f && x <= 1.f) return x;
+  bad |= isfinite(x) ? 1 : 2;
+  return 0.f;
+}
+// floor(2^44 x), 0 <= x <= 1: the significand (x = m 2^(e - 150)) shifted.
+__device__ __forceinline__ unsigned long long whole(float x) {
+  const uint32_t b = __float_as_uint(x), e = b >> 23;
+  const unsigned long long m = static_cast<unsigned long long>(b & 0x7FFFFFu | 0x800000u) << 21;
+  return e == 0 ? 0 : m >> min(127u - e, 63u);
+}
+__device__ __forceinline__ float rest(float p, float q, float c) { return fmaxf(__fsub_rn(p, __fmul_rn(c, q)), 0.f); }
+
+// Scores in the order of their values as unsigned numbers: NaN lowest, -0 as 0.
+__device__ __forceinline__ uint32_t ordered(float x, int& bad) {
+  if (x != x) {
+    bad |= 2;
+    x = -INFINITY;
+  }
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+enum class Pass { kGreedy, kTarget, kRest };
+
+// A warp's piece of a row: the sum of whole(p), of whole(rest(p, q, c)), or the largest (score, ~index).
+template <bool BF16, Pass PASS>
+__device__ __forceinline__ unsigned long long pass_over(const uint8_t* p, const uint8_t* q, float c, int vocab, int piece, int& bad) {
+  constexpr int kVec = kVecOf<BF16>;
+  const int lane = threadIdx.x & 31, off = phase_of<BF16>(p);
+  const int n = (vocab + off + kVec - 1) / kVec;
+  const int v0 = n * piece / kPieces, v1 = n * (piece + 1) / kPieces;
+  unsigned long long sum = 0;
+#pragma unroll 4
+  for (int v = v0 + lane; v < v1; v += 32) {
+    const int i = v * kVec - off;
+    float x[kVec], y[kVec];
+    load_vec<BF16>(p, i, vocab, x, PASS == Pass::kGreedy ? -INFINITY : 0.f);
+    if (PASS == Pass::kRest) load_vec<BF16>(q, i, vocab, y, 0.f);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      if (PASS == Pass::kGreedy) {
+        const unsigned long long key = static_cast<unsigned long long>(ordered(x[e], bad)) << 32 | static_cast<uint32_t>(~(i + e));
+        if (i + e >= 0 && i + e < vocab && key > sum) sum = key;
+      } else if (PASS == Pass::kTarget) {
+        sum += whole(probability(x[e], bad));
+      } else {
+        sum += whole(rest(probability(x[e], bad), probability(y[e], bad), c));
+      }
+    }
+  }
+  if (PASS != Pass::kGreedy) return warp_sum(sum);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const unsigned long long other = __shfl_xor_sync(kAll, sum, o);
+    if (other > sum) sum = other;
+  }
+  return sum;
+}
+
+// The token of a piece at which the sum over the piece first exceeds t (t is less than the piece's sum).
+template <bool BF16, bool REST>
+__device__ __forceinline__ int token_at(const uint8_t* p, const uint8_t* q, float c, int vocab, int piece, unsigned long long t) {
+  constexpr int kVec = kVecOf<BF16>;
+  const int lane = threadIdx.x & 31, off = phase_of<BF16>(p);
+  const int n = (vocab + off + kVec - 1) / kVec;
+  const int v0 = n * piece / kPieces, v1 = n * (piece + 1) / kPieces;
+  int bad = 0;
+  for (int b = v0; b < v1; b += 32) {
+    const int i = (b + lane) * kVec - off;
+    float x[kVec] = {}, y[kVec] = {};
+    if (b + lane < v1) {
+      load_vec<BF16>(p, i, vocab, x, 0.f);
+      if (REST) load_vec<BF16>(q, i, vocab, y, 0.f);
+    }
+    unsigned long long w[kVec], mine = 0;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      const float pe = probability(x[e], bad);
+      mine += w[e] = whole(REST ? rest(pe, probability(y[e], bad), c) : pe);
+    }
+    unsigned long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long up = __shfl_up_sync(kAll, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const unsigned hit = __ballot_sync(kAll, inc > t);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      unsigned long long before = inc - mine;
+      int tok = 0;
+#pragma unroll
+      for (int e = kVec - 1; e >= 0; --e) {  // the first e with before + w[0] + .. + w[e] > t
+        unsigned long long s = before;
+#pragma unroll
+        for (int f = 0; f <= e; ++f) s += w[f];
+        if (s > t) tok = i + e;
+      }
+      return __shfl_sync(kAll, tok, l);
+    }
+    t -= __shfl_sync(kAll, inc, 31);
+  }
+  return 0;  // cannot be, unless the row changed under the call
+}
+
+template <bool BF16>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+  __shared__ Shared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int s = blockIdx.x / kCluster, piece = rank * kWarps + warp;
+  cluster.sync();  // every block runs before another one writes to it
+  if (rank == 0) {  // the run and its tree, to all blocks
+    __shared__ int run[4];
+    if (tid == 0) {
+      const int r0 = a.run_starts ? a.run_starts[s] : s, r1 = a.run_starts ? a.run_starts[s + 1] : s + 1;
+      const int len = a.seq_lens ? a.seq_lens[s] : 0;
+      const bool ok = r0 >= 0 && r1 >= r0 && r1 <= a.num_rows && r1 - r0 <= KVQ_MAX_TREE && (!a.seq_lens || (len >= r1 - r0 && len <= kMaxContext));
+      if (!ok) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
+      run[0] = r0;
+      run[1] = ok ? r1 - r0 : 0;
+      run[2] = len;
+      run[3] = ok;
+    }
+    __syncthreads();
+    for (int r = 0; r < kCluster; ++r) {
+      Shared* to = cluster.map_shared_rank(&sh, r);
+      if (tid < 4) to->run[tid] = run[tid];
+    }
+    for (int i = tid; i < run[1]; i += kThreads) {
+      const int up = a.parents[run[0] + i], tok = a.tokens[run[0] + i];
+      if (up < -1 || up >= i) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
+      if (i > 0 && (tok < 0 || tok >= a.vocab)) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
+      for (int r = 0; r < kCluster; ++r) {
+        Shared* to = cluster.map_shared_rank(&sh, r);
+        to->parent[i] = i == 0 || up >= i ? -1 : up;
+        to->token[i] = tok;
+      }
+    }
+  }
+  cluster.sync();
+  const int row0 = sh.run[0], n = sh.run[1];
+  const bool writer = rank == 0 && tid == 0;
+  if (n == 0) {
+    if (writer) {
+      a.kept[s] = 0;
+      a.next[s] = -1;
+      if (a.seq_lens_out) a.seq_lens_out[s] = sh.run[2];
+    }
+    return;
+  }
+  const bool greedy = a.uniform == nullptr, drafts = a.draft != nullptr;
+  int turn = 0;  // which of the two exchanges
+  int bad = 0;
+  constexpr int kSize = BF16 ? 2 : 4;
+  // the first child of `cur` behind row `j`, n for none
+  auto next_child = [&](int cur, int j) {
+    for (int b = (j + 1) & ~31; b < n; b += 32) {
+      const int i = b + lane;
+      const unsigned hit = __ballot_sync(kAll, i > j && i < n && sh.parent[i] == cur);
+      if (hit) return b + __ffs(hit) - 1;
+    }
+    return n;
+  };
+  // the numbers that decide about a child, and the row's own
+  auto ask = [&](int cur, int child) {
+    Ask k{0.f, 0.f, 0.f, 0.f};
+    k.draw = a.uniform[2 * (static_cast<long long>(row0) + cur) + 1];
+    if (child < n) {
+      const int tok = sh.token[child];
+      k.u = a.uniform[2 * (static_cast<long long>(row0) + child)];
+      if (!(k.u >= 0.f && k.u < 1.f)) report(a.err, KVQ_ERR_RANGE);
+      if (tok >= 0 && tok < a.vocab) {
+        const long long row = row0 + cur;
+        k.p = probability(value_at<BF16>(a.target, row * a.target_stride + tok), bad);
+        k.q = probability(value_at<BF16>(a.draft, row * a.draft_stride + tok), bad);
+      }
+    }
+    return k;
+  };
+  // a warp's sum, and beside it what is asked, to all blocks; the sums of all warps are in sh.part[turn ^ 1] afterwards
+  auto exchange = [&](unsigned long long v, const Ask* k) {
+    if (lane < kCluster) cluster.map_shared_rank(&sh, lane)->part[turn][piece] = v;
+    if (k && rank == 0 && warp == 0 && lane < kCluster) cluster.map_shared_rank(&sh, lane)->ask[turn] = *k;
+    cluster.sync();
+    turn ^= 1;
+  };
+  auto total = [&](const unsigned long long* part) {
+    unsigned long long v = 0;
+#pragma unroll
+    for (int i = 0; i < kPieces / 32; ++i) v += part[32 * i + lane];
+    return warp_sum(v);
+  };
+  int cur = 0, kept = 1, last = -1;
+  if (writer) a.keep[row0] = 0;
+  for (int step = 0; step < n; ++step) {  // a path has at most n rows
+    const long long row = row0 + cur;
+    const uint8_t* p = static_cast<const uint8_t*>(a.target) + row * a.target_stride * kSize;
+    const uint8_t* q = drafts ? static_cast<const uint8_t*>(a.draft) + row * a.draft_stride * kSize : nullptr;
+    int go = n, drawn = -1;
+    if (greedy) {
+      exchange(pass_over<BF16, Pass::kGreedy>(p, q, 0.f, a.vocab, piece, bad), nullptr);
+      unsigned long long best = 0;
+#pragma unroll
+      for (int i = 0; i < kPieces / 32; ++i) best = max(best, sh.part[turn ^ 1][32 * i + lane]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(kAll, best, o));
+      drawn = static_cast<int>(~static_cast<uint32_t>(best));
+    } else {
+      int child = drafts ? next_child(cur, 0) : n;
+      Ask k{};
+      if (rank == 0 && warp == 0) k = ask(cur, child);
+      exchange(pass_over<BF16, Pass::kTarget>(p, q, 0.f, a.vocab, piece, bad), &k);
+      const unsigned long long* part = sh.part[turn ^ 1];
+      unsigned long long z = total(part);
+      const unsigned long long z0 = z;
+      float c = 0.f;
+      if (child < n) {
+        for (int i = tid; i < kPieces; i += kThreads) sh.first[i] = part[i];
+        while (child < n) {
+          k = sh.ask[turn ^ 1];
+          const double zd = static_cast<double>(z) * 0x1p-44, cq = static_cast<double>(c) * static_cast<double>(k.q);
+          if (__dmul_rn(static_cast<double>(k.u) * static_cast<double>(k.q), zd) < __dsub_rn(static_cast<double>(k.p), cq)) {
+            go = child;
+            break;
+          }
+          c = static_cast<float>(__dadd_rn(static_cast<double>(c), zd));
+          child = next_child(cur, child);
+          if (rank == 0 && warp == 0) k = ask(cur, child);
+          exchange(pass_over<BF16, Pass::kRest>(p, q, c, a.vocab, piece, bad), &k);
+          part = sh.part[turn ^ 1];
+          z = total(part);
+        }
+        __syncthreads();  // sh.first
+      }
+      if (go == n) {  // draw
+        float u = sh.ask[turn ^ 1].draw;
+        if (writer && !(u >= 0.f && u < 1.f)) report(a.err, KVQ_ERR_RANGE);
+        if (z == 0 && c != 0.f) {
+          part = sh.first;
+          z = z0;
+          c = 0.f;
+        }
+        if (z == 0) {
+          if (writer) report(a.err, KVQ_ERR_RANGE);
+        } else {
+          const double td = floor(__dmul_rn(static_cast<double>(u), static_cast<double>(z)));
+          const unsigned long long t = td > 0. ? (td < static_cast<double>(z) ? static_cast<unsigned long long>(td) : z - 1) : 0;
+          // the piece that holds t, and what is before it
+          unsigned long long before = 0, mine = 0;
+          int which = -1;
+          for (int i = 0; i < kPieces / 32 && which < 0; ++i) {
+            const unsigned long long v = part[32 * i + lane];
+            unsigned long long inc = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const unsigned long long up = __shfl_up_sync(kAll, inc, o);
+              if (lane >= o) inc += up;
+            }
+            const unsigned hit = __ballot_sync(kAll, before + inc > min(t, z - 1));
+            if (hit) {
+              const int l = __ffs(hit) - 1;
+              which = 32 * i + l;
+              mine = before + __shfl_sync(kAll, inc - v, l);
+            }
+            before += __shfl_sync(kAll, inc, 31);
+          }
+          if (which == piece) {
+            const int tok = c != 0.f ? token_at<BF16, true>(p, q, c, a.vocab, piece, min(t, z - 1) - mine)
+                                     : token_at<BF16, false>(p, q, c, a.vocab, piece, min(t, z - 1) - mine);
+            if (lane < kCluster) cluster.map_shared_rank(&sh, lane)->found[turn] = tok;
+          }
+          cluster.sync();
+          drawn = sh.found[turn];
+          turn ^= 1;
+        }
+      }
+    }
+    if (!drafts && drawn >= 0) {
+      go = cur;
+      do go = next_child(cur, go); while (go < n && sh.token[go] != drawn);
+    }
+    if (go >= n) {
+      last = drawn;
+      break;
+    }
+    if (writer) a.keep[row0 + kept] = go;
+    ++kept;
+    cur = go;
+  }
+  if (bad) report(a.err, bad & 2 ? KVQ_ERR_NONFINITE_INPUT : KVQ_ERR_RANGE);
+  if (rank == 0) {
+    for (int i = kept + tid; i < n; i += kThreads) a.keep[row0 + i] = -1;
+    if (tid == 0) {
+      a.kept[s] = kept;
+      a.next[s] = last;
+      if (a.seq_lens_out) a.seq_lens_out[s] = sh.run[2] - n + kept;
+    }
+  }
+  cluster.sync();  // no block ends while another may still write to it
+}
+
+}  // namespace
+}  // namespace runs
+}  // namespace kvq
+
+extern "C" kvq_status kvq_verify_runs(const void* target, int64_t target_row_stride, const void* draft, int64_t draft_row_stride,
+                                      int32_t dtype, int32_t vocab, const int32_t* tokens, const int32_t* parents, const float* uniform,
+                                      const int32_t* run_starts, int32_t batch, int32_t num_rows, int32_t* keep, int32_t* kept_lens,
+                                      int32_t* next_tokens, const int32_t* seq_lens, int32_t* seq_lens_out, int32_t* err_word,
+                                      kvq_stream_t stream) {
+  using namespace kvq;
+  using namespace kvq::runs;
+  if (dtype != KVQ_DTYPE_F32 && dtype != KVQ_DTYPE_BF16) return KVQ_ERR_INVALID_ARG;
+  if (vocab < 1 || vocab > kMaxVocab || batch < 0 || batch > kMaxBatch || num_rows < 0) return KVQ_ERR_INVALID_ARG;
+  if (!run_starts && num_rows != batch) return KVQ_ERR_INVALID_ARG;
+  if ((seq_lens != nullptr) != (seq_lens_out != nullptr) || (draft && !uniform)) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  if (!kept_lens || !next_tokens) return KVQ_ERR_INVALID_ARG;
+  const uintptr_t mask = dtype == KVQ_DTYPE_BF16 ? 1u : 3u;
+  if (num_rows > 0) {
+    if (!target || !tokens || !parents || !keep) return KVQ_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(target) & mask) || (reinterpret_cast<uintptr_t>(draft) & mask)) return KVQ_ERR_INVALID_ARG;
+    if (target_row_stride < vocab || (draft && draft_row_stride < vocab)) return KVQ_ERR_INVALID_ARG;
+  }
+  const VerifyArgs a{target, draft, target_row_stride, draft_row_stride, vocab, tokens, parents, uniform, run_starts, batch, num_rows, keep, kept_lens,
+                     next_tokens, seq_lens, seq_lens_out, err_word};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == KVQ_DTYPE_BF16) verify_kernel<true><<<batch * kCluster, kThreads, 0, st>>>(a);
+  else verify_kernel<false><<<batch * kCluster, kThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
