@@ -545,6 +545,12 @@ def _own(st):
                         seq_lens=st["seq_lens"], seq_lens_out=st["seq_lens_out"], run_starts=starts, err=err)
         return _verify_out(st)
     if "caches" not in st:
+        if st["k_scale"][0].numel() % 8:  # planes begin on 16 bytes: each layer's in a piece of memory of its own
+            for name in ("k_scale", "v_scale"):
+                one = st[name][0].numel()
+                roomy = torch.zeros((len(st[name]), -(-one // 8) * 8), dtype=torch.float16, device=err.device)
+                roomy[:, :one] = st[name].flatten(1)
+                st[name] = roomy[:, :one].unflatten(1, st[name].shape[1:])
         st["caches"] = [kvq.PagedCache.over(case["fmt"], case["fmt"], case["kv_heads"], st["total"], k=k, v=v, k_scale=ks, v_scale=vs, layer=i)
                         for i, (k, v, ks, vs) in enumerate(zip(st["k"], st["v"], st["k_scale"], st["v_scale"]))]
     if st["op"] == "keep":
