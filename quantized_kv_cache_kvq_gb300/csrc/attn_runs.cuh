@@ -79,6 +79,9 @@ kvq_status attn_args(AttnArgs* args, const kvq_cache* cache, const void* q, int6
 // Tile kernel and its merge (attn_runs_tile.cu); its part of the workspace, with the offsets of the three arrays.
 cudaError_t launch_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s);
 size_t tile_workspace(int sms, size_t* acc, size_t* stats, size_t* rec);
+// The same for trees (attn_tree_tile.cu).
+cudaError_t launch_tree_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s);
+size_t tree_tile_workspace(int sms, size_t* acc, size_t* stats, size_t* rec);
 
 }  // namespace runs
 }  // namespace kvq

@@ -1,7 +1,8 @@
 // attn_tree.cu -- kvq_attn_tree: attention of trees of drafted tokens over a page-scaled cache; the host side.
 //
-// Every row sees the tokens before its run, and of its run what its mask says.  The split kernel (attn_runs_split.cuh) looks at the masks
-// in the pages that the run touches, as it looks at the causal limit in the last pages of a draft.
+// Every row sees the tokens before its run, and of its run what its mask says.  Calls of few rows (and of fp32 queries) have the split
+// kernel (attn_runs_split.cuh), which looks at the masks in the pages that the run touches; the others the tile kernel (attn_tree_tile.cu),
+// for all their runs.
 #include <algorithm>
 
 #include "attn_runs_split.cuh"
@@ -10,17 +11,27 @@ namespace kvq {
 namespace runs {
 namespace {
 
+// Calls whose longest run has more (token, head) rows are the tile kernel's.
+constexpr int kFewRows = 16;
+
 struct Workspace {
   SplitWorkspace split;
-  size_t total;
-  int nt;
+  size_t tw_acc, tw_stats, tw_rec, total;
+  int nt;     // split kernel: row tiles of 8 nt rows
+  bool tile;  // the tile kernel's
 };
-Workspace workspace(int batch, int num_rows, int max_run, int hkv, int hq, int sms) {
+Workspace workspace(int batch, int num_rows, int max_run, int hkv, int hq, int q_dtype, int sms) {
   const int G = hq / hkv;
+  const long long max_rows = static_cast<long long>(max_run) * G;
   Workspace w{};
-  w.nt = row_blocks(static_cast<long long>(max_run) * G);
-  w.split = split_workspace((static_cast<size_t>(num_rows) * G) / (8 * w.nt) + batch, w.nt, hkv, sms);
-  w.total = w.split.total;
+  w.tile = q_dtype == KVQ_DTYPE_BF16 && max_rows > kFewRows;
+  w.nt = row_blocks(max_rows);
+  if (w.tile) {
+    w.total = tree_tile_workspace(sms, &w.tw_acc, &w.tw_stats, &w.tw_rec);
+  } else {
+    w.split = split_workspace((static_cast<size_t>(num_rows) * G) / (8 * w.nt) + batch, w.nt, hkv, sms);
+    w.total = w.split.total;
+  }
   return w;
 }
 
@@ -38,7 +49,7 @@ extern "C" size_t kvq_attn_tree_workspace_size(int32_t batch, int32_t num_rows, 
     return 0;
   const int sms = device_sm_count();
   if (sms <= 0) return 0;
-  return workspace(batch, num_rows, std::min(max_run, num_rows), num_kv_heads, num_q_heads, sms).total;
+  return workspace(batch, num_rows, std::min(max_run, num_rows), num_kv_heads, num_q_heads, q_dtype, sms).total;
 }
 
 extern "C" kvq_status kvq_attn_tree(const kvq_cache* cache, const void* q, int64_t q_row_stride, int32_t q_dtype, int32_t num_q_heads,
@@ -57,13 +68,23 @@ extern "C" kvq_status kvq_attn_tree(const kvq_cache* cache, const void* q, int64
   a.mask_words = mask_words;
   const int sms = device_sm_count(), smem_max = device_smem_optin();
   if (sms <= 0 || smem_max <= 0) return KVQ_ERR_CUDA;
-  const Workspace w = workspace(batch, num_rows, a.max_run, a.Hkv, a.Hq, sms);
+  const Workspace w = workspace(batch, num_rows, a.max_run, a.Hkv, a.Hq, q_dtype, sms);
   if (ws_bytes < w.total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
-  a.few_rows = 0x7FFFFFFF;
-  w.split.put(a, static_cast<uint8_t*>(workspace_dev));
+  uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool f32 = q_dtype == KVQ_DTYPE_F32;
-  const cudaError_t e = cache->k_fmt == KVQ_FMT_INT8_PAGE ? launch<true, true>(a, f32, w.nt, sms, smem_max, s)
-                                                          : launch<false, true>(a, f32, w.nt, sms, smem_max, s);
+  const bool int8 = cache->k_fmt == KVQ_FMT_INT8_PAGE, f32 = q_dtype == KVQ_DTYPE_F32;
+  cudaError_t e;
+  if (w.tile) {
+    a.few_rows = 0;
+    a.tw_acc = reinterpret_cast<float*>(ws + w.tw_acc);
+    a.tw_stats = reinterpret_cast<float*>(ws + w.tw_stats);
+    a.tw_rec = reinterpret_cast<int32_t*>(ws + w.tw_rec);
+    if (a.num_pages == 0) a.k = a.v = ws;  // absent pages are read as page 0 and thrown away
+    e = launch_tree_tile(a, int8, sms, s);
+  } else {
+    a.few_rows = 0x7FFFFFFF;
+    w.split.put(a, ws);
+    e = int8 ? launch<true, true>(a, f32, w.nt, sms, smem_max, s) : launch<false, true>(a, f32, w.nt, sms, smem_max, s);
+  }
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
