@@ -205,7 +205,7 @@ def load(path: str = LIB_PATH):
     L.kvq_verify_runs.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
                                   c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]
     L.kvq_keep_runs.restype = c_int32
-    L.kvq_keep_runs.argtypes = [POINTER(_Cache), c_int32, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
+    L.kvq_keep_runs.argtypes = [c_void_p, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
                                 c_void_p, c_void_p, c_void_p]
     L.kvq_sizeof.restype = c_size_t
     L.kvq_sizeof.argtypes = [c_int32]
@@ -339,6 +339,18 @@ class PagedCache:
                       self.seed & 0xFFFFFFFFFFFFFFFF, _ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
                       _ptr(self.v_scale), _ptr(self.witness), _ptr(self.v_witness), _ptr(self.outlier_pairs),
                       self.n_out, 0, _ptr(self.k_outlier))
+
+    def _packed(self, device: int) -> bytes:
+        """desc() as bytes, checked to be on ``device``; made anew where a plane is another one than the last time (a step's keep_runs takes
+        the descriptors of all layers)."""
+        if self.k_fmt not in PAGE_SCALED:
+            return bytes(self.desc())  # the library's to refuse
+        at = (self._k.data_ptr(), self._v.data_ptr(), self._k_scale.data_ptr(), self._v_scale.data_ptr(), device, self.num_kv_heads,
+              self.num_pages, self.k_fmt)
+        if self.__dict__.get("_packed_at") != at:
+            self._check_device(device)
+            self._packed_desc, self._packed_at = bytes(self.desc()), at
+        return self._packed_desc
 
     def nbytes(self) -> int:
         return sum(t.nbytes for t in (self.k, self.v, self.k_scale, self.v_scale, self.witness, self.v_witness,
@@ -738,13 +750,11 @@ def keep_runs(caches, seq_lens: torch.Tensor, block_table: torch.Tensor, keep: t
     list of them, one for each layer, all alike).  seq_lens [B] count the kept tokens already (verify_runs's seq_lens_out)."""
     caches = [caches] if isinstance(caches, PagedCache) else list(caches)
     device = seq_lens.get_device()
-    for c in caches:
-        c._check_device(device)
+    descs = b"".join([c._packed(device) for c in caches])
     _i32(device, seq_lens, block_table, keep, kept_lens, run_starts, err)
     B, width = block_table.shape
     assert seq_lens.numel() == B and kept_lens.numel() == B
     _tree(B, keep.numel(), run_starts)
-    descs = (_Cache * len(caches))(*[c.desc() for c in caches])
     _launch("kvq_keep_runs", lib().kvq_keep_runs, device, stream, descs, len(caches), _ptr(run_starts), B, keep.numel(),
             block_table.data_ptr(), width, seq_lens.data_ptr(), keep.data_ptr(), kept_lens.data_ptr(), _ptr(err))
 

@@ -4,8 +4,10 @@
 // takes tokens only from itself and from later ones: a request's pages are rewritten from the first on, each read whole before it is written.
 // A page's scale becomes the largest, 2^e, that its tokens had; codes of a token under 2^(e - d) become rne(code 2^-d), as in an append.
 //
-// One launch for all layers: one block for each (request, layer, kv head).  A key token is eight 16-byte words of its tile, so a thread moves one word of the
-// new tile; a value word holds four tokens of four channels, so a thread puts one together from the words of its four tokens.
+// One launch for all layers.  A block has one request and a few (layer, kv head) pairs: where every slot's token comes from is looked up once for
+// all of them.  A key token is eight 16-byte words of its tile, so a thread moves one word of the new tile; a value word holds four tokens of four
+// channels, so a thread puts one together from the words of its four tokens.  Words that stay as they are are neither read nor written.
+// Bound by memory: a value tile's tokens lie in all of its lines, so moving one token reads and writes 2 KB.
 #include <algorithm>
 
 #include "codes.cuh"
@@ -18,6 +20,7 @@ namespace {
 constexpr int kThreads = 128;  // a 16-byte word of a tile each
 constexpr int kTile = 2048;
 constexpr int kMaxLayers = 128;  // of a launch
+constexpr int kResident = 8;     // blocks on an SM
 
 struct Planes {
   uint8_t* k;
@@ -26,7 +29,7 @@ struct Planes {
   uint16_t* vs;
 };
 struct KeepArgs {
-  int H, num_pages;
+  int H, num_pages, layers;
   const int32_t* run_starts;
   const int32_t* seq_lens;
   const int32_t* block_table;
@@ -38,14 +41,14 @@ struct KeepArgs {
 };
 
 template <bool INT8>
-__global__ void __launch_bounds__(kThreads) keep_kernel(const __grid_constant__ KeepArgs a) {
+__global__ void __launch_bounds__(kThreads, kResident) keep_kernel(const __grid_constant__ KeepArgs a) {
   __shared__ int s_list[KVQ_MAX_TREE];
   __shared__ int s_phys[KVQ_MAX_TREE / kPage + 2];  // pages of the run, from its first token's on
-  const int s = blockIdx.z, h = blockIdx.x, tid = threadIdx.x;
+  const int s = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int m = a.kept[s];
   const int r0 = a.run_starts ? a.run_starts[s] : s, r1 = a.run_starts ? a.run_starts[s + 1] : s + 1, len = a.seq_lens[s];
   const int n = r1 - r0, p0 = len - m;
-  const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+  const bool first = blockIdx.x == 0;
   if (r0 < 0 || r1 < r0 || r1 > a.num_rows || n > KVQ_MAX_TREE || m < 0 || m > n || len < m || len > kMaxContext ||
       static_cast<long long>(p0) + n > static_cast<long long>(a.max_pages) * kPage) {
     if (first && tid == 0) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
@@ -77,68 +80,73 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const __grid_constant__ 
     if (first && tid == 0) report(a.err, KVQ_ERR_DEVICE_BOUNDS);
     return;
   }
-  const Planes& P = a.layer[blockIdx.y];
   const int dst_pages = (len - 1) / kPage - page0 + 1;
+  const int tk = ((tid >> 6) << 3) | ((tid >> 2) & 7), q = tid & 3;  // the key word's token; the value word's are 2 q, 2 q + 1, 2 q + 8, 2 q + 9
+  const int pairs = a.H * a.layers;
   for (int d = 0; d < dst_pages; ++d) {
     const int at = (page0 + d) * kPage;        // position of the page's first token
     const int from = max(0, p0 - at), to = min(kPage, len - at);  // kept tokens of the run
     if (s_list[at + to - 1 - p0] == at + to - 1 - p0) continue;  // the list rises: nothing moves before it either
-    // where slot t's token is: page of the run, slot
-    auto source = [&](int t) {
-      const int p = t < from ? at + t : p0 + s_list[at + t - p0];
-      return p - page0 * kPage;
-    };
-    int ek = kMinExp, ev = kMinExp;
-    for (int t = 0; t < to; ++t) {
-      const size_t si = static_cast<size_t>(h) * a.num_pages + s_phys[source(t) / kPage];
-      ek = max(ek, f16_to_exp(P.ks[si]));
-      ev = max(ev, f16_to_exp(P.vs[si]));
-    }
-    auto tile_of = [&](int src) { return (static_cast<size_t>(s_phys[src / kPage]) * a.H + h) * kTile; };
-    auto scale_at = [&](int src) { return static_cast<size_t>(h) * a.num_pages + s_phys[src / kPage]; };
+    // Where slot t's token is, counted from the run's first page on; -1: behind the last token.
+    auto source = [&](int t) { return t >= to ? -1 : t < from ? at + t - page0 * kPage : p0 + s_list[at + t - p0] - page0 * kPage; };
+    const int self = d * kPage;  // slot 0 of the page in that count
+    const int sk = source(tk);
+    int sv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sv[i] = source(2 * q + (i & 1) + 8 * (i >> 1));
+    const bool v_stays = sv[0] == self + 2 * q && sv[1] == self + 2 * q + 1 && sv[2] == self + 2 * q + 8 && sv[3] == self + 2 * q + 9;
+    const int mine = source(lane & 15);  // lanes 0..15 look up the keys' scales, the others the values'
+    auto phys_of = [&](int src) { return s_phys[src >> 4]; };
     constexpr uint32_t kZero = INT8 ? 0x80808080u : 0u;
-    uint4 wk = make_uint4(kZero, kZero, kZero, kZero), wv = wk;
-    {  // key word tid: token 8 (tid >> 6) + (tid >> 2 & 7), 16 channels
-      const int t = ((tid >> 6) << 3) | ((tid >> 2) & 7);
-      if (t < to) {
-        const int src = source(t), slot = src % kPage;
-        wk = *reinterpret_cast<const uint4*>(P.k + tile_of(src) + 16 * (((((slot >> 3) << 1) | ((tid >> 5) & 1)) << 5) | ((slot & 7) << 2) | (tid & 3)));
-        const int e = f16_to_exp(P.ks[scale_at(src)]);
-        if (e < ek) wk = rescale<INT8>(wk, exp2_int(e - ek));
+#pragma unroll 1
+    for (int pair = blockIdx.x; pair < pairs; pair += gridDim.x) {
+      const int layer = pair / a.H, h = pair - layer * a.H;
+      const Planes& P = a.layer[layer];
+      auto tile_of = [&](int src) { return (static_cast<size_t>(phys_of(src)) * a.H + h) * kTile; };
+      const size_t si = static_cast<size_t>(h) * a.num_pages;
+      int e_mine = kMinExp;
+      if (mine >= 0) e_mine = f16_to_exp((lane < 16 ? P.ks : P.vs)[si + phys_of(mine)]);
+      uint4 wk = make_uint4(kZero, kZero, kZero, kZero), v[4];
+      if (sk >= 0) {
+        const int slot = sk & 15;
+        wk = *reinterpret_cast<const uint4*>(P.k + tile_of(sk) + 16 * (((((slot >> 3) << 1) | ((tid >> 5) & 1)) << 5) | ((slot & 7) << 2) | q));
       }
-    }
-    {  // value word tid: channels 32 (tid >> 5) + (tid >> 2 & 7) + {0, 8, 16, 24} of tokens 2 q, 2 q + 1, 2 q + 8, 2 q + 9
-      const int q = tid & 3;
-      uint32_t out[2] = {kZero, kZero};    // per channel half (bit 4): of channels + 0, + 8 tokens t, t + 1 ..
-      uint32_t out2[2] = {kZero, kZero};   // .. and t + 8, t + 9
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (sv[i] >= 0) v[i] = *reinterpret_cast<const uint4*>(P.v + tile_of(sv[i]) + 16 * ((tid & ~3) | ((sv[i] & 7) >> 1)));
+      int top = e_mine;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int ek = __shfl_sync(0xffffffffu, top, 0), ev = __shfl_sync(0xffffffffu, top, 16);
+      const bool grows = __any_sync(0xffffffffu, mine >= 0 && e_mine < top);  // some code is rescaled
+      const int e_k = __shfl_sync(0xffffffffu, e_mine, tk & 15);
+      if (sk >= 0 && e_k < ek) wk = rescale<INT8>(wk, exp2_int(e_k - ek));
+      uint32_t out[2] = {kZero, kZero};   // per channel half (bit 4): of channels + 0, + 8 tokens t, t + 1 ..
+      uint32_t out2[2] = {kZero, kZero};  // .. and t + 8, t + 9
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = 2 * q + (i & 1) + 8 * (i >> 1);
-        if (t >= to) continue;
-        const int src = source(t), slot = src % kPage;
-        const uint4 w = *reinterpret_cast<const uint4*>(P.v + tile_of(src) + 16 * ((tid & ~3) | ((slot & 7) >> 1)));
+        const int e_v = __shfl_sync(0xffffffffu, e_mine, 16 + 2 * q + (i & 1) + 8 * (i >> 1));
+        if (sv[i] < 0) continue;
+        const int slot = sv[i] & 15;
         // the token's bytes: words 2 h + (slot >> 3), bytes (slot & 1) and 2 + (slot & 1)
-        const uint32_t a0 = slot >> 3 ? w.y : w.x, a1 = slot >> 3 ? w.w : w.z;
-        // four codes of one token: channels + 0, + 8, + 16, + 24
-        uint32_t four = __byte_perm(a0, a1, slot & 1 ? 0x7531 : 0x6420);
-        const int e = f16_to_exp(P.vs[scale_at(src)]);
-        if (e < ev) four = rescale4<INT8>(four, exp2_int(e - ev));
+        const uint32_t a0 = slot >> 3 ? v[i].y : v[i].x, a1 = slot >> 3 ? v[i].w : v[i].z;
+        uint32_t four = __byte_perm(a0, a1, slot & 1 ? 0x7531 : 0x6420);  // its codes of channels + 0, + 8, + 16, + 24
+        if (e_v < ev) four = rescale4<INT8>(four, exp2_int(e_v - ev));
         const uint32_t keep = i & 1 ? 0x00FF00FFu : 0xFF00FF00u;  // bytes of the other token of the pair
-        const uint32_t c0 = i & 1 ? __byte_perm(four, 0, 0x1404) : __byte_perm(four, 0, 0x4140);  // channels + 0 and + 8
-        const uint32_t c1 = i & 1 ? __byte_perm(four, 0, 0x3424) : __byte_perm(four, 0, 0x4342);
+        const uint32_t c0 = __byte_perm(four, 0, i & 1 ? 0x1404 : 0x4140);  // channels + 0 and + 8
+        const uint32_t c1 = __byte_perm(four, 0, i & 1 ? 0x3424 : 0x4342);
         uint32_t* o = i >> 1 ? out2 : out;
         o[0] = (o[0] & keep) | c0;
         o[1] = (o[1] & keep) | c1;
       }
-      wv = make_uint4(out[0], out2[0], out[1], out2[1]);
-    }
-    const size_t tile = (static_cast<size_t>(s_phys[d]) * a.H + h) * kTile, si = static_cast<size_t>(h) * a.num_pages + s_phys[d];
-    __syncthreads();  // everything that goes into the page has been read
-    *reinterpret_cast<uint4*>(P.k + tile + 16 * tid) = wk;
-    *reinterpret_cast<uint4*>(P.v + tile + 16 * tid) = wv;
-    if (tid == 0) {
-      P.ks[si] = exp_to_f16(ek);
-      P.vs[si] = exp_to_f16(ev);
+      const size_t tile = (static_cast<size_t>(s_phys[d]) * a.H + h) * kTile;
+      __syncthreads();  // everything that goes into the page has been read
+      if (grows || sk != self + tk) *reinterpret_cast<uint4*>(P.k + tile + 16 * tid) = wk;
+      if (grows || !v_stays) *reinterpret_cast<uint4*>(P.v + tile + 16 * tid) = make_uint4(out[0], out2[0], out[1], out2[1]);
+      if (tid == 0) {
+        P.ks[si + s_phys[d]] = exp_to_f16(ek);
+        P.vs[si + s_phys[d]] = exp_to_f16(ev);
+      }
     }
     __syncthreads();  // later pages do not look at this one again, but a table with the same page twice would
   }
@@ -182,7 +190,10 @@ extern "C" kvq_status kvq_keep_runs(const kvq_cache* caches, int32_t n_caches, c
       const kvq_cache& c = caches[i0 + i];
       a.layer[i] = Planes{static_cast<uint8_t*>(c.k_data), static_cast<uint8_t*>(c.v_data), c.k_scale, c.v_scale};
     }
-    const dim3 grid(a.H, n, batch);
+    a.layers = n;
+    // Blocks for as many pairs at a time as the SMs hold of them (kResident each): 32 requests of 36 layers and 8 heads have 38 blocks each.
+    const int want = std::max(1, device_sm_count() * kResident / batch);
+    const dim3 grid(std::min(a.H * n, want), batch);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (caches[0].k_fmt == KVQ_FMT_INT8_PAGE) keep_kernel<true><<<grid, kThreads, 0, s>>>(a);
     else keep_kernel<false><<<grid, kThreads, 0, s>>>(a);

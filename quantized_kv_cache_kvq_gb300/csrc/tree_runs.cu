@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a, int mo
     exits[i] = up;
   }
   __syncthreads();
+  // 1 << shift lanes to a row, a word each: a chunk's 32 rows are four rounds of the block at most
+  const int shift = a.words > 16 ? 5 : a.words > 1 ? 32 - __clz(a.words - 1) : 0;
   for (int c = 0; c < chunks; ++c) {
     const int rows = min(kChunk, n - kChunk * c);
     uint32_t* mine = below + chunk_at(c);
@@ -78,17 +80,29 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a, int mo
       if (a.positions) a.positions[run.row0 + i] = run.len - n + depth[i] - 1;
     }
     int32_t* out = a.mask + static_cast<long long>(run.row0 + kChunk * c) * a.words;
-    for (int k = tid; k < rows * a.words; k += kThreads) {
-      const int r = k / a.words, w = k - r * a.words;
-      uint32_t x = 0;
-      if (w < c) {
-        const int e = exits[kChunk * c + r], ec = e / kChunk;
-        if (e >= 0 && w <= ec) x = w < ec ? below[chunk_at(ec) + (e % kChunk) * ec + w] : own[e];
-        mine[r * c + w] = x;
-      } else if (w == c) {
-        x = own[kChunk * c + r];
-      }
-      out[k] = static_cast<int32_t>(x);
+    const int step = kThreads >> shift, word = lane & ((1 << shift) - 1);
+    // at most four rows a lane, all of whose loads are issued before the first is used
+    int e[4];
+    uint32_t here[4], x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = (tid >> shift) + k * step;
+      e[k] = r < rows ? exits[kChunk * c + r] : -1;
+      here[k] = r < rows ? own[kChunk * c + r] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ec = e[k] >> 5;  // -1 for none
+      x[k] = e[k] < 0 || word > ec ? 0u : word == ec ? own[e[k]] : below[chunk_at(ec) + (e[k] & 31) * ec + word];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = (tid >> shift) + k * step;
+      if (r >= rows || word >= a.words) continue;
+      if (word < c) mine[r * c + word] = x[k];
+      int32_t* to = out + static_cast<long long>(r) * a.words;
+      to[word] = static_cast<int32_t>(word == c ? here[k] : x[k]);
+      for (int w = word + 32; w < a.words; w += 32) to[w] = 0;  // words that no run has
     }
     __syncthreads();
   }

@@ -28,8 +28,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kCluster = 8;
-constexpr int kWarps = 16;  // of a block
-constexpr int kThreads = 32 * kWarps;
+// Warps of a block.  64 registers a thread: two blocks on an SM, so that 38 requests run at once.
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kPieces = kCluster * kWarps;
 constexpr int kMaxVocab = 1 << 19;  // sums of 2^19 times 2^44 fit 64 bits
 constexpr uint32_t kAll = 0xffffffffu;
@@ -73,26 +73,34 @@ __device__ __forceinline__ float value_at(const void* p, long long i) {
 template <bool BF16>
 constexpr int kVecOf = BF16 ? 8 : 4;  // elements of 16 bytes
 
-// Elements i .. of a row of n elements; `fill` outside.  One load where the 16 bytes are aligned and all inside.
+// 16 bytes of a row of n elements from element i on, zeros outside.  One load where they are aligned and all inside.
 template <bool BF16>
-__device__ __forceinline__ void load_vec(const uint8_t* row, int i, int n, float (&x)[kVecOf<BF16>], float fill) {
+__device__ __forceinline__ uint4 load_vec(const uint8_t* row, int i, int n) {
   constexpr int kSize = BF16 ? 2 : 4, kVec = kVecOf<BF16>;
   const uint8_t* p = row + static_cast<long long>(i) * kSize;
-  if (i >= 0 && i + kVec <= n && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  if (i >= 0 && i + kVec <= n && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) return *reinterpret_cast<const uint4*>(p);
+  uint32_t u[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (BF16) {
-        x[(2 * e) % kVec] = __uint_as_float(u[e] << 16);
-        x[(2 * e + 1) % kVec] = __uint_as_float(u[e] & 0xFFFF0000u);
-      } else {
-        x[e] = __uint_as_float(u[e]);
-      }
+  for (int e = 0; e < 4; ++e) {
+    auto bits = [&](int j) -> uint32_t {
+      if (j < 0 || j >= n) return 0u;
+      return BF16 ? reinterpret_cast<const uint16_t*>(row)[j] : reinterpret_cast<const uint32_t*>(row)[j];
+    };
+    u[e] = BF16 ? bits(i + 2 * e) | bits(i + 2 * e + 1) << 16 : bits(i + e);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack(uint4 w, float (&x)[kVecOf<BF16>]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (BF16) {
+      x[(2 * e) % kVecOf<BF16>] = __uint_as_float(u[e] << 16);
+      x[(2 * e + 1) % kVecOf<BF16>] = __uint_as_float(u[e] & 0xFFFF0000u);
+    } else {
+      x[e] = __uint_as_float(u[e]);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) x[e] = i + e >= 0 && i + e < n ? value_at<BF16>(row, i + e) : fill;
   }
 }
 // Elements by which a row begins behind a 16-byte boundary.
@@ -113,6 +121,22 @@ __device__ __forceinline__ unsigned long long whole(float x) {
   const unsigned long long m = static_cast<unsigned long long>(b & 0x7FFFFFu | 0x800000u) << 21;
   return e == 0 ? 0 : m >> min(127u - e, 63u);
 }
+// The same of many values at once, in 32-bit sums of two parts.  x + 2 is x rounded to a multiple of 2^-22 (values in [2, 4) have that step), what
+// it leaves is exact, and times 2^44 it is below 2^22 in magnitude, so that adding 1.5 2^23, rounded down, is its floor.  Up to 2^9 values.
+struct Whole {
+  uint32_t high = 0, low = 0, n = 0;
+  __device__ __forceinline__ void add(float x) {
+    const float t = __fadd_rn(x, 2.f), left = __fsub_rn(x, __fsub_rn(t, 2.f));
+    high += __float_as_uint(t);
+    low += __float_as_uint(__fmaf_rd(left, 0x1p44f, 12582912.f));
+    ++n;
+  }
+  __device__ __forceinline__ unsigned long long sum() const {
+    const uint32_t h = high - n * 0x40000000u;
+    const int32_t l = static_cast<int32_t>(low - n * 0x4B400000u);
+    return (static_cast<unsigned long long>(h) << 22) + static_cast<long long>(l);
+  }
+};
 __device__ __forceinline__ float rest(float p, float q, float c) { return fmaxf(__fsub_rn(p, __fmul_rn(c, q)), 0.f); }
 
 // Scores in the order of their values as unsigned numbers: NaN lowest, -0 as 0.
@@ -130,91 +154,153 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
   return v;
 }
 
+// A hint to the L2 to bring a warp's piece of a row that a refusal would need.
+template <bool BF16>
+__device__ __forceinline__ void bring(const uint8_t* row, int vocab, int piece) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row), bytes = static_cast<uintptr_t>(vocab) * (BF16 ? 2 : 4);
+  const uintptr_t from = (at + bytes * piece / kPieces + 15) & ~static_cast<uintptr_t>(15), to = (at + bytes * (piece + 1) / kPieces) & ~static_cast<uintptr_t>(15);
+  if (from < to) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(static_cast<uint32_t>(to - from)) : "memory");
+}
+
 enum class Pass { kGreedy, kTarget, kRest };
 
-// A warp's piece of a row: the sum of whole(p), of whole(rest(p, q, c)), or the largest (score, ~index).
+// A warp's piece of a row: the sum of whole(p), of whole(rest(p, q, c)), or the largest (score, ~index).  kAtOnce loads of a row are on their way
+// together.
+constexpr int kAtOnce = 4;
 template <bool BF16, Pass PASS>
 __device__ __forceinline__ unsigned long long pass_over(const uint8_t* p, const uint8_t* q, float c, int vocab, int piece, int& bad) {
   constexpr int kVec = kVecOf<BF16>;
   const int lane = threadIdx.x & 31, off = phase_of<BF16>(p);
   const int n = (vocab + off + kVec - 1) / kVec;
   const int v0 = n * piece / kPieces, v1 = n * (piece + 1) / kPieces;
-  unsigned long long sum = 0;
-#pragma unroll 4
-  for (int v = v0 + lane; v < v1; v += 32) {
-    const int i = v * kVec - off;
-    float x[kVec], y[kVec];
-    load_vec<BF16>(p, i, vocab, x, PASS == Pass::kGreedy ? -INFINITY : 0.f);
-    if (PASS == Pass::kRest) load_vec<BF16>(q, i, vocab, y, 0.f);
+  unsigned long long best = 0;
+  Whole sum;
+  uint32_t top = 0;  // largest value as bits: above 1.0's, one of them is no probability
+#pragma unroll 1
+  for (int v = v0 + lane; v - lane < v1; v += 32 * kAtOnce) {
+    uint4 x[kAtOnce], y[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      if (PASS == Pass::kGreedy) {
-        const unsigned long long key = static_cast<unsigned long long>(ordered(x[e], bad)) << 32 | static_cast<uint32_t>(~(i + e));
-        if (i + e >= 0 && i + e < vocab && key > sum) sum = key;
-      } else if (PASS == Pass::kTarget) {
-        sum += whole(probability(x[e], bad));
-      } else {
-        sum += whole(rest(probability(x[e], bad), probability(y[e], bad), c));
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = v + 32 * k < v1 ? (v + 32 * k) * kVec - off : vocab;
+      x[k] = load_vec<BF16>(p, i, vocab);
+      if (PASS == Pass::kRest) y[k] = load_vec<BF16>(q, i, vocab);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (v - lane + 32 * k >= v1) break;  // no lane has one
+      const int i = v + 32 * k < v1 ? (v + 32 * k) * kVec - off : vocab;
+      float a[kVec], b[kVec];
+      unpack<BF16>(x[k], a);
+      if (PASS == Pass::kRest) unpack<BF16>(y[k], b);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        if (PASS == Pass::kGreedy) {
+          const bool in = i + e >= 0 && i + e < vocab;
+          const unsigned long long key = static_cast<unsigned long long>(ordered(a[e], bad)) << 32 | static_cast<uint32_t>(~(i + e));
+          if (in && key > best) best = key;
+        } else {
+          top = max(top, __float_as_uint(a[e]));
+          if (PASS == Pass::kRest) top = max(top, __float_as_uint(b[e]));
+          sum.add(PASS == Pass::kRest ? rest(a[e], b[e], c) : a[e]);
+        }
       }
     }
   }
-  if (PASS != Pass::kGreedy) return warp_sum(sum);
+  if (PASS == Pass::kGreedy) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const unsigned long long other = __shfl_xor_sync(kAll, sum, o);
-    if (other > sum) sum = other;
+    for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(kAll, best, o));
+    return best;
   }
-  return sum;
+  unsigned long long total = sum.sum();
+  if (top > 0x3F800000u) {  // value by value
+    total = 0;
+    for (int v = v0 + lane; v < v1; v += 32) {
+      float a[kVec], b[kVec] = {};
+      unpack<BF16>(load_vec<BF16>(p, v * kVec - off, vocab), a);
+      if (PASS == Pass::kRest) unpack<BF16>(load_vec<BF16>(q, v * kVec - off, vocab), b);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const float pe = probability(a[e], bad);
+        total += whole(PASS == Pass::kRest ? rest(pe, probability(b[e], bad), c) : pe);
+      }
+    }
+  }
+  return warp_sum(total);
 }
 
 // The token of a piece at which the sum over the piece first exceeds t (t is less than the piece's sum).
 template <bool BF16, bool REST>
 __device__ __forceinline__ int token_at(const uint8_t* p, const uint8_t* q, float c, int vocab, int piece, unsigned long long t) {
-  constexpr int kVec = kVecOf<BF16>;
+  constexpr int kVec = kVecOf<BF16>, kSteps = 4;  // steps of 32 vectors whose loads are on their way together
   const int lane = threadIdx.x & 31, off = phase_of<BF16>(p);
   const int n = (vocab + off + kVec - 1) / kVec;
   const int v0 = n * piece / kPieces, v1 = n * (piece + 1) / kPieces;
   int bad = 0;
-  for (int b = v0; b < v1; b += 32) {
-    const int i = (b + lane) * kVec - off;
-    float x[kVec] = {}, y[kVec] = {};
-    if (b + lane < v1) {
-      load_vec<BF16>(p, i, vocab, x, 0.f);
-      if (REST) load_vec<BF16>(q, i, vocab, y, 0.f);
-    }
-    unsigned long long w[kVec], mine = 0;
+  auto weight = [&](float x, float y) {
+    const float pe = probability(x, bad);
+    return whole(REST ? rest(pe, probability(y, bad), c) : pe);
+  };
+#pragma unroll 1
+  for (int b = v0; b < v1; b += 32 * kSteps) {
+    uint4 x[kSteps], y[kSteps];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const float pe = probability(x[e], bad);
-      mine += w[e] = whole(REST ? rest(pe, probability(y[e], bad), c) : pe);
+    for (int k = 0; k < kSteps; ++k) {
+      const int v = b + 32 * k + lane, i = v < v1 ? v * kVec - off : vocab;
+      x[k] = load_vec<BF16>(p, i, vocab);
+      y[k] = REST ? load_vec<BF16>(q, i, vocab) : make_uint4(0, 0, 0, 0);
     }
-    unsigned long long inc = mine;
+    unsigned long long mine[kSteps], all[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      float u[kVec], w[kVec];
+      unpack<BF16>(x[k], u);
+      unpack<BF16>(y[k], w);
+      mine[k] = 0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) mine[k] += weight(u[e], w[e]);
+    }
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) all[k] = warp_sum(mine[k]);
+    int step = -1;
+    uint4 px = make_uint4(0, 0, 0, 0), py = px;
+    unsigned long long sum = 0;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      if (step >= 0) continue;
+      if (t < all[k]) {
+        step = k;
+        px = x[k];
+        py = y[k];
+        sum = mine[k];
+      } else {
+        t -= all[k];
+      }
+    }
+    if (step < 0) continue;
+    unsigned long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned long long up = __shfl_up_sync(kAll, inc, o);
       if (lane >= o) inc += up;
     }
-    const unsigned hit = __ballot_sync(kAll, inc > t);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      unsigned long long before = inc - mine;
-      int tok = 0;
+    const int l = __ffs(__ballot_sync(kAll, inc > t)) - 1;
+    float u[kVec], w[kVec];
+    unpack<BF16>(px, u);
+    unpack<BF16>(py, w);
+    unsigned long long cum = inc - sum;
+    int tok = -1;
 #pragma unroll
-      for (int e = kVec - 1; e >= 0; --e) {  // the first e with before + w[0] + .. + w[e] > t
-        unsigned long long s = before;
-#pragma unroll
-        for (int f = 0; f <= e; ++f) s += w[f];
-        if (s > t) tok = i + e;
-      }
-      return __shfl_sync(kAll, tok, l);
+    for (int e = 0; e < kVec; ++e) {  // the first e at which the sum exceeds t
+      cum += weight(u[e], w[e]);
+      if (tok < 0 && cum > t) tok = (b + 32 * step + lane) * kVec - off + e;
     }
-    t -= __shfl_sync(kAll, inc, 31);
+    return __shfl_sync(kAll, tok, l);
   }
   return 0;  // cannot be, unless the row changed under the call
 }
 
 template <bool BF16>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -250,7 +336,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
   }
   cluster.sync();
   const int row0 = sh.run[0], n = sh.run[1];
-  const bool writer = rank == 0 && tid == 0;
+  const bool writer = rank == 0 && tid == 0, asks = rank == 0 && warp == 0;
   if (n == 0) {
     if (writer) {
       a.kept[s] = 0;
@@ -272,26 +358,35 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
     }
     return n;
   };
-  // the numbers that decide about a child, and the row's own
+  // The numbers that decide about a child, and the row's own: loaded before a pass, looked at (`taken`) behind it, so that nothing waits for them.
   auto ask = [&](int cur, int child) {
     Ask k{0.f, 0.f, 0.f, 0.f};
     k.draw = a.uniform[2 * (static_cast<long long>(row0) + cur) + 1];
     if (child < n) {
       const int tok = sh.token[child];
       k.u = a.uniform[2 * (static_cast<long long>(row0) + child)];
-      if (!(k.u >= 0.f && k.u < 1.f)) report(a.err, KVQ_ERR_RANGE);
       if (tok >= 0 && tok < a.vocab) {
         const long long row = row0 + cur;
-        k.p = probability(value_at<BF16>(a.target, row * a.target_stride + tok), bad);
-        k.q = probability(value_at<BF16>(a.draft, row * a.draft_stride + tok), bad);
+        k.p = value_at<BF16>(a.target, row * a.target_stride + tok);
+        k.q = value_at<BF16>(a.draft, row * a.draft_stride + tok);
       }
     }
     return k;
   };
+  auto taken = [&](Ask k) {
+    if (asks) {
+      if (!(k.u >= 0.f && k.u < 1.f)) report(a.err, KVQ_ERR_RANGE);
+      k.p = probability(k.p, bad);
+      k.q = probability(k.q, bad);
+    }
+    return k;
+  };
   // a warp's sum, and beside it what is asked, to all blocks; the sums of all warps are in sh.part[turn ^ 1] afterwards
-  auto exchange = [&](unsigned long long v, const Ask* k) {
+  auto exchange = [&](unsigned long long v, const Ask* raw) {
+    Ask k{};
+    if (raw) k = taken(*raw);
     if (lane < kCluster) cluster.map_shared_rank(&sh, lane)->part[turn][piece] = v;
-    if (k && rank == 0 && warp == 0 && lane < kCluster) cluster.map_shared_rank(&sh, lane)->ask[turn] = *k;
+    if (raw && asks && lane < kCluster) cluster.map_shared_rank(&sh, lane)->ask[turn] = k;
     cluster.sync();
     turn ^= 1;
   };
@@ -319,7 +414,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
     } else {
       int child = drafts ? next_child(cur, 0) : n;
       Ask k{};
-      if (rank == 0 && warp == 0) k = ask(cur, child);
+      if (asks) k = ask(cur, child);
+      if (child < n && lane == 0) bring<BF16>(q, a.vocab, piece);
       exchange(pass_over<BF16, Pass::kTarget>(p, q, 0.f, a.vocab, piece, bad), &k);
       const unsigned long long* part = sh.part[turn ^ 1];
       unsigned long long z = total(part);
@@ -336,7 +432,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) ver
           }
           c = static_cast<float>(__dadd_rn(static_cast<double>(c), zd));
           child = next_child(cur, child);
-          if (rank == 0 && warp == 0) k = ask(cur, child);
+          if (asks) k = ask(cur, child);
           exchange(pass_over<BF16, Pass::kRest>(p, q, c, a.vocab, piece, bad), &k);
           part = sh.part[turn ^ 1];
           z = total(part);
