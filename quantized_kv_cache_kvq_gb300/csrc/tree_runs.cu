@@ -3,7 +3,8 @@
 // mask(i) = mask(parent(i)) | bit i, depth(i) = depth(parent(i)) + 1.  One block a request.  Rows are taken 32 at a time (a chunk, whose
 // bits are one word): inside a chunk a warp finds every row's ancestors by pointer doubling in registers, five rounds whatever the shape, and
 // the row's first ancestor before the chunk; the words of that ancestor, complete when the chunk's turn comes, are the row's other words.  So
-// a chain of 1024 tokens is 32 dependent steps, not 1024.  Only words below the diagonal are kept in shared memory (62 KB for 1024 rows).
+// a chain of 1024 tokens is 32 dependent steps, not 1024.  Shared memory keeps the rows' words up to their own, in 16-byte pieces (74 KB for 1024
+// rows); a thread takes such a piece of a row.  Bound by the bytes written where rows are long, by the latency of its steps where they are few.
 #include <algorithm>
 
 #include "runs.cuh"
@@ -25,10 +26,11 @@ struct TreeArgs {
   int32_t* err;
 };
 
-// First word of a chunk's rows in shared memory: 32 rows of as many words as there are chunks before.
-__host__ __device__ constexpr int chunk_at(int c) { return kChunk * (c * (c - 1) / 2); }
-// Rows of a run, rounded up to whole chunks; their own words, exits and depths, and the words below the diagonal.
-__host__ __device__ constexpr size_t tree_smem(int chunks) { return (3 * kChunk * chunks + chunk_at(chunks)) * sizeof(int32_t); }
+// Pieces of four words that a row of chunk c keeps, and the first of the chunk's 32 rows: the chunks 4 i .. 4 i + 3 before have i + 1 each.
+__host__ __device__ constexpr int row_pieces(int c) { return (c >> 2) + 1; }
+__host__ __device__ constexpr int chunk_at(int c) { return kChunk * (2 * (c >> 2) * ((c >> 2) + 1) + (c & 3) * row_pieces(c)); }
+// Rows of a run, rounded up to whole chunks: their own words, exits and depths, and their pieces.
+__host__ __device__ constexpr size_t tree_smem(int chunks) { return 3 * kChunk * chunks * sizeof(int32_t) + chunk_at(chunks) * sizeof(uint4); }
 
 __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a, int most) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -42,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a, int mo
   uint32_t* own = reinterpret_cast<uint32_t*>(smem);              // [rows] ancestors inside the chunk, and the row itself
   int* exits = reinterpret_cast<int*>(own + kChunk * chunks);     // [rows] first ancestor before the chunk, -1 for none
   int* depth = exits + kChunk * chunks;                           // [rows]
-  uint32_t* below = reinterpret_cast<uint32_t*>(depth + kChunk * chunks);
+  uint4* kept = reinterpret_cast<uint4*>(depth + kChunk * chunks);
   for (int c = warp; c < chunks; c += kThreads / 32) {
     const int i = kChunk * c + lane;
     int up = -1;
@@ -69,40 +71,39 @@ __global__ void __launch_bounds__(kThreads) tree_kernel(const TreeArgs a, int mo
     exits[i] = up;
   }
   __syncthreads();
-  // 1 << shift lanes to a row, a word each: a chunk's 32 rows are four rounds of the block at most
-  const int shift = a.words > 16 ? 5 : a.words > 1 ? 32 - __clz(a.words - 1) : 0;
+  // 1 << shift threads to a row, four words each: a chunk's rows are one round of the block
+  const int quads = (min(a.words, kChunk) + 3) >> 2, shift = quads > 1 ? 32 - __clz(quads - 1) : 0;
+  const int r = tid >> shift, quad = tid & ((1 << shift) - 1);
+  const bool whole = (a.words & 3) == 0 && (reinterpret_cast<uintptr_t>(a.mask) & 15u) == 0;  // pieces of the mask are 16-byte words
   for (int c = 0; c < chunks; ++c) {
     const int rows = min(kChunk, n - kChunk * c);
-    uint32_t* mine = below + chunk_at(c);
     if (tid < rows) {
       const int i = kChunk * c + tid, e = exits[i];
       depth[i] = __popc(own[i]) + (e >= 0 ? depth[e] : 0);
       if (a.positions) a.positions[run.row0 + i] = run.len - n + depth[i] - 1;
     }
-    int32_t* out = a.mask + static_cast<long long>(run.row0 + kChunk * c) * a.words;
-    const int step = kThreads >> shift, word = lane & ((1 << shift) - 1);
-    // at most four rows a lane, all of whose loads are issued before the first is used
-    int e[4];
-    uint32_t here[4], x[4];
+    if (r < rows && quad < quads) {
+      const int e = exits[kChunk * c + r], ec = e >> 5;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (e >= 0 && quad < row_pieces(ec)) x = kept[chunk_at(ec) + (e & 31) * row_pieces(ec) + quad];
+      if (quad == c >> 2) {
+        const uint32_t here = own[kChunk * c + r];
+        if ((c & 3) == 0) x.x = here;
+        if ((c & 3) == 1) x.y = here;
+        if ((c & 3) == 2) x.z = here;
+        if ((c & 3) == 3) x.w = here;
+      }
+      if (quad < row_pieces(c)) kept[chunk_at(c) + r * row_pieces(c) + quad] = x;
+      int32_t* out = a.mask + static_cast<long long>(run.row0 + kChunk * c + r) * a.words;
+      if (whole) {
+        *reinterpret_cast<uint4*>(out + 4 * quad) = x;
+      } else {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = (tid >> shift) + k * step;
-      e[k] = r < rows ? exits[kChunk * c + r] : -1;
-      here[k] = r < rows ? own[kChunk * c + r] : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int ec = e[k] >> 5;  // -1 for none
-      x[k] = e[k] < 0 || word > ec ? 0u : word == ec ? own[e[k]] : below[chunk_at(ec) + (e[k] & 31) * ec + word];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = (tid >> shift) + k * step;
-      if (r >= rows || word >= a.words) continue;
-      if (word < c) mine[r * c + word] = x[k];
-      int32_t* to = out + static_cast<long long>(r) * a.words;
-      to[word] = static_cast<int32_t>(word == c ? here[k] : x[k]);
-      for (int w = word + 32; w < a.words; w += 32) to[w] = 0;  // words that no run has
+        for (int i = 0; i < 4; ++i)
+          if (4 * quad + i < a.words) out[4 * quad + i] = static_cast<int32_t>(w[i]);
+      }
+      for (int w = kChunk + quad; w < a.words; w += quads) out[w] = 0;  // words that no run has
     }
     __syncthreads();
   }

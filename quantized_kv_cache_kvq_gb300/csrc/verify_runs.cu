@@ -11,14 +11,15 @@
 // hundred would find another token).
 //
 // A cluster of eight blocks has a request and walks its tree: only the rows of the path are read.  A row is cut into one piece for each warp;
-// after every pass the warps write their sums to all blocks, one cluster barrier, and all blocks take the same decision.  What decides is
+// after every pass the warps send their sums to all blocks, whose mbarriers count the bytes, and all blocks take the same decision.  What decides is
 // read by the first block alone and handed to the others (the tree at the start, a child's numbers beside the sums), so that blocks take
-// the same number of barriers whatever another stream does to the inputs.
+// the same number of exchanges whatever another stream does to the inputs.  (A cluster barrier for each exchange instead: ...)
 #include <cooperative_groups.h>
 
 #include <algorithm>
 #include <cmath>
 
+#include "decode_kernel.cuh"
 #include "runs.cuh"
 
 namespace kvq {
@@ -59,11 +60,11 @@ struct Ask {
 };
 struct Shared {
   int32_t parent[KVQ_MAX_TREE], token[KVQ_MAX_TREE];
-  unsigned long long part[2][kPieces];  // sums of a pass (two in turn), or its largest keys
-  unsigned long long first[kPieces];    // those of p itself
-  Ask ask[2];
+  // Sums of a pass, its largest keys, or the token drawn + 1, of all warps: two in turn, and two for the passes over p itself, of rows in turn.
+  unsigned long long part[4][kPieces];
+  unsigned long long ask[2][2];  // an Ask
+  uint64_t bar[2];               // of the exchanges in turn
   int run[4];   // row0, n, len, whether there is a run
-  int found[2];  // drawn token
 };
 
 template <bool BF16>
@@ -148,11 +149,31 @@ __device__ __forceinline__ uint32_t ordered(float x, int& bad) {
   const uint32_t b = __float_as_uint(x + 0.f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+// Of values below 2^63: three parts of 22 bits, whose sums fit 32.
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
+  const uint32_t a = __reduce_add_sync(kAll, static_cast<uint32_t>(v) & 0x3FFFFFu);
+  const uint32_t b = __reduce_add_sync(kAll, static_cast<uint32_t>(v >> 22) & 0x3FFFFFu);
+  const uint32_t c = __reduce_add_sync(kAll, static_cast<uint32_t>(v >> 44));
+  return a + (static_cast<unsigned long long>(b) << 22) + (static_cast<unsigned long long>(c) << 44);
 }
+
+// What a block tells the others goes straight into their shared memory and counts there as bytes of an mbarrier's phase.
+__device__ __forceinline__ uint32_t at_rank(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(dec::smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void send(uint32_t to, unsigned long long v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(to), "l"(v), "r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(dec::smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+constexpr long long kWaitClocks = 4000000000ll;  // some seconds: a wait that lasts longer gives up
 
 // A hint to the L2 to bring a warp's piece of a row that a refusal would need.
 template <bool BF16>
@@ -305,7 +326,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x / kCluster, piece = rank * kWarps + warp;
-  cluster.sync();  // every block runs before another one writes to it
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) dec::mbar_init(&sh.bar[i], 1);
+    dec::fence_mbar_init();
+  }
+  cluster.sync();  // every block runs, and has its barriers, before another one writes to it
   if (rank == 0) {  // the run and its tree, to all blocks
     __shared__ int run[4];
     if (tid == 0) {
@@ -346,7 +371,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
     return;
   }
   const bool greedy = a.uniform == nullptr, drafts = a.draft != nullptr;
-  int turn = 0;  // which of the two exchanges
   int bad = 0;
   constexpr int kSize = BF16 ? 2 : 4;
   // the first child of `cur` behind row `j`, n for none
@@ -381,14 +405,35 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
     }
     return k;
   };
-  // a warp's sum, and beside it what is asked, to all blocks; the sums of all warps are in sh.part[turn ^ 1] afterwards
-  auto exchange = [&](unsigned long long v, const Ask* raw) {
-    Ask k{};
-    if (raw) k = taken(*raw);
-    if (lane < kCluster) cluster.map_shared_rank(&sh, lane)->part[turn][piece] = v;
-    if (raw && asks && lane < kCluster) cluster.map_shared_rank(&sh, lane)->ask[turn] = k;
-    cluster.sync();
-    turn ^= 1;
+  // A warp's number, and beside it what is asked, to all blocks; those of all warps are in sh.part[buf] afterwards.  A block sends for an exchange when
+  // it has all of the last one's, so the barriers and buffers of two exchanges in turn are never written while they are still in use.
+  uint32_t turn = 0;
+  bool alive = true;
+  Ask asked{};
+  auto exchange = [&](unsigned long long v, int buf, const Ask& raw) {
+    uint64_t* bar = &sh.bar[turn & 1];
+    if (tid == 0) {  // 8 bytes of every warp, 16 that are asked
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(dec::smem_u32(bar)), "r"(kPieces * 8 + 16) : "memory");
+    }
+    const Ask k = taken(raw);
+    if (lane < kCluster) {
+      const uint32_t there = at_rank(bar, lane);
+      send(at_rank(&sh.part[buf][piece], lane), v, there);
+      if (asks) {
+        auto pair = [](float a, float b) { return static_cast<unsigned long long>(__float_as_uint(b)) << 32 | __float_as_uint(a); };
+        send(at_rank(&sh.ask[turn & 1][0], lane), pair(k.u, k.p), there);
+        send(at_rank(&sh.ask[turn & 1][1], lane), pair(k.q, k.draw), there);
+      }
+    }
+    if (alive && !try_wait_cluster(bar, (turn >> 1) & 1u)) {
+      const long long t0 = clock64();
+      while (alive && !try_wait_cluster(bar, (turn >> 1) & 1u)) alive = clock64() - t0 <= kWaitClocks;
+    }
+    alive = __all_sync(kAll, alive);
+    const unsigned long long a0 = sh.ask[turn & 1][0], a1 = sh.ask[turn & 1][1];
+    asked = Ask{__uint_as_float(static_cast<uint32_t>(a0)), __uint_as_float(static_cast<uint32_t>(a0 >> 32)), __uint_as_float(static_cast<uint32_t>(a1)),
+                __uint_as_float(static_cast<uint32_t>(a1 >> 32))};
+    ++turn;
   };
   auto total = [&](const unsigned long long* part) {
     unsigned long long v = 0;
@@ -398,16 +443,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
   };
   int cur = 0, kept = 1, last = -1;
   if (writer) a.keep[row0] = 0;
-  for (int step = 0; step < n; ++step) {  // a path has at most n rows
+  for (int step = 0; step < n && alive; ++step) {  // a path has at most n rows
     const long long row = row0 + cur;
     const uint8_t* p = static_cast<const uint8_t*>(a.target) + row * a.target_stride * kSize;
     const uint8_t* q = drafts ? static_cast<const uint8_t*>(a.draft) + row * a.draft_stride * kSize : nullptr;
     int go = n, drawn = -1;
     if (greedy) {
-      exchange(pass_over<BF16, Pass::kGreedy>(p, q, 0.f, a.vocab, piece, bad), nullptr);
+      const int buf = 2 + (step & 1);
+      exchange(pass_over<BF16, Pass::kGreedy>(p, q, 0.f, a.vocab, piece, bad), buf, Ask{});
       unsigned long long best = 0;
 #pragma unroll
-      for (int i = 0; i < kPieces / 32; ++i) best = max(best, sh.part[turn ^ 1][32 * i + lane]);
+      for (int i = 0; i < kPieces / 32; ++i) best = max(best, sh.part[buf][32 * i + lane]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(kAll, best, o));
       drawn = static_cast<int>(~static_cast<uint32_t>(best));
@@ -416,15 +462,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
       Ask k{};
       if (asks) k = ask(cur, child);
       if (child < n && lane == 0) bring<BF16>(q, a.vocab, piece);
-      exchange(pass_over<BF16, Pass::kTarget>(p, q, 0.f, a.vocab, piece, bad), &k);
-      const unsigned long long* part = sh.part[turn ^ 1];
+      const unsigned long long* const first = sh.part[2 + (step & 1)];
+      exchange(pass_over<BF16, Pass::kTarget>(p, q, 0.f, a.vocab, piece, bad), 2 + (step & 1), k);
+      const unsigned long long* part = first;
       unsigned long long z = total(part);
       const unsigned long long z0 = z;
       float c = 0.f;
       if (child < n) {
-        for (int i = tid; i < kPieces; i += kThreads) sh.first[i] = part[i];
-        while (child < n) {
-          k = sh.ask[turn ^ 1];
+        while (child < n && alive) {
+          k = asked;
           const double zd = static_cast<double>(z) * 0x1p-44, cq = static_cast<double>(c) * static_cast<double>(k.q);
           if (__dmul_rn(static_cast<double>(k.u) * static_cast<double>(k.q), zd) < __dsub_rn(static_cast<double>(k.p), cq)) {
             go = child;
@@ -433,17 +479,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
           c = static_cast<float>(__dadd_rn(static_cast<double>(c), zd));
           child = next_child(cur, child);
           if (asks) k = ask(cur, child);
-          exchange(pass_over<BF16, Pass::kRest>(p, q, c, a.vocab, piece, bad), &k);
-          part = sh.part[turn ^ 1];
+          const int buf = turn & 1;
+          exchange(pass_over<BF16, Pass::kRest>(p, q, c, a.vocab, piece, bad), buf, k);
+          part = sh.part[buf];
           z = total(part);
         }
-        __syncthreads();  // sh.first
       }
       if (go == n) {  // draw
-        float u = sh.ask[turn ^ 1].draw;
+        const float u = asked.draw;
         if (writer && !(u >= 0.f && u < 1.f)) report(a.err, KVQ_ERR_RANGE);
         if (z == 0 && c != 0.f) {
-          part = sh.first;
+          part = first;
           z = z0;
           c = 0.f;
         }
@@ -471,14 +517,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
             }
             before += __shfl_sync(kAll, inc, 31);
           }
-          if (which == piece) {
-            const int tok = c != 0.f ? token_at<BF16, true>(p, q, c, a.vocab, piece, min(t, z - 1) - mine)
-                                     : token_at<BF16, false>(p, q, c, a.vocab, piece, min(t, z - 1) - mine);
-            if (lane < kCluster) cluster.map_shared_rank(&sh, lane)->found[turn] = tok;
-          }
-          cluster.sync();
-          drawn = sh.found[turn];
-          turn ^= 1;
+          unsigned long long tok = 0;
+          if (which == piece)
+            tok = 1 + (c != 0.f ? token_at<BF16, true>(p, q, c, a.vocab, piece, min(t, z - 1) - mine)
+                                : token_at<BF16, false>(p, q, c, a.vocab, piece, min(t, z - 1) - mine));
+          const int buf = turn & 1;
+          exchange(tok, buf, Ask{});
+          drawn = static_cast<int>(total(sh.part[buf])) - 1;
         }
       }
     }
@@ -486,6 +531,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
       go = cur;
       do go = next_child(cur, go); while (go < n && sh.token[go] != drawn);
     }
+    if (!alive) break;
     if (go >= n) {
       last = drawn;
       break;
@@ -494,8 +540,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2) 
     ++kept;
     cur = go;
   }
+  if (!alive) report(a.err, KVQ_ERR_TIMEOUT);
   if (bad) report(a.err, bad & 2 ? KVQ_ERR_NONFINITE_INPUT : KVQ_ERR_RANGE);
   if (rank == 0) {
+    __syncthreads();
     for (int i = kept + tid; i < n; i += kThreads) a.keep[row0 + i] = -1;
     if (tid == 0) {
       a.kept[s] = kept;
