@@ -641,12 +641,6 @@ def tree_runs(parents: torch.Tensor, seq_lens: torch.Tensor, mask: torch.Tensor,
             seq_lens.data_ptr(), mask.data_ptr(), words, _ptr(positions), _ptr(err))
 
 
-def _dense_rows(x: torch.Tensor, heads_of: str) -> int:
-    """Row stride of [rows, heads, 128] whose rows are dense."""
-    assert x.dim() == 3 and x.shape[2] == HEAD_DIM, f"{heads_of}: [rows, heads, 128]"
-    return _rows(x, x.shape[0], x.shape[1])
-
-
 def _f32(device: int, n: int, t):
     assert t is None or (t.dtype is torch.float32 and t.is_contiguous() and t.numel() == n and t.get_device() == device), \
         f"{n} fp32, contiguous and on one CUDA device"
@@ -660,26 +654,30 @@ def rope_runs(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.T
     where q_weight / k_weight [128] (fp32) are given, and rotated to positions [rows] with the table ``cos_sin`` of append_rope.  In place
     unless q_out / k_out are given.  run_starts [B + 1]: rows behind the last run are left as they are."""
     one = q if q is not None else k
-    device, rows = one.get_device(), one.shape[0]
-    assert q is None or k is None or (q.dtype == k.dtype and k.shape[0] == rows)
-    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    device, rows, dtype = one.get_device(), one.shape[0], one.dtype
     args = []
-    for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+    for x, y in ((q, q_out), (k, k_out)):
         if x is None:
             assert y is None
             args.append((None, 0, 0, None, 0))
             continue
-        assert y.shape == x.shape and y.dtype == x.dtype
-        _on(device, x, y)
-        args.append((x.data_ptr(), _dense_rows(x, what), x.shape[1], y.data_ptr(), _dense_rows(y, what)))
+        n, heads, d = x.shape
+        assert n == rows and d == HEAD_DIM and x.dtype is dtype and x.get_device() == device
+        stride = _rows(x, n, heads)
+        if y is None:
+            args.append((x.data_ptr(), stride, heads, x.data_ptr(), stride))
+        else:
+            assert y.shape == x.shape and y.dtype is dtype and y.get_device() == device
+            args.append((x.data_ptr(), stride, heads, y.data_ptr(), _rows(y, n, heads)))
     (qp, qs, hq, qo, qos), (kp, ks, hk, ko, kos) = args
     _i32(device, positions, run_starts, err)
-    assert positions.numel() == rows and cos_sin.dim() == 2 and cos_sin.shape[1] == HEAD_DIM
-    _f32(device, cos_sin.numel(), cos_sin)
+    table = cos_sin.shape
+    assert positions.numel() == rows and len(table) == 2 and table[1] == HEAD_DIM
+    _f32(device, table[0] * HEAD_DIM, cos_sin)
     _f32(device, HEAD_DIM, q_weight)
     _f32(device, HEAD_DIM, k_weight)
-    _launch("kvq_rope_runs", lib().kvq_rope_runs, device, stream, qp, qs, hq, kp, ks, hk, DTYPE[one.dtype], _ptr(q_weight),
-            _ptr(k_weight), eps, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], qo, qos, ko, kos, _ptr(run_starts),
+    _launch("kvq_rope_runs", lib().kvq_rope_runs, device, stream, qp, qs, hq, kp, ks, hk, DTYPE[dtype], _ptr(q_weight),
+            _ptr(k_weight), eps, positions.data_ptr(), cos_sin.data_ptr(), table[0], qo, qos, ko, kos, _ptr(run_starts),
             0 if run_starts is None else run_starts.numel() - 1, rows, _ptr(err))
 
 

@@ -294,6 +294,87 @@ __device__ void mma_role(Tail* t, uint32_t smem_base, uint32_t tmem, uint32_t le
 }
 
 // ------------------------------------------------------------------------------------------------ softmax
+// Two threads have a row: one the keys 0..63 of a tile and the output's channels 0..63, its peer (8 warps on) the others.
+// Each goes over its columns of S in TMEM twice, the maximum, then the weights, 32 columns (pages 2 i and 2 i + 1, in groups
+// of four columns) at a time.  y = x log2 e + ev = S k + ev; since k >= 0 a page's largest S gives its largest y.  Keys that
+// the row does not see (token >= seen of the tile) have -inf, whatever S holds there.
+__device__ __forceinline__ float row_max(uint32_t ts, const float2* scale, float rk) {
+  float tm = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    float s[32];
+    tmem_ld32(ts + 32 * i, s);
+    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
+    wait_ld();
+    loaded<32>(s);
+    float pm[2];
+#pragma unroll
+    for (int par = 0; par < 2; ++par) {
+      const float* x = s + 4 * par;  // columns 0..3, 8..11, 16..19, 24..27 from here
+      const float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[8], x[9]), m2 = max3(x[10], x[11], x[16]);
+      const float m3 = max3(x[17], x[18], x[19]), m4 = max3(x[24], x[25], x[26]);
+      pm[par] = fmaxf(max3(m0, m1, m2), max3(m3, m4, x[27]));
+    }
+    tm = max3(tm, fmaf(pm[0], sc.x * rk, sc.y), fmaf(pm[1], sc.z * rk, sc.w));
+  }
+  return tm;
+}
+__device__ __forceinline__ float row_max_masked(uint32_t ts, const float2* scale, float rk, int seen) {
+  float tm = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    float s[32];
+    tmem_ld32(ts + 32 * i, s);
+    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
+    const float k0 = sc.x * rk, k1 = sc.z * rk;
+    wait_ld();
+    loaded<32>(s);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float y = (e >> 2) & 1 ? fmaf(s[e], k1, sc.w) : fmaf(s[e], k0, sc.y);
+      tm = fmaxf(tm, kPage * (2 * i + ((e >> 2) & 1)) + col_token(e) < seen ? y : -INFINITY);
+    }
+  }
+  return tm;
+}
+// Weights 2^{y + base} as fp16 pairs over the columns of S, and their sum without the value scales.
+template <bool MASKED>
+__device__ __forceinline__ float weights(uint32_t ts, const float2* scale, float rk, float base, int seen) {
+  float l = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    float s[32];
+    uint32_t pk[16];
+    tmem_ld32(ts + 32 * i, s);
+    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
+    const dec::f2x k2[2] = {dec::f2_splat(sc.x * rk), dec::f2_splat(sc.z * rk)};
+    const dec::f2x b2[2] = {dec::f2_splat(sc.y + base), dec::f2_splat(sc.w + base)};
+    const float un[2] = {sc.y == -INFINITY ? 0.f : ex2(-sc.y), sc.w == -INFINITY ? 0.f : ex2(-sc.w)};
+    wait_ld();
+    loaded<32>(s);
+    dec::f2x sum[2];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const int par = (e >> 2) & 1;
+      float y0, y1;
+      dec::f2_unpack(dec::f2_fma(dec::f2_pack(s[e], s[e + 1]), k2[par], b2[par]), y0, y1);
+      if (MASKED) {
+        y0 = kPage * (2 * i + par) + col_token(e) < seen ? y0 : -INFINITY;
+        y1 = kPage * (2 * i + par) + col_token(e + 1) < seen ? y1 : -INFINITY;
+      }
+      const float p0 = ex2(y0), p1 = ex2(y1);
+      const dec::f2x p2 = dec::f2_pack(p0, p1);
+      sum[par] = (e & ~4) == 0 ? p2 : dec::f2_add(sum[par], p2);
+      pk[e >> 1] = dec::pack_f16(p0, p1);
+    }
+    tmem_st16(ts + 16 * i, pk);
+    float l0, l1, l2, l3;
+    dec::f2_unpack(sum[0], l0, l1);
+    dec::f2_unpack(sum[1], l2, l3);
+    l = fmaf(l0 + l1, un[0], fmaf(l2 + l3, un[1], l));
+  }
+  return l;
+}
 // Rows 16 part .. of the warp pair's 32 (at: element of this lane's row in q, negative for none) times a power of two each, to
 // shared memory (qs: the half's operand); the factors go to scale[row].  Sixteen lanes read a row: with a row to a thread,
 // every load touched 32 lines and the L1 took 17,000 clocks for a unit's queries.
@@ -326,7 +407,6 @@ __device__ __noinline__ void stage_query(const uint16_t* q, long long at, float 
   }
   dec::fence_proxy_async();
 }
-// Two threads have a row: one the keys 0..63 of a tile and the output's channels 0..63, its peer (8 warps on) the others.
 // At the end of a unit the next one's query is staged, so that its first S is issued, before O is stored.
 __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t tmem, int32_t* rec) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -396,7 +476,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
     const float2* scale = t->scale[jj % kScaleSlots] + 4 * part;
     const int seen = limit - c.j * kKeys - 64 * part;  // of this thread's 64 keys
     const bool masked = __any_sync(dec::kFull, seen < 64);
-    float tm = masked ? row_max_masked(ts, scale, rk, Causal{seen}) : row_max(ts, scale, rk);
+    float tm = masked ? row_max_masked(ts, scale, rk, seen) : row_max(ts, scale, rk);
     tm = fmaxf(tm, exchange(tm));
     if (c.first) {
       m = tm;
@@ -412,7 +492,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint8_t* smem, uint32_t
       }
     }
     const float base = kTileShift - (m == -INFINITY ? 0.f : m);
-    l += masked ? weights<true>(ts, scale, rk, base, Causal{seen}) : weights<false>(ts, scale, rk, base, Causal{0});
+    l += masked ? weights<true>(ts, scale, rk, base, seen) : weights<false>(ts, scale, rk, base, 0);
     wait_st();
     fence_before();
     __syncwarp();
@@ -568,7 +648,7 @@ cudaError_t launch_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s) {
   cfg.dynamicSmemBytes = 0;
   cfg.gridDim = dim3(static_cast<unsigned>(sms), kRows / 8);
   cfg.blockDim = dim3(256);
-  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<kRows>, a);
+  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<kRows, 4>, a);
 }
 
 }  // namespace runs

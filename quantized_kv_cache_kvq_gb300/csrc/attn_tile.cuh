@@ -18,8 +18,7 @@ constexpr int kKeys = 128;      // keys of a tile
 constexpr int kPagesPerTile = kKeys / kPage;
 constexpr float kTileShift = 7.f;  // weights are held times 2^7 ..
 constexpr float kSlack = 8.f;      // .. and may grow to 2^15 before the running maximum (and O) is moved
-__host__ __device__ constexpr uint32_t idesc(uint32_t n) { return (1u << 4) | ((n / 8) << 17) | ((128u / 16) << 24); }  // fp16 x fp16 -> fp32, M = 128
-constexpr uint32_t kIdesc = idesc(128);
+constexpr uint32_t kIdesc = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);  // fp16 x fp16 -> fp32, M = N = 128
 
 struct RunInfo {
   int len, n, row0;
@@ -45,11 +44,10 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(kIdesc), "r"(acc), "r"(leader)
       : "memory");
 }
-template <uint32_t N = 128>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc, uint32_t leader) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc(N)), "r"(acc), "r"(leader)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(kIdesc), "r"(acc), "r"(leader)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
@@ -298,95 +296,6 @@ __device__ __forceinline__ uint4 ldg_codes(const uint8_t* p) {
 __device__ __forceinline__ constexpr int col_token(int k) { return 2 * (k >> 3) + (k & 1) + 8 * ((k >> 1) & 1); }
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-// A thread has 64 keys of a row.  It goes over their columns of S in TMEM twice, the maximum, then the weights, 32 columns (pages 2 i and 2 i + 1, in
-// groups of four columns) at a time.  y = x log2 e + ev = S k + ev; since k >= 0 a page's largest S gives its largest y.  Keys that
-// the row does not see (`Seen`, by page and token) have -inf, whatever S holds there.
-struct Causal {
-  int seen;  // of the 64 keys
-  __device__ __forceinline__ bool operator()(int i, int par, int token) const { return kPage * (2 * i + par) + token < seen; }
-};
-struct Masked {  // a bit for each token of the pages 0, 1 and 2, 3
-  uint32_t b01, b23;
-  __device__ __forceinline__ bool operator()(int i, int par, int token) const { return (i ? b23 : b01) >> (kPage * par + token) & 1u; }
-};
-__device__ __forceinline__ float row_max(uint32_t ts, const float2* scale, float rk) {
-  float tm = -INFINITY;
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    float s[32];
-    tmem_ld32(ts + 32 * i, s);
-    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
-    wait_ld();
-    loaded<32>(s);
-    float pm[2];
-#pragma unroll
-    for (int par = 0; par < 2; ++par) {
-      const float* x = s + 4 * par;  // columns 0..3, 8..11, 16..19, 24..27 from here
-      const float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[8], x[9]), m2 = max3(x[10], x[11], x[16]);
-      const float m3 = max3(x[17], x[18], x[19]), m4 = max3(x[24], x[25], x[26]);
-      pm[par] = fmaxf(max3(m0, m1, m2), max3(m3, m4, x[27]));
-    }
-    tm = max3(tm, fmaf(pm[0], sc.x * rk, sc.y), fmaf(pm[1], sc.z * rk, sc.w));
-  }
-  return tm;
-}
-template <class Seen>
-__device__ __forceinline__ float row_max_masked(uint32_t ts, const float2* scale, float rk, Seen seen) {
-  float tm = -INFINITY;
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    float s[32];
-    tmem_ld32(ts + 32 * i, s);
-    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
-    const float k0 = sc.x * rk, k1 = sc.z * rk;
-    wait_ld();
-    loaded<32>(s);
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float y = (e >> 2) & 1 ? fmaf(s[e], k1, sc.w) : fmaf(s[e], k0, sc.y);
-      tm = fmaxf(tm, seen(i, (e >> 2) & 1, col_token(e)) ? y : -INFINITY);
-    }
-  }
-  return tm;
-}
-// Weights 2^{y + base} as fp16 pairs over the columns of S, and their sum without the value scales.
-template <bool MASKED, class Seen>
-__device__ __forceinline__ float weights(uint32_t ts, const float2* scale, float rk, float base, Seen seen) {
-  float l = 0.f;
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    float s[32];
-    uint32_t pk[16];
-    tmem_ld32(ts + 32 * i, s);
-    const float4 sc = *reinterpret_cast<const float4*>(scale + 2 * i);
-    const dec::f2x k2[2] = {dec::f2_splat(sc.x * rk), dec::f2_splat(sc.z * rk)};
-    const dec::f2x b2[2] = {dec::f2_splat(sc.y + base), dec::f2_splat(sc.w + base)};
-    const float un[2] = {sc.y == -INFINITY ? 0.f : ex2(-sc.y), sc.w == -INFINITY ? 0.f : ex2(-sc.w)};
-    wait_ld();
-    loaded<32>(s);
-    dec::f2x sum[2];
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const int par = (e >> 2) & 1;
-      float y0, y1;
-      dec::f2_unpack(dec::f2_fma(dec::f2_pack(s[e], s[e + 1]), k2[par], b2[par]), y0, y1);
-      if (MASKED) {
-        y0 = seen(i, par, col_token(e)) ? y0 : -INFINITY;
-        y1 = seen(i, par, col_token(e + 1)) ? y1 : -INFINITY;
-      }
-      const float p0 = ex2(y0), p1 = ex2(y1);
-      const dec::f2x p2 = dec::f2_pack(p0, p1);
-      sum[par] = (e & ~4) == 0 ? p2 : dec::f2_add(sum[par], p2);
-      pk[e >> 1] = dec::pack_f16(p0, p1);
-    }
-    tmem_st16(ts + 16 * i, pk);
-    float l0, l1, l2, l3;
-    dec::f2_unpack(sum[0], l0, l1);
-    dec::f2_unpack(sum[1], l2, l3);
-    l = fmaf(l0 + l1, un[0], fmaf(l2 + l3, un[1], l));
-  }
-  return l;
-}
 // This thread's channels of O times alpha.
 template <int CHANNELS>
 __device__ __noinline__ void rescale_o(uint32_t to, float alpha) {
@@ -442,7 +351,7 @@ __device__ __noinline__ void store_piece(uint32_t to, float* dst_row) {
 
 // ------------------------------------------------------------------------------------------------ merge
 // The units that more than one CTA worked on: warp i of block (c, .) merges row i of the unit that began in CTA c.
-template <int kRows>
+template <int kRows, int kAtOnce>
 __global__ void __launch_bounds__(256) tile_merge_kernel(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, lane = threadIdx.x & 31;
@@ -465,18 +374,28 @@ __global__ void __launch_bounds__(256) tile_merge_kernel(const AttnArgs a) {
     end = c + 33;
     while (end + 1 < a.tile_ctas && !a.tw_rec[8 * end + 4]) ++end;
   }
-#pragma unroll 4
-  for (int k = c; k <= end; ++k) {
-    const float2 st = stats_of(k);
-    const float4 v = acc_of(k);
-    const float mn = fmaxf(m, st.x);
-    const float f0 = m == -INFINITY ? 0.f : ex2(m - mn), f1 = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : ex2(st.x - mn);
-    m = mn;
-    l = l * f0 + st.y * f1;
-    acc.x = acc.x * f0 + v.x * f1;
-    acc.y = acc.y * f0 + v.y * f1;
-    acc.z = acc.z * f0 + v.z * f1;
-    acc.w = acc.w * f0 + v.w * f1;
+  // Loads of kAtOnce pieces are on their way together.
+  for (int k0 = c; k0 <= end; k0 += kAtOnce) {
+    float2 st[kAtOnce];
+    float4 v[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (k0 + i <= end) {
+        st[i] = stats_of(k0 + i);
+        v[i] = acc_of(k0 + i);
+      }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (k0 + i > end) break;
+      const float mn = fmaxf(m, st[i].x);
+      const float f0 = m == -INFINITY ? 0.f : ex2(m - mn), f1 = st[i].x == -INFINITY ? (st[i].y == 0.f ? 0.f : 1.f) : ex2(st[i].x - mn);
+      m = mn;
+      l = l * f0 + st[i].y * f1;
+      acc.x = acc.x * f0 + v[i].x * f1;
+      acc.y = acc.y * f0 + v[i].y * f1;
+      acc.z = acc.z * f0 + v[i].z * f1;
+      acc.w = acc.w * f0 + v[i].w * f1;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int head = unit.z * a.G + r % a.G;

@@ -4,17 +4,16 @@
 // few beside its context, so the tiles are what the cache costs to bring: 32.8 KB from HBM, 1,520 clocks of an SM's share of the copy
 // rate.  Everything else is laid out to stay below that:
 //   * the query lies in TMEM (the first operand of S = Q K^T), so all shared memory is a ring of six operand tiles;
-//   * the softmax takes half tiles of 64 keys: four teams of four warps (a thread has a row) take them in turn and S has five buffers, so that
-//     the exponentials never wait for a product or a barrier;
-//   * O is one accumulator for all teams.  Its reference, a row's running maximum, goes from a half tile to the next through shared memory; it moves
-//     only where a row outgrows it by 2^8, and only then is O rescaled, when all P V so far are through;
-//   * one warp issues S, another P V, each as soon as its operands are there;
+//   * S has two buffers in TMEM and O one: while the softmax works on a tile, the next one's S and the last one's P V run (512 clocks each);
+//   * four threads have a row, 32 keys each, and keep their S in registers: one read of TMEM a tile;
+//   * the running maximum moves only where a row outgrows it by 2^8; whether any row does is one barrier with a vote among the four warps of
+//     32 rows, so the maximum itself is exchanged, and O rescaled, only then;
 //   * codes of K and V are loaded a whole tile ahead (eight words of 16 bytes a thread), and a warp of its own looks several tiles ahead and has
 //     the L2 bring them;
 //   * of the masks only those words are read that say something of the tile: tokens before the run are seen by all.
 //
-// TMEM columns: S (and P, over the first half of each) five times 64, Q 64, O 128.
-// Warps: 0-15 softmax (team w >> 2, rows 32 (w & 3) ..), 16-23 convert, 24 issues S, 25 looks ahead, 26 issues P V.
+// TMEM columns: S (and P, over the first half of each 32 columns) twice 128, O 128, Q 64.
+// Warps: 0-15 softmax (rows 32 (w & 3) .., keys 32 (w >> 2) .. of a tile), 16-23 convert, 24 issues the products, 25 looks ahead.
 // Operand layouts, key order inside a tile, scales in the exponent: as in attn_runs_tile.cu.
 #include "attn_tile.cuh"
 
@@ -25,7 +24,7 @@ namespace {
 constexpr int kRows = 128;      // rows of a unit
 constexpr int kSlots = 6;       // ring of operand tiles
 constexpr int kOperand = 32768;  // 128 x 128 fp16
-constexpr int kSoftmaxWarps = 16, kConvertWarp = 16, kMmaWarp = 24, kScoutWarp = 25, kPvWarp = 26;  // first warps of the roles
+constexpr int kSoftmaxWarps = 16, kConvertWarp = 16, kMmaWarp = 24, kScoutWarp = 25;  // first warps of the roles
 constexpr int kThreads = 28 * 32;
 // Registers: 72 a thread at launch; the softmax warps take what the last warpgroup, of which only one warp works, gives back.  None of the loops
 // may spill (with 72 the softmax does).
@@ -36,8 +35,7 @@ static_assert(16 * kRegsSoftmax + 8 * kRegsConvert + 4 * kRegsMma <= 28 * 72, "n
 constexpr int kGroup = 4, kGroups = 4, kDescs = kGroup * kGroups;
 constexpr int kOffTail = kSlots * kOperand, kTailBytes = 10 * 1024;
 constexpr int kSmemBytes = kOffTail + kTailBytes;
-constexpr int kBufs = 5;  // of S
-constexpr uint32_t kTmemS = 0, kTmemQ = 320, kTmemO = 384;
+constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemQ = 384;
 
 struct Desc {  // of a key tile
   float2 scale[kPagesPerTile];   // 2^ek |sm_scale| log2 e, ev (0, -inf for an absent page)
@@ -48,9 +46,9 @@ struct Desc {  // of a key tile
 struct Tail {  // shared memory behind the operands
   Desc desc[kDescs];
   uint64_t full[kSlots], empty[kSlots];
-  // Of the half tiles in turn: S there, weights there, P V done; and of the teams' half tiles, for each 32 rows: the running maximum there.
-  // (A parity tells apart only a phase and the one before it: tests/test_tree_tile_waits.py goes through the waits.)
-  uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs], m_ready[4][4];
+  // Of the tiles in turn.  A parity tells apart only a phase and the one before it: when a warp is at a tile, the P V of the tile before
+  // may be running still (this tile's S went ahead of it) or this tile's be over, so one barrier would not do.
+  uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_full;
   uint64_t desc_full[kGroups], desc_done[kGroups];
   uint64_t drained;  // every product of the CTA
@@ -59,9 +57,8 @@ struct Tail {  // shared memory behind the operands
   UnitInfo unit[kScoutWarp + 1];  // where each warp is
   int start[4];             // request, kv head, unit, first tile of the CTA's range
   int n;                    // its tiles
-  float m[kRows];         // a row's running maximum, O's reference
-  float peer[4][kRows];   // what the four threads of a row tell each other about its query
-  float2 ends[4][kRows];  // references and sums of a row's four threads at the end of a piece
+  // What the four threads of a row tell each other: maxima of a tile (two in turn), then sums or exponents.
+  float peer_m[2][4][kRows], peer[4][kRows];
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
 struct Tree {
@@ -226,66 +223,66 @@ __device__ void convert_role(const AttnArgs& a, Tail* t, uint8_t* ring) {
 }
 
 // ------------------------------------------------------------------------------------------------ products
-// Steps of 16 channels or keys: 32 bytes apart inside a 64-element column of rows, the second column 16 KB on.
-__device__ __forceinline__ uint64_t k_step(int ks) { return static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4); }
-// Half tile u: keys 64 (u & 1) .. of tile u >> 1.  S of one is issued when its buffer's last weights have been used.
-__device__ void score_role(Tail* t, uint32_t smem_base, uint32_t tmem, uint32_t leader) {
+__device__ void mma_role(Tail* t, uint32_t smem_base, uint32_t tmem, uint32_t leader) {
   tmem = dec::uniform_u32(tmem);
   const uint64_t ring = smem_desc(smem_base);
+  // Eight steps of 16: 32 bytes apart inside a 64-element column of rows, the second column 16 KB on; the weights of 32 keys lie in the first
+  // half of those 32 columns of S.
+  auto k_step = [](int ks) { return static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4); };
   const int total = dec::uniform_u32(t->n);
-  int slot = 0, buf = 0;
-  uint32_t phase = 0, q_phase = 0, used = 0;  // used: times that the buffer has been used, mod 2
-#pragma unroll 1
-  for (int tile = 0; tile < total; ++tile) {
-    if (!wait_warp(&t->full[slot], phase, &t->abort)) return;
+  int slot = 0;  // of the operand tile taken next
+  uint32_t phase = 0, q_phase = 0;
+  auto next_slot = [&]() {
+    if (++slot == kSlots) { slot = 0; phase ^= 1u; }
+  };
+  // S of tile `tile`, whose K is in `slot`; its flags, or -1 where a wait gave up.
+  auto score = [&](int tile, int k_slot, uint32_t k_phase) {
+    if (!wait_warp(&t->full[k_slot], k_phase, &t->abort)) return -1;
     const int flags = dec::uniform_u32(*reinterpret_cast<volatile int*>(&t->desc[tile % kDescs].flags));
     if (flags & kFirst) {
-      if (!wait_warp(&t->q_full, q_phase, &t->abort)) return;
+      if (!wait_warp(&t->q_full, q_phase, &t->abort)) return -1;
       q_phase ^= 1u;
     }
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      if (2 * tile + half >= kBufs && !wait_warp(&t->pv_done[buf], used ^ 1u, &t->abort)) return;
-      fence_after();
-      // rows 64 half .. of the K tile: 8 KB on
-      const uint64_t y = ring + static_cast<uint64_t>((slot * kOperand + half * 8192) >> 4);
-      const uint32_t s = tmem + kTmemS + 64 * buf;
+    fence_after();
+    const uint64_t y = ring + static_cast<uint64_t>(k_slot * (kOperand >> 4));
+    const uint32_t s = tmem + kTmemS + 128 * (tile & 1);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_ts<64>(s, tmem + kTmemQ + 8 * ks, y + k_step(ks), ks > 0, leader);
-      commit(&t->s_full[buf], leader);
-      if (++buf == kBufs) { buf = 0; used ^= 1u; }
-    }
-    commit(&t->empty[slot], leader);
-    slot += 2;
-    if (slot >= kSlots) { slot -= kSlots; phase ^= 1u; }
-  }
-}
-__device__ void pv_role(Tail* t, uint32_t smem_base, uint32_t tmem, uint32_t leader) {
-  tmem = dec::uniform_u32(tmem);
-  const uint64_t ring = smem_desc(smem_base);
-  const int total = dec::uniform_u32(t->n);
-  int slot = 1, buf = 0;
-  uint32_t phase = 0, used = 0;
+    for (int ks = 0; ks < 8; ++ks) mma_ts(s, tmem + kTmemQ + 8 * ks, y + k_step(ks), ks > 0, leader);
+    commit(&t->s_full[tile & 1], leader);
+    commit(&t->empty[k_slot], leader);
+    return flags;
+  };
+  int flags = score(0, 0, 0);
+  if (flags < 0) return;
+  next_slot();
 #pragma unroll 1
   for (int tile = 0; tile < total; ++tile) {
-    if (!wait_warp(&t->full[slot], phase, &t->abort)) return;
-    const int flags = dec::uniform_u32(*reinterpret_cast<volatile int*>(&t->desc[tile % kDescs].flags));
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      if (!wait_warp(&t->p_full[buf], used, &t->abort)) return;
-      fence_after();
-      // keys 64 half .. of the V tile: its second column of rows
-      const uint64_t y = ring + static_cast<uint64_t>((slot * kOperand + half * 16384) >> 4);
-      const uint32_t p = tmem + kTmemS + 64 * buf;
-      const bool fresh = (flags & kFirst) && half == 0;
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) mma_ts(tmem + kTmemO, p + 8 * ks, y + k_step(ks), !fresh || ks > 0, leader);
-      commit(&t->pv_done[buf], leader);
-      if (++buf == kBufs) { buf = 0; used ^= 1u; }
+    const int v_slot = slot;
+    const uint32_t v_phase = phase;
+    next_slot();
+    // The next tile's S goes before this one's P V while it belongs to the same piece (the next piece's query comes with this tile's end).
+    int next_flags = 0;
+    const bool last = (flags & kLast) != 0, more = tile + 1 < total;
+    if (more && !last) {
+      next_flags = score(tile + 1, slot, phase);
+      if (next_flags < 0) return;
     }
-    commit(&t->empty[slot], leader);
-    slot += 2;
-    if (slot >= kSlots) { slot -= kSlots; phase ^= 1u; }
+    if (!wait_warp(&t->p_full[tile & 1], (tile >> 1) & 1u, &t->abort)) return;
+    if (!wait_warp(&t->full[v_slot], v_phase, &t->abort)) return;
+    fence_after();
+    const uint64_t y = ring + static_cast<uint64_t>(v_slot * (kOperand >> 4));
+    const uint32_t p = tmem + kTmemS + 128 * (tile & 1);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+      mma_ts(tmem + kTmemO, p + 32 * (ks >> 1) + 8 * (ks & 1), y + k_step(ks), !(flags & kFirst) || ks > 0, leader);
+    commit(&t->pv_done[tile & 1], leader);
+    commit(&t->empty[v_slot], leader);
+    if (more && last) {
+      next_flags = score(tile + 1, slot, phase);
+      if (next_flags < 0) return;
+    }
+    if (more) next_slot();
+    flags = next_flags;
   }
 }
 
@@ -299,23 +296,30 @@ __device__ __forceinline__ uint32_t page_bits(const AttnArgs& a, long long row, 
 }
 
 // At the end of a piece the next one's query is staged, so that its first S is issued, before O is stored.  A warp whose wait has given up
-// goes on to the end of its range all the same, without waiting or handing anything on: the four warps of 32 rows take every meeting that the range
+// goes on to the end of its range all the same, without waiting or handing anything on: the four warps of a row take every meeting that the range
 // has.  What it computes from then on is thrown away with the call's error.
 __device__ void softmax_role(const AttnArgs& a, Tail* t, uint32_t tmem, int32_t* rec) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = warp >> 2, quarter = warp & 3;
-  const int row = quarter * 32 + lane;  // of the unit
-  const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;  // TMEM lane 32 (warp & 3)
-  auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory"); };  // the four warps of 32 rows
+  const int part = warp >> 2;                  // keys 32 part .. of a tile, channels 32 part ..
+  const int row = (warp & 3) * 32 + lane;      // of the unit
+  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp & 3)
+  const uint32_t ts = tmem + kTmemS + 32 * part + lanes, to = tmem + kTmemO + 32 * part + lanes;
+  const int bar = 1 + (warp & 3);
+  auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); };
+  auto meet_any = [&](bool x) {  // whether any thread of the four warps says so
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"(static_cast<uint32_t>(x)), "r"(bar) : "memory");
+    return r != 0;
+  };
   bool alive = true;
   auto wait_for = [&](uint64_t* b, uint32_t parity) {
     if (alive) alive = wait_warp(b, parity, &t->abort);
   };
-  auto wait_turn = [&](uint64_t* bars, int u) { wait_for(&bars[u % kBufs], (u / kBufs) & 1u); };  // a half tile's of kBufs in turn
   Cursor<Tree> c;
   c.begin(a, t);
   const int total = c.left;
-  float m = -INFINITY, l = 0.f, rk = 1.f;  // the reference of this thread's sum, and that
+  float m = -INFINITY, l = 0.f, rk = 1.f;
   int ctx = 0, end = 0;    // the unit's run begins there, its context ends there
   int mask_row = -1;       // this thread's row of the mask, -1 past the run's last
   bool begins = false, active = false;  // the piece has its unit's first tile; the warp has rows
@@ -326,8 +330,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint32_t tmem, int32_t*
     tok = valid ? r / a.G : 0;
     out_at = static_cast<long long>(u.run.row0 + tok) * a.Hq + u.kvh * a.G + (valid ? r - tok * a.G : 0);
   };
-  // The row (channels 32 team .. of it) times a power of two, its largest element in [2^8, 2^9) (bf16 elements are then exact in fp16 down to 2^-22
-  // of it), to TMEM.
+  // The row times a power of two, its largest element in [2^8, 2^9) (bf16 elements are then exact in fp16 down to 2^-22 of it), to TMEM.
   auto begin_unit = [&]() {
     bool valid;
     int tok;
@@ -338,13 +341,13 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint32_t tmem, int32_t*
     end = run.len;
     mask_row = valid ? run.row0 + tok : -1;
     begins = c.j == 0;
-    active = c.at->u * kRows + quarter * 32 < run.n * a.G;
+    active = c.at->u * kRows + (warp & 3) * 32 < run.n * a.G;
     m = -INFINITY;
     l = 0.f;
     if (active) {
       uint32_t u[16];
       const long long row_at = static_cast<long long>(run.row0 + tok);
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + row_at * a.q_stride + (out_at - row_at * a.Hq) * kHeadDim + 32 * team;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + row_at * a.q_stride + (out_at - row_at * a.Hq) * kHeadDim + 32 * part;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4 w = valid ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
@@ -353,8 +356,8 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint32_t tmem, int32_t*
       uint32_t top = 0;  // largest exponent field
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = max(top, max((u[e] >> 7) & 0xFFu, (u[e] >> 23) & 0xFFu));
-      meet();  // the others have read what the last meetings left
-      t->peer[team][row] = static_cast<float>(top);
+      meet();  // the others have read what the last meeting left
+      t->peer[part][row] = static_cast<float>(top);
       meet();
       const float all = fmaxf(fmaxf(t->peer[0][row], t->peer[1][row]), fmaxf(t->peer[2][row], t->peer[3][row]));
       const int er = min(max(static_cast<int>(all) - 127 - 8, -100), 120);
@@ -362,7 +365,7 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint32_t tmem, int32_t*
 #pragma unroll
       for (int e = 0; e < 16; ++e) u[e] = dec::pack_f16(__uint_as_float(u[e] << 16) * f, __uint_as_float(u[e] & 0xFFFF0000u) * f);
       rk = exp2_int(er);
-      tmem_st16(tmem + kTmemQ + 16 * team + lanes, u);
+      tmem_st16(tmem + kTmemQ + 16 * part + lanes, u);
       wait_st();
     }
     fence_before();
@@ -372,47 +375,76 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint32_t tmem, int32_t*
   begin_unit();
 #pragma unroll 1
   for (int jj = 0; jj < total; ++jj) {
-    if ((jj & 1) == team >> 1) {
-      const int half = team & 1, u = 2 * jj + half;  // u & 3 is the team
-      const uint32_t ts = tmem + kTmemS + 64 * (u % kBufs) + lanes;
-      const float2* scale = t->desc[jj % kDescs].scale + 4 * half;
-      const int p0 = c.j * kKeys + 64 * half;  // position of the half tile's first token
-      const bool masked = p0 + 64 > ctx;       // the same in all lanes
-      Masked seen{0, 0};
-      if (masked && mask_row >= 0) {
-        seen.b01 = page_bits(a, mask_row, p0, ctx, end) | page_bits(a, mask_row, p0 + kPage, ctx, end) << 16;
-        seen.b23 = page_bits(a, mask_row, p0 + 2 * kPage, ctx, end) | page_bits(a, mask_row, p0 + 3 * kPage, ctx, end) << 16;
+    const int buf = jj & 1;
+    wait_for(&t->s_full[buf], (jj >> 1) & 1u);
+    fence_after();
+    if (active) {
+      float s[32];
+      tmem_ld32(ts + 128 * buf, s);
+      const float4 sc = *reinterpret_cast<const float4*>(t->desc[jj % kDescs].scale + 2 * part);
+      // y = S k + e of the two pages; k >= 0, so a page's largest S gives its largest y
+      float k0 = sc.x * rk, k1 = sc.z * rk, e0 = sc.y, e1 = sc.w;
+      wait_ld();
+      loaded<32>(s);
+      const int p0 = c.j * kKeys + 32 * part;  // position of the thread's first page
+      if (p0 + 2 * kPage > ctx) {  // the same in all lanes of the warp
+        const uint32_t b0 = mask_row < 0 ? 0 : page_bits(a, mask_row, p0, ctx, end), b1 = mask_row < 0 ? 0 : page_bits(a, mask_row, p0 + kPage, ctx, end);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float y = (e >> 2) & 1 ? fmaf(s[e], k1, e1) : fmaf(s[e], k0, e0);
+          s[e] = ((e >> 2) & 1 ? b1 : b0) >> col_token(e) & 1u ? y : -INFINITY;
+        }
+        k0 = k1 = 1.f;
+        e0 = e1 = 0.f;
       }
-      wait_turn(t->s_full, u);
-      fence_after();
-      float tm = -INFINITY;
-      if (active) tm = masked ? row_max_masked(ts, scale, rk, seen) : row_max(ts, scale, rk);
-      const bool first = c.first && half == 0;  // of the piece
-      if (u > 0) wait_for(&t->m_ready[(u - 1) & 3][quarter], ((u - 1) >> 2) & 1u);
-      const float was = first ? -INFINITY : t->m[row];
-      const bool move = tm > was + kSlack;
-      const float now = move ? tm : was;
-      if (active && (first || move)) t->m[row] = now;
-      __syncwarp();
-      if (alive && lane == 0) arrive(&t->m_ready[team][quarter]);
-      if (active) {
-        if (!first && __any_sync(dec::kFull, move)) {
-          wait_turn(t->pv_done, u - 1);  // O is the sum of the half tiles before
+      float pm[2];
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const float* x = s + 4 * par;  // columns 0..3, 8..11, 16..19, 24..27 from here
+        const float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[8], x[9]), m2 = max3(x[10], x[11], x[16]);
+        const float m3 = max3(x[17], x[18], x[19]), m4 = max3(x[24], x[25], x[26]);
+        pm[par] = fmaxf(max3(m0, m1, m2), max3(m3, m4, x[27]));
+      }
+      const float tm = fmaxf(fmaf(pm[0], k0, e0), fmaf(pm[1], k1, e1));
+      t->peer_m[buf][part][row] = tm;
+      if (meet_any(tm > m + kSlack)) {
+        const float all = fmaxf(fmaxf(t->peer_m[buf][0][row], t->peer_m[buf][1][row]), fmaxf(t->peer_m[buf][2][row], t->peer_m[buf][3][row]));
+        const bool move = all > m + kSlack;
+        if (!c.first && __any_sync(dec::kFull, move)) {
+          wait_for(&t->pv_done[buf ^ 1], ((jj - 1) >> 1) & 1u);  // O is the previous tiles' sum
           fence_after();
-          rescale_o<128>(tmem + kTmemO + lanes, !move ? 1.f : was == -INFINITY ? 0.f : ex2(was - now));
+          const float alpha = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - all);
+          l *= alpha;
+          rescale_o<32>(to, alpha);
         }
-        if (m != now) {
-          l *= m == -INFINITY ? 0.f : ex2(m - now);
-          m = now;
-        }
-        const float base = kTileShift - (m == -INFINITY ? 0.f : m);
-        l += masked ? weights<true>(ts, scale, rk, base, seen) : weights<false>(ts, scale, rk, base, seen);
-        wait_st();
+        m = move ? all : m;
       }
-      fence_before();
-      __syncwarp();
-      if (alive && lane == 0) arrive(&t->p_full[u % kBufs]);
+      const float base = kTileShift - (m == -INFINITY ? 0.f : m);
+      const dec::f2x k2[2] = {dec::f2_splat(k0), dec::f2_splat(k1)};
+      const dec::f2x b2[2] = {dec::f2_splat(e0 + base), dec::f2_splat(e1 + base)};
+      const float un[2] = {sc.y == -INFINITY ? 0.f : ex2(-sc.y), sc.w == -INFINITY ? 0.f : ex2(-sc.w)};
+      dec::f2x sum[2];
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const int par = (e >> 2) & 1;
+        float y0, y1;
+        dec::f2_unpack(dec::f2_fma(dec::f2_pack(s[e], s[e + 1]), k2[par], b2[par]), y0, y1);
+        const float w0 = ex2(y0), w1 = ex2(y1);
+        const dec::f2x w2 = dec::f2_pack(w0, w1);
+        sum[par] = (e & ~4) == 0 ? w2 : dec::f2_add(sum[par], w2);
+        pk[e >> 1] = dec::pack_f16(w0, w1);
+      }
+      tmem_st16(ts + 128 * buf, pk);
+      float l0, l1, l2, l3;
+      dec::f2_unpack(sum[0], l0, l1);
+      dec::f2_unpack(sum[1], l2, l3);
+      l = fmaf(l0 + l1, un[0], fmaf(l2 + l3, un[1], l));
+      wait_st();
     }
+    fence_before();
+    __syncwarp();
+    if (alive && lane == 0) arrive(&t->p_full[buf]);
     if (!c.last()) {
       c.advance(a);
       continue;
@@ -425,17 +457,13 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint32_t tmem, int32_t*
       rec[0] = 1;
     }
     const bool had = active;
-    float top = -INFINITY, sum = 0.f;
+    const float m0 = m;
+    float l0 = 0.f;
     if (had) {
-      t->ends[team][row] = make_float2(m, l);
+      meet();  // the others have read what the last meeting left
+      t->peer[part][row] = l;
       meet();
-      top = t->m[row];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = t->ends[i][row];
-        // a sum without a maximum is 0, or no number (of a query that is none), and stays
-        sum += x.y * (x.x == -INFINITY ? 1.f : ex2(x.x - top));
-      }
+      l0 = (t->peer[0][row] + t->peer[1][row]) + (t->peer[2][row] + t->peer[3][row]);
     }
     const size_t piece = static_cast<size_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kRows + row;
     bool valid;
@@ -443,22 +471,20 @@ __device__ void softmax_role(const AttnArgs& a, Tail* t, uint32_t tmem, int32_t*
     long long out_at;
     locate(valid, tok, out_at);
     c.advance(a);
-    wait_turn(t->s_full, 2 * jj + 1);  // the last S: the query in TMEM is free
     if (jj + 1 < total) begin_unit();
-    if (had) {  // (warps without rows do not wait: the meeting below is what keeps the barriers from going on to a later phase meanwhile)
-      wait_turn(t->pv_done, 2 * jj + 1);
-      fence_after();
-      valid = valid && alive;
+    wait_for(&t->pv_done[buf], (jj >> 1) & 1u);
+    fence_after();
+    valid = valid && alive;
+    if (had) {
       if (whole) {
-        store_out<32>(tmem + kTmemO + 32 * team + lanes, sum == 0.f ? 0.f : 1.f / sum, static_cast<uint16_t*>(a.out) + out_at * kHeadDim + 32 * team, valid);
-        if (a.lse && valid && team == 0) a.lse[out_at] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kTileShift)) * dec::kLn2;
+        store_out<32>(to, l0 == 0.f ? 0.f : 1.f / l0, static_cast<uint16_t*>(a.out) + out_at * kHeadDim + 32 * part, valid);
+        if (a.lse && valid && part == 0) a.lse[out_at] = l0 == 0.f ? -INFINITY : (m0 + (log2f(l0) - kTileShift)) * dec::kLn2;
       } else {
-        store_piece<32>(tmem + kTmemO + 32 * team + lanes, a.tw_acc + piece * kHeadDim + 32 * team);
-        if (team == 0) *reinterpret_cast<float2*>(a.tw_stats + piece * 2) = make_float2(top, sum);
+        store_piece<32>(to, a.tw_acc + piece * kHeadDim + 32 * part);
+        if (part == 0) *reinterpret_cast<float2*>(a.tw_stats + piece * 2) = make_float2(m0, l0);
       }
-      fence_before();
-      meet();  // no team goes on to its next weights before the other three warps have read this O
     }
+    fence_before();
   }
 }
 
@@ -482,18 +508,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tile_kernel(const __grid_con
       dec::mbar_init(&t->full[i], 8);
       dec::mbar_init(&t->empty[i], 1);
     }
-    for (int i = 0; i < kBufs; ++i) {
+    for (int i = 0; i < 2; ++i) {
       dec::mbar_init(&t->s_full[i], 1);
-      dec::mbar_init(&t->p_full[i], 4);
+      dec::mbar_init(&t->p_full[i], kSoftmaxWarps);
       dec::mbar_init(&t->pv_done[i], 1);
     }
-    for (int i = 0; i < 16; ++i) dec::mbar_init(&t->m_ready[i >> 2][i & 3], 1);
     for (int i = 0; i < kGroups; ++i) {
       dec::mbar_init(&t->desc_full[i], 1);
       dec::mbar_init(&t->desc_done[i], 8);
     }
     dec::mbar_init(&t->q_full, kSoftmaxWarps);
-    dec::mbar_init(&t->drained, 2);
+    dec::mbar_init(&t->drained, 1);
     dec::fence_mbar_init();
     // which pieces of this CTA the merge has to look at
     const int first_tiles = tiles_of<Tree>(a, run_info(a, t->start[0]), t->start[2]);
@@ -516,16 +541,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tile_kernel(const __grid_con
     convert_role<INT8>(a, t, smem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
-    if (warp == kMmaWarp || warp == kPvWarp) {
+    if (warp == kMmaWarp) {
       const uint32_t leader = dec::elect_one();
-      if (warp == kMmaWarp) score_role(t, smem_u32(smem), tmem, leader);
-      else pv_role(t, smem_u32(smem), tmem, leader);
-      // However the roles ended: TMEM and shared memory are given back when the last products that they issued are through with
+      mma_role(t, smem_u32(smem), tmem, leader);
+      // However the role ended: TMEM and shared memory are given back when the last product that it issued is through with
       // them (products wait for nothing; the limit is there all the same).
       commit(&t->drained, leader);
       const long long t0 = clock64();
       while (!__all_sync(dec::kFull, dec::mbar_try_wait(&t->drained, 0)))
-        if (__any_sync(dec::kFull, clock64() - t0 > 2 * kWaitClocks)) {
+        if (__any_sync(dec::kFull, clock64() - t0 > kWaitClocks)) {
           *reinterpret_cast<volatile int*>(&t->abort) = 1;
           break;
         }
@@ -563,7 +587,7 @@ cudaError_t launch_tree_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.gridDim = dim3(static_cast<unsigned>(sms), kRows / 8);
   cfg.blockDim = dim3(256);
-  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<kRows>, a);
+  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<kRows, 8>, a);
 }
 
 }  // namespace runs
