@@ -11,7 +11,8 @@ namespace kvq {
 namespace runs {
 namespace {
 
-// Calls whose longest run has more (token, head) rows are the tile kernel's.
+// Calls whose longest run has more (token, head) rows are the tile kernel's.  16 trees over 11500 tokens, 8 and 32 heads, E4M3: the split kernel, one
+// pass over the context for every 16 rows, 84 us at 16 rows and 222 at up to 64; the tile kernel 113 at 20 rows, 119 at 64, 129 at 128.
 constexpr int kFewRows = 16;
 
 struct Workspace {

@@ -2,7 +2,7 @@
 //
 // A unit is one (request, kv head, 128 consecutive (token, head) rows); its key tiles are the 128-token tiles of the whole context.  A tree's rows are
 // few beside its context, so the tiles are what the cache costs to bring: 32.8 KB from HBM, 1,520 clocks of an SM's share of the copy
-// rate.  Everything else is laid out to stay below that:
+// rate.  The layout aims at that and comes to about 2,400:
 //   * the query lies in TMEM (the first operand of S = Q K^T), so all shared memory is a ring of six operand tiles;
 //   * S has two buffers in TMEM and O one: while the softmax works on a tile, the next one's S and the last one's P V run (512 clocks each);
 //   * four threads have a row, 32 keys each, and keep their S in registers: one read of TMEM a tile;
@@ -11,6 +11,13 @@
 //   * codes of K and V are loaded a whole tile ahead (eight words of 16 bytes a thread), and a warp of its own looks several tiles ahead and has
 //     the L2 bring them;
 //   * of the masks only those words are read that say something of the tile: tokens before the run are seen by all.
+//
+// Bound by the warps' work together: converting 16 K codes of K and V and handing them on is about 1,750 clocks a tile with nothing beside it, the
+// softmax's chain (maximum 600, weights 1,200, waits) about 2,300.  16 trees of 9..16 tokens over 11500, 8 and 32 heads, E4M3: 117 us, 3,270 GB/s; 64 trees
+// of 25..64 over 2000..8192, 4 and 28 heads, INT8: 250 us.  Some 27 us of a call are its start (10 us to the first weights) and its end (9 us from
+// the last tile through the merge).  Slower, on the first of the two (117) and the second (250): two teams of softmax warps with an O each 122 and 269; half
+// tiles for two, three or four teams with one O, S and P V issued by two warps, 153, 143, 128 and 297, 292, 263; K and V converted by warps of their own 121
+// and 261; lookups by the converting warps themselves 150 and 335.
 //
 // TMEM columns: S (and P, over the first half of each 32 columns) twice 128, O 128, Q 64.
 // Warps: 0-15 softmax (rows 32 (w & 3) .., keys 32 (w >> 2) .. of a tile), 16-23 convert, 24 issues the products, 25 looks ahead.
@@ -575,7 +582,9 @@ cudaError_t launch_tree_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s) {
   cudaError_t e = limit[int8].raise(kern, kSmemBytes);
   if (e != cudaSuccess) return e;
   a.tile_ctas = sms;
-  a.unit_cost = 3;
+  // A unit's own cost in tiles.  16 trees of 64 rows over 11500 tokens, 64 trees of up to 448 over up to 8192: 120 and 272 us with 0, 123 and 263
+  // with 1, 121 and 258 with 2, 119 and 250 with 3 and with 6.
+  a.unit_cost = 4;
   kern<<<sms, kThreads, kSmemBytes, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -587,7 +596,7 @@ cudaError_t launch_tree_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.gridDim = dim3(static_cast<unsigned>(sms), kRows / 8);
   cfg.blockDim = dim3(256);
-  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<kRows, 8>, a);
+  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<kRows, 4>, a);
 }
 
 }  // namespace runs

@@ -7,7 +7,9 @@
 // One launch for all layers.  A block has one request and a few (layer, kv head) pairs: where every slot's token comes from is looked up once for
 // all of them.  A key token is eight 16-byte words of its tile, so a thread moves one word of the new tile; a value word holds four tokens of four
 // channels, so a thread puts one together from the words of its four tokens.  Words that stay as they are are neither read nor written.
-// Bound by memory: a value tile's tokens lie in all of its lines, so moving one token reads and writes 2 KB.
+// A value tile's tokens lie in all of its lines, so moving one token reads and writes 2 KB: 32 requests that keep about four tokens of 25..64 in 36
+// layers of 8 heads move some 90 MB for the 19 that the tokens are (26.8 us; 13 at the copy rate), a layer of 4 requests takes 8 us.  With one block for
+// each (request, layer, head) and the lookups in each it was 69 us.  The next pair's loads issued a pair ahead: 34.
 #include <algorithm>
 
 #include "codes.cuh"
@@ -191,8 +193,9 @@ extern "C" kvq_status kvq_keep_runs(const kvq_cache* caches, int32_t n_caches, c
       a.layer[i] = Planes{static_cast<uint8_t*>(c.k_data), static_cast<uint8_t*>(c.v_data), c.k_scale, c.v_scale};
     }
     a.layers = n;
-    // Blocks for as many pairs at a time as the SMs hold of them (kResident each): 32 requests of 36 layers and 8 heads have 38 blocks each.
-    const int want = std::max(1, device_sm_count() * kResident / batch);
+    // Three times the blocks that the SMs hold at once, so that requests of more pages, or of none that change, even out: 32 requests of 36 layers
+    // and 8 heads take 26.8 us, with as many blocks as are held 30.8, with six times 28.8 (in a graph; 33, 37 and 35 with the L2 flushed).
+    const int want = std::max(1, 3 * device_sm_count() * kResident / batch);
     const dim3 grid(std::min(a.H * n, want), batch);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (caches[0].k_fmt == KVQ_FMT_INT8_PAGE) keep_kernel<true><<<grid, kThreads, 0, s>>>(a);
