@@ -14,7 +14,7 @@
 //
 // Bound by the warps' work together: converting 16 K codes of K and V and handing them on is about 1,750 clocks a tile with nothing beside it, the
 // softmax's chain (maximum 600, weights 1,200, waits) about 2,300.  16 trees of 9..16 tokens over 11500, 8 and 32 heads, E4M3: 117 us, 3,270 GB/s; 64 trees
-// of 25..64 over 2000..8192, 4 and 28 heads, INT8: 250 us.  Some 27 us of a call are its start (10 us to the first weights) and its end (9 us from
+// of 25..64 over 2000..8192, 4 and 28 heads, INT8: 246 us.  Some 27 us of a call are its start (10 us to the first weights) and its end (9 us from
 // the last tile through the merge).  Slower, on the first of the two (117) and the second (250): two teams of softmax warps with an O each 122 and 269; half
 // tiles for two, three or four teams with one O, S and P V issued by two warps, 153, 143, 128 and 297, 292, 263; K and V converted by warps of their own 121
 // and 261; lookups by the converting warps themselves 150 and 335.

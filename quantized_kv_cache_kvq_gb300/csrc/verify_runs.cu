@@ -14,8 +14,8 @@
 // after every pass the warps send their sums to all blocks, whose mbarriers count the bytes, and all blocks take the same decision.  What decides is
 // read by the first block alone and handed to the others (the tree at the start, a child's numbers beside the sums), so that blocks take
 // the same number of exchanges whatever another stream does to the inputs.
-// Bound by the latency of the passes, which follow each other (about 1 us each for the sums' way): 32 trees over 131072 tokens, fp32, about three rows of
-// the path and five refusals each, 48 us (62 with the L2 flushed; 14 for the path's rows at the copy rate); 16 greedy ones over 32000, bf16, 15 us.  A
+// Bound by the latency of the passes, which follow each other, each with its loads, an exchange and a decision: 32 trees of 25..64 over 131072
+// tokens, fp32, 48 us (62 with the L2 flushed; 14 for the path's rows at the copy rate); 16 greedy ones over 32000, bf16, 17 us.  A
 // cluster barrier for each exchange took 54, sums by shifted significands and two loads in flight 87.
 #include <cooperative_groups.h>
 
