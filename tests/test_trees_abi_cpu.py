@@ -174,3 +174,18 @@ def test_strided_rows_are_taken_as_they_are(kvq, sent):  # noqa: F811
     probs = torch.zeros((6, 12))
     kvq.verify_runs(probs[:, 1:10], i32(6), i32(6), None, i32(6), i32(6), i32(6))
     assert sent[1][1][1] == 12 and sent[1][1][5] == 9
+
+
+def test_descriptors_of_all_layers_are_those_of_their_planes(kvq, sent):  # noqa: F811
+    layers = [kvq.PagedCache("e4m3p", "e4m3p", 2, 4, layer=i, device="cpu") for i in range(3)]
+    for _ in range(2):
+        kvq.keep_runs(layers, i32(2), i32(2, 2), i32(6), i32(2), run_starts=i32(3))
+        descs, n = sent[-1][1][:2]
+        assert n == 3 and descs == b"".join(bytes(c.desc()) for c in layers)
+        layers[1].v, layers[2].k_scale = torch.zeros_like(layers[1].v), torch.ones_like(layers[2].k_scale)
+        layers[0].k.data = torch.zeros_like(layers[0].k)
+
+
+def test_rotation_of_nothing_is_refused(kvq, sent):  # noqa: F811
+    with pytest.raises(AssertionError):
+        kvq.rope_runs(None, None, i32(2), torch.zeros(4, 128))
