@@ -463,6 +463,27 @@ def test_greedy_scores_of_every_kind(kvq):
         assert following.tolist() == (want if dt is torch.float32 else want) and err.item() == 6 and kept.tolist() == [1] * 7
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ns,V", [([129, 3, 128], 300), ([2, 64, 65, 33], 45), ([60, 4], 30011), ([5, 9], 120000), ([3] * 60, 70001)])
+def test_greedy_trees_of_many_sizes(kvq, dtype, ns, V):
+    verify_case(kvq, "greedy", dtype, ns, V, 5)
+    verify_case(kvq, "greedy", dtype, ns, V, 6, spread=1, stride=(1, 2))
+
+
+@pytest.mark.parametrize("n,V", [(6, 50), (6, 9000), (130, 50), (6, 400000)])
+def test_only_scores_on_the_path_are_reported(kvq, n, V):
+    """Row 0 leads to row 2; a NaN of row 1 or 3 is nobody's, one of row 2 is the path's and loses against every other score."""
+    tokens, parents = [9] + [4, 7] + [7] * (n - 3), [-1, 0, 0] + [1] * (n - 3)
+    for row, status in ((None, 0), (1, 0), (3, 0), (0, 6), (2, 6)):
+        scores = torch.zeros((n, V), device="cuda")
+        scores[0, 7], scores[2, V - 1] = 2.0, 1.0
+        if row is not None:
+            scores[row, V // 2 + 1] = scores[row, 0] = float("nan")
+        keep, kept, following, err = dev([7] * n), dev([7]), dev([7]), err_word()
+        kvq.verify_runs(scores, dev(tokens), dev(parents), None, keep, kept, following, run_starts=dev([0, n]), err=err)
+        assert err.item() == status and kept.tolist() == [2] and following.tolist() == [V - 1] and keep.tolist() == [0, 2] + [-1] * (n - 2)
+
+
 # ------------------------------------------------------------------------------------------------ the kept path
 def keep_case(kvq, fmt, before, new, paths, heads, layers, seed=0, single=False):
     rng = np.random.default_rng(seed)
