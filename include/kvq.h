@@ -585,7 +585,8 @@ kvq_status kvq_rope_runs(const void* q_dev, int64_t q_row_stride, int32_t num_q_
                          int64_t q_out_row_stride, void* k_out_dev, int64_t k_out_row_stride, const int32_t* run_starts_dev,
                          int32_t batch, int32_t num_rows, int32_t* err_word_dev, kvq_stream_t stream);
 
-/* Workspace bytes kvq_attn_tree needs on the current device; max_run is the call's. */
+/* Workspace bytes kvq_attn_tree needs on the current device; max_run is the call's.  So many also serve every call of no more requests, rows and
+ * max_run: a server sizes the workspace once, for its largest step. */
 size_t kvq_attn_tree_workspace_size(int32_t batch, int32_t num_rows, int32_t max_run, int32_t num_kv_heads, int32_t num_q_heads,
                                     int32_t q_dtype);
 

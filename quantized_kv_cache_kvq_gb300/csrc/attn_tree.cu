@@ -30,10 +30,19 @@ Workspace workspace(int batch, int num_rows, int max_run, int hkv, int hq, int q
   if (w.tile) {
     w.total = tree_tile_workspace(sms, &w.tw_acc, &w.tw_stats, &w.tw_rec);
   } else {
-    w.split = split_workspace((static_cast<size_t>(num_rows) * G) / (8 * w.nt) + batch, w.nt, hkv, sms);
+    // Row tiles: no run has more than max_run tokens, and all of them no more than num_rows.
+    const long long of_run = std::max(1ll, (max_rows + 8 * w.nt - 1) / (8 * w.nt));
+    const long long tiles = std::min(static_cast<long long>(num_rows) * G / (8 * w.nt) + batch, of_run * batch);
+    w.split = split_workspace(static_cast<size_t>(tiles), w.nt, hkv, sms);
     w.total = w.split.total;
   }
   return w;
+}
+// What a caller is told: enough for every call of no more requests, rows and max_run too.  The split kernel's part grows with each of them;
+// the tile kernel's is the same for all its calls, so beside it stands the largest that a call of few rows takes.
+size_t workspace_size(int batch, int num_rows, int max_run, int hkv, int hq, int q_dtype, int sms) {
+  const Workspace w = workspace(batch, num_rows, max_run, hkv, hq, q_dtype, sms);
+  return w.tile ? std::max(w.total, split_workspace(batch, row_blocks(kFewRows), hkv, sms).total) : w.total;
 }
 
 }  // namespace
@@ -50,7 +59,7 @@ extern "C" size_t kvq_attn_tree_workspace_size(int32_t batch, int32_t num_rows, 
     return 0;
   const int sms = device_sm_count();
   if (sms <= 0) return 0;
-  return workspace(batch, num_rows, std::min(max_run, num_rows), num_kv_heads, num_q_heads, q_dtype, sms).total;
+  return workspace_size(batch, num_rows, std::min(max_run, num_rows), num_kv_heads, num_q_heads, q_dtype, sms);
 }
 
 extern "C" kvq_status kvq_attn_tree(const kvq_cache* cache, const void* q, int64_t q_row_stride, int32_t q_dtype, int32_t num_q_heads,
