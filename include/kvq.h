@@ -547,7 +547,9 @@ kvq_status kvq_attn_runs(const kvq_cache* cache, const void* q_dev, int64_t q_ro
  *   kvq_map_runs -> kvq_tree_runs -> kvq_rope_runs -> kvq_append_runs -> kvq_attn_tree (each layer) -> kvq_verify_runs -> kvq_keep_runs
  * where tokens are cached in the order of the run's rows, whatever their positions, until kvq_keep_runs moves the accepted path to the
  * front.  A run has at most KVQ_MAX_TREE tokens; a longer one is reported as KVQ_ERR_DEVICE_BOUNDS and skipped.  Rows behind the last run
- * are left as they are.
+ * are left as they are.  A step that has prompts beside its trees puts the requests with trees first and gives kvq_tree_runs, kvq_attn_tree,
+ * kvq_verify_runs and kvq_keep_runs those (batch, run_starts, seq_lens, tables from the first on, num_rows the step's), and kvq_attn_runs the
+ * others (run_starts + T, seq_lens + T, the table from row T on): rows before a call's first run are left as they are too.
  */
 
 /*
