@@ -1,4 +1,4 @@
-// attn_runs.cuh -- arguments shared by the kernels of kvq_attn_runs.
+// attn_runs.cuh -- arguments shared by the kernels of kvq_attn_runs and kvq_attn_tree.
 //
 // For row r of a run (query token i = r / G of query head kvh G + r % G, at position p = len - n + i):
 //     x_t = sm_scale 2^{ek} (q . kc_t)   for t <= p,       out = sum_t e^{x_t} 2^{ev} vc_t / sum_t e^{x_t}
@@ -62,8 +62,8 @@ struct AttnArgs {
   int max_tiles;            // row tiles that the workspace has room for
   int w_max, nwa, stages;
   // tile kernel
-  float* tw_acc;    // [2 w][256][128]
-  float* tw_stats;  // [2 w][256][2]
+  float* tw_acc;    // [2 w][rows of a unit][128]: 256, of trees 128
+  float* tw_stats;  // [2 w][rows of a unit][2]
   int32_t* tw_rec;  // [w][8]
   int tile_ctas;            // CTAs
   int unit_cost;            // what a unit costs beside its tiles, in tiles

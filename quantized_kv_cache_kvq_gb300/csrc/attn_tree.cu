@@ -11,8 +11,12 @@ namespace kvq {
 namespace runs {
 namespace {
 
-// Calls whose longest run has more (token, head) rows are the tile kernel's.  16 trees over 11500 tokens, 8 and 32 heads, E4M3: the split kernel, one
-// pass over the context for every 16 rows, 84 us at 16 rows and 222 at up to 64; the tile kernel 113 at 20 rows, 119 at 64, 129 at 128.
+// Calls whose longest run has more (token, head) rows are the tile kernel's.  The split kernel makes one pass over the context for every 16 rows.  Both
+// kernels at 16, 20, 64 and 256 rows a request, 8 and 32 heads, E4M3, in a graph (us, split / tile):
+//     1 request of 300 tokens     20/17   21/15    20/17     21/21       1 of 12000     21/27    26/27    35/29     76/39
+//     4 of 12000                  40/41   50/42    80/48    263/80      16 of 2000      29/37    40/37    65/39    215/68
+//     16 of 12000                 86/113 143/114  271/123  1006/233     64 of 2000      76/92   120/94   224/100   822/193
+// Above 16 rows the tile kernel is the faster one in all of them but one (26/27); at 16 it is so where the context is short, by 3 us.
 constexpr int kFewRows = 16;
 
 struct Workspace {

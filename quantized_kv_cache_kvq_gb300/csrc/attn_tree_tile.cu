@@ -13,11 +13,11 @@
 //   * of the masks only those words are read that say something of the tile: tokens before the run are seen by all.
 //
 // Bound by the warps' work together: converting 16 K codes of K and V and handing them on is about 1,750 clocks a tile with nothing beside it, the
-// softmax's chain (maximum 600, weights 1,200, waits) about 2,300.  16 trees of 9..16 tokens over 11500, 8 and 32 heads, E4M3: 117 us, 3,270 GB/s; 64 trees
-// of 25..64 over 2000..8192, 4 and 28 heads, INT8: 246 us.  Some 27 us of a call are its start (10 us to the first weights) and its end (9 us from
-// the last tile through the merge).  Slower, on the first of the two (117) and the second (250): two teams of softmax warps with an O each 122 and 269; half
-// tiles for two, three or four teams with one O, S and P V issued by two warps, 153, 143, 128 and 297, 292, 263; K and V converted by warps of their own 121
-// and 261; lookups by the converting warps themselves 150 and 335.
+// softmax's chain (maximum 600, weights 1,200, waits) about 2,300.  16 trees of 9..16 tokens over 11500, 8 and 32 heads, E4M3: 114 us, 3,340 GB/s; 64 trees
+// of 25..64 over 2000..8192, 4 and 28 heads, INT8: 246 us.  A call's start (10 us to the first weights) and end (9 us from the last tile through the
+// merge) are what a single request over 300 tokens takes, 15 to 17 us.  Slower, where this form took 117 for the first of the two and 250 for the second: two teams of
+// softmax warps with an O each 122 and 269; half tiles for two, three or four teams with one O, S and P V issued by two warps, 153, 143, 128 and
+// 297, 292, 263; K and V converted by warps of their own 121 and 261; lookups by the converting warps themselves 150 and 335.
 //
 // TMEM columns: S (and P, over the first half of each 32 columns) twice 128, O 128, Q 64.
 // Warps: 0-15 softmax (rows 32 (w & 3) .., keys 32 (w >> 2) .. of a tile), 16-23 convert, 24 issues the products, 25 looks ahead.
@@ -33,7 +33,7 @@ constexpr int kSlots = 6;       // ring of operand tiles
 constexpr int kOperand = 32768;  // 128 x 128 fp16
 constexpr int kSoftmaxWarps = 16, kConvertWarp = 16, kMmaWarp = 24, kScoutWarp = 25;  // first warps of the roles
 constexpr int kThreads = 28 * 32;
-// Registers: 72 a thread at launch; the softmax warps take what the last warpgroup, of which only one warp works, gives back.  None of the loops
+// Registers: 72 a thread at launch; the softmax warps take what the last warpgroup, of which only two warps work, gives back.  None of the loops
 // may spill (with 72 the softmax does).
 constexpr int kRegsSoftmax = 80, kRegsConvert = 72, kRegsMma = 40;
 static_assert(16 * kRegsSoftmax + 8 * kRegsConvert + 4 * kRegsMma <= 28 * 72, "no more than the block was launched with");
@@ -582,8 +582,8 @@ cudaError_t launch_tree_tile(AttnArgs& a, bool int8, int sms, cudaStream_t s) {
   cudaError_t e = limit[int8].raise(kern, kSmemBytes);
   if (e != cudaSuccess) return e;
   a.tile_ctas = sms;
-  // A unit's own cost in tiles.  16 trees of 64 rows over 11500 tokens, 64 trees of up to 448 over up to 8192: 120 and 272 us with 0, 123 and 263
-  // with 1, 121 and 258 with 2, 119 and 250 with 3 and with 6.
+  // A unit's own cost in tiles.  16 trees of up to 64 rows over 11000..11996 tokens and 64 trees of up to 448 over up to 8192, in a graph: 117 and 272 us
+  // with 0, 117 and 262 with 1, 117 and 257 with 2, 116 and 248 with 3, 115 and 247 with 4, 115 and 249 with 6, 121 and 253 with 8.
   a.unit_cost = 4;
   kern<<<sms, kThreads, kSmemBytes, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

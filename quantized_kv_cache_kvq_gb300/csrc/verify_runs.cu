@@ -15,9 +15,10 @@
 // read by the first block alone and handed to the others (the tree at the start, a child's numbers beside the sums), so that blocks take
 // the same number of exchanges whatever another stream does to the inputs.
 // Bound by the latency of the passes, which follow each other, each with its loads, an exchange and a decision: 32 trees of 25..64 over 131072
-// tokens, fp32, 48 us (62 with the L2 flushed; 14 for the path's rows at the copy rate); 16 greedy ones over 32000, bf16, 17 us.  A
-// cluster barrier for each exchange took 54, sums by shifted significands and two loads in flight 87.  Greedy trees read whole, all rows before one
-// exchange: 26 us for 16 trees of 12 over 32000, bf16, that take 16.5 row by row.
+// tokens, fp32, 48 us in a graph (62 with the L2 flushed; 14 for the paths' rows at the copy rate), the slowest tree's time, so 49 to 60 with other
+// draws; 16 greedy ones of 9..16 rows over 32000, bf16, 14 to 19 us.  A cluster barrier for each exchange took 54, sums by shifted significands and
+// two loads in flight 87.  Greedy trees read whole, all rows before one exchange: 26 us for 16 trees of 12 rows over 32000, bf16, that take 16.5
+// row by row.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -33,7 +34,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kCluster = 8;
-// Warps of a block.  64 registers a thread: two blocks on an SM, so that 38 requests run at once.
+// Warps of a block.  64 registers a thread: two blocks on an SM, so that 38 requests run at once.  Some spill for it (88 bytes with fp32, 164 with BF16);
+// with 102 registers and none, one block on an SM, 32 trees take 64 us where they take 48, 64 greedy ones 39 for 29, and up to 16 trees the same
+// to 1 or 2 us either way.
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kPieces = kCluster * kWarps;
 constexpr int kMaxVocab = 1 << 19;  // sums of 2^19 times 2^44 fit 64 bits
