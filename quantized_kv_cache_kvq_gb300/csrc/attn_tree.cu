@@ -16,7 +16,7 @@ namespace {
 //     1 request of 300 tokens     20/17   21/15    20/17     21/21       1 of 12000     21/27    26/27    35/29     76/39
 //     4 of 12000                  40/41   50/42    80/48    263/80      16 of 2000      29/37    40/37    65/39    215/68
 //     16 of 12000                 86/113 143/114  271/123  1006/233     64 of 2000      76/92   120/94   224/100   822/193
-// Above 16 rows the tile kernel is the faster one in all of them but one (26/27); at 16 it is so where the context is short, by 3 us.
+// Above 16 rows the tile kernel is no slower in any but one of them (26/27); at 16 it is the faster one where the context is short, by up to 3 us.
 constexpr int kFewRows = 16;
 
 struct Workspace {

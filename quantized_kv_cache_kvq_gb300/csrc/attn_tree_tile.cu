@@ -15,9 +15,10 @@
 // Bound by the warps' work together: converting 16 K codes of K and V and handing them on is about 1,750 clocks a tile with nothing beside it, the
 // softmax's chain (maximum 600, weights 1,200, waits) about 2,300.  16 trees of 9..16 tokens over 11500, 8 and 32 heads, E4M3: 114 us, 3,340 GB/s; 64 trees
 // of 25..64 over 2000..8192, 4 and 28 heads, INT8: 246 us.  A call's start (10 us to the first weights) and end (9 us from the last tile through the
-// merge) are what a single request over 300 tokens takes, 15 to 17 us.  Slower, where this form took 117 for the first of the two and 250 for the second: two teams of
-// softmax warps with an O each 122 and 269; half tiles for two, three or four teams with one O, S and P V issued by two warps, 153, 143, 128 and
-// 297, 292, 263; K and V converted by warps of their own 121 and 261; lookups by the converting warps themselves 150 and 335.
+// merge) are about what a single request over 300 tokens takes, 15 to 17 us.  Slower, where this form took 117 for the first of the two and 250
+// for the second: two teams of softmax warps with an O each 122 and 269; half tiles for two, three or four teams with one O, S and P V issued by
+// two warps, 153, 143, 128 and 297, 292, 263; K and V converted by warps of their own 121 and 261; lookups by the converting warps themselves
+// 150 and 335.
 //
 // TMEM columns: S (and P, over the first half of each 32 columns) twice 128, O 128, Q 64.
 // Warps: 0-15 softmax (rows 32 (w & 3) .., keys 32 (w >> 2) .. of a tile), 16-23 convert, 24 issues the products, 25 looks ahead.

@@ -6,12 +6,12 @@
 //
 // One launch for all layers.  A block has one request and a few (layer, kv head) pairs: where every slot's token comes from is looked up once for
 // all of them.  A key token is eight 16-byte words of its tile, so a thread moves one word of the new tile; a value word holds four tokens of four
-// channels, so a thread puts one together from the words of its four tokens.  Words that stay as they are are read, since a scale that grows would change
-// them, but not written.
+// channels, so a thread puts one together from the words of its four tokens.  Words that stay as they are are read, since a scale that grows
+// would change them, but not written.
 // A value tile's tokens lie in all of its lines, so moving one token reads and writes 2 KB: 32 requests that keep a path of trees of 25..64 in 36
 // layers of 8 heads read 44 MB where the tokens, read and written, are 19 (26.8 us; 2.8 for the tokens at the copy rate), a layer of 4 requests
-// takes 8 us.  With one block for each (request, layer, head) and the lookups in each it was 69 us.  The next pair's loads issued a pair ahead: 34.  Keys and values by blocks of their
-// own: 33.  Ten blocks on an SM with 48 registers: no change.
+// takes 8 us.  With one block for each (request, layer, head) and the lookups in each it was 69 us.  The next pair's loads issued a pair
+// ahead: 34.  Keys and values by blocks of their own: 33.  Ten blocks on an SM with 48 registers: no change.
 #include <algorithm>
 
 #include "codes.cuh"

@@ -34,9 +34,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kCluster = 8;
-// Warps of a block.  64 registers a thread: two blocks on an SM, so that 38 requests run at once.  Some spill for it (88 bytes with fp32, 164 with BF16);
-// with 102 registers and none, one block on an SM, 32 trees take 64 us where they take 48, 64 greedy ones 39 for 29, and up to 16 trees the same
-// to 1 or 2 us either way.
+// Warps of a block.  64 registers a thread: two blocks on an SM, so that 38 requests run at once.  That costs spills (88 bytes with fp32, 164 with
+// BF16).  With 102 registers, no spills and one block on an SM the 32 trees above take 64 us, not 48, 64 greedy ones 39, not 29; up to 16 trees take
+// the same to 1 or 2 us either way.
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kPieces = kCluster * kWarps;
 constexpr int kMaxVocab = 1 << 19;  // sums of 2^19 times 2^44 fit 64 bits
